@@ -62,9 +62,12 @@ typedef enum {
   TQ_PRESET_4BIT_NC = 1,  /* K: 4-bit Lloyd-Max + norm correction; V: 4-bit */
   TQ_PRESET_K3V4_NC = 2,  /* K: 3-bit Lloyd-Max + norm correction; V: 4-bit */
   TQ_PRESET_3BIT_NC = 3,  /* K: 3-bit + norm correction; V: 3-bit           */
-  TQ_PRESET_PROD3 = 4     /* keys only: 2-bit Lloyd-Max code + 1-bit QJL residual
+  TQ_PRESET_PROD3 = 4,    /* keys only: 2-bit Lloyd-Max code + 1-bit QJL residual
                              sign per coordinate (TurboQuant_prod; the tq_prod_*
                              entry points below, its own key cache)          */
+  TQ_PRESET_E4M3_BLK = 5, /* K and V: e4m3 with one fp32 scale per (block, KV head)
+                             (the tq_b8_* entry points below, their own cache) */
+  TQ_PRESET_INT8_BLK = 6  /* K and V: int8 (-127 .. 127), scales as above      */
 } tq_preset;
 
 typedef enum { TQ_DTYPE_F16 = 0, TQ_DTYPE_BF16 = 1, TQ_DTYPE_F32 = 2 } tq_dtype;
@@ -75,6 +78,7 @@ typedef enum { TQ_DTYPE_F16 = 0, TQ_DTYPE_BF16 = 1, TQ_DTYPE_F32 = 2 } tq_dtype;
 #define TQ_DEV_SEQ_TOO_LONG       4u  /* decode: seq_len > max_seq_len or > row cap */
 #define TQ_DEV_TIMEOUT            8u  /* decode: a bounded wait on a copy expired, or the
                                          launch's shared-memory plan did not fit */
+#define TQ_DEV_NOT_FINITE        16u  /* tq_b8_store: an infinity or a NaN among the inputs */
 
 /* Problem description shared by store and decode. */
 typedef struct {
@@ -456,6 +460,132 @@ tq_status tq_prod_scores(const tq_config* cfg, const tq_codebook* cb, const floa
                          const int* block_table, int bt_stride, const int* seq_lens, int batch,
                          int max_seq_len, float scale, float* scores,
                          void* workspace, size_t workspace_bytes,
+                         unsigned int* dev_status, tq_stream_t stream);
+
+/* ---- 8-bit cache with a scale per block and head --------------------------
+ * Keys and values in 8 bits, unrotated: a code times the fp32 scale of its
+ * (cache block, KV head), one scale for the keys and one for the values.
+ *   TQ_PRESET_E4M3_BLK  code = e4m3, largest Q = 448
+ *   TQ_PRESET_INT8_BLK  code = int8, largest Q = 127
+ * The tq_b8_* entry points use cfg->head_dim (128), block_size (16, 32, 64 or
+ * 128), num_kv_heads, num_q_heads (attention: n_q % n_kv == 0 and
+ * n_q / n_kv <= 8) and flags; partition_tokens must be 0.
+ *
+ * Cache: cache[num_blocks] of block_bytes each,
+ *   tiles   [n_kv][block_size / 16][tile_bytes]: a tile holds 16 positions of
+ *           one KV head, 16 key rows of 128 codes at k_off, then 16 value rows
+ *           at v_off; the 16-byte group c (coordinates 16 c .. 16 c + 15) of
+ *           row r is at r * 128 + 16 * (c ^ (r & 7)), so that the readers'
+ *           shared-memory accesses meet no bank twice
+ *   scales  [n_kv][2] fp32 at scale_off: key scale, value scale
+ *   and padding to a multiple of 128 bytes.
+ * Position p of sequence b is in block block_table[b][p / block_size], row
+ * p % block_size. */
+typedef struct {
+  int code_limit;          /* Q: 448 or 127 */
+  int is_int8;
+  int tile_tokens;         /* 16 */
+  int tile_bytes;          /* 4096 */
+  int k_off, v_off;        /* 0, 2048 */
+  int scale_off;
+  long long block_bytes;
+} tq_b8_layout;
+
+/* Host. The layout of cfg's 8-bit cache (num_q_heads is not used). */
+tq_status tq_b8_layout_for(const tq_config* cfg, tq_b8_layout* out);
+
+/* Device. Quantise and write chunks of new tokens. Rows query_start[b] ..
+ * query_start[b + 1] - 1 of key and value are the last positions of sequence
+ * b: row query_start[b] + i is position seq_lens[b] - q_len + i. Per touched
+ * (block, KV head), for keys and for values:
+ *   s' = max(A / Q, 2^-100), A the largest finite |x| of the block's new rows
+ *   s  = max(s', the block's scale) if the block already holds earlier
+ *        positions of the sequence, else s' (what a reused block held before
+ *        does not count)
+ *   new codes  round(x * (1 / s)) to nearest, ties to even, saturated at +-Q
+ *   codes of the earlier positions, if s grew: round(code * (old s / s))
+ * every operation in IEEE fp32, so the bytes are defined exactly. An infinity
+ * is stored as +-Q and a NaN as 0, with TQ_DEV_NOT_FINITE. Rows of a block
+ * past the sequence's end keep their bytes.
+ *   key, value    device [total_q][n_kv][d] of in_dtype (f16 or bf16), 16-byte
+ *                 aligned; consecutive rows are key_stride / value_stride
+ *                 elements apart (0: n_kv * d; else >= n_kv * d and a multiple
+ *                 of 8), so a slice of a fused projection's output can be given
+ *   query_start   device int32 [batch + 1], non-decreasing from 0; rows from
+ *                 query_start[batch] to total_q are not used
+ *   max_q_len     host; rows of a chunk past max_q_len are not stored
+ *                 (TQ_DEV_SEQ_TOO_LONG)
+ *   block_table, bt_stride, seq_lens
+ *                 as for tq_continue: lengths WITH the chunk. Positions past
+ *                 bt_stride * block_size and rows before position 0 are not
+ *                 stored (TQ_DEV_SEQ_TOO_LONG), nor are those of a block id
+ *                 outside [0, num_blocks) (TQ_DEV_BLOCK_OUT_OF_RANGE)
+ * A block that is written belongs to one sequence of the batch alone (blocks
+ * shared as a common prefix may be read by all, not written); two sequences
+ * writing one block race. batch, total_q or max_q_len == 0 is a no-op. One
+ * launch, no workspace; results do not depend on the order of execution. */
+tq_status tq_b8_store(const tq_config* cfg, const void* key, long long key_stride,
+                      const void* value, long long value_stride, int in_dtype,
+                      const int* query_start, int batch, int total_q, int max_q_len,
+                      void* cache, long long num_blocks,
+                      const int* block_table, int bt_stride, const int* seq_lens,
+                      unsigned int* dev_status, tq_stream_t stream);
+
+/* Device. The cached keys and values expanded to key_out, value_out
+ * [batch][max_seq_len][n_kv][d] of out_dtype (f16, bf16 or f32): code * scale
+ * in fp32, rounded once. Arguments, zeros behind the sequences and device
+ * errors as for tq_dequant. One launch. */
+tq_status tq_b8_dequant(const tq_config* cfg, const void* cache, long long num_blocks,
+                        const int* block_table, int bt_stride,
+                        const int* seq_lens, int batch, int max_seq_len,
+                        void* key_out, void* value_out, int out_dtype,
+                        unsigned int* dev_status, tq_stream_t stream);
+
+/* Host. Bytes of workspace of tq_b8_decode: at most batch * n_kv + 4096 partial
+ * records of (d + 1) fp32 per query head of a KV head. 0 on bad input. */
+size_t tq_b8_decode_workspace_size(const tq_config* cfg, int batch, int max_seq_len);
+
+/* Device. Attention of one query per sequence over its seq_lens[b] cached
+ * positions, as tq_decode (scale <= 0: 1 / sqrt(d); an empty sequence gives
+ * zeros; positions of a bad block id are left out).
+ *   q          device [batch][n_q][d] of q_dtype (f16 or bf16), 16-byte
+ *              aligned, rows q_stride elements apart (0: n_q * d; else
+ *              >= n_q * d and a multiple of 8)
+ *   out        device [batch][n_q][d] of out_dtype, contiguous, 16-byte aligned
+ *   workspace  device, >= tq_b8_decode_workspace_size bytes, 16-byte aligned,
+ *              any contents; calls that may overlap need one each
+ * TQ_FLAG_INDICES_READY as for tq_decode. */
+tq_status tq_b8_decode(const tq_config* cfg, const void* q, long long q_stride, int q_dtype,
+                       const void* cache, long long num_blocks,
+                       const int* block_table, int bt_stride,
+                       const int* seq_lens, int batch, int max_seq_len, float scale,
+                       void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                       unsigned int* dev_status, tq_stream_t stream);
+
+/* Host. Bytes of workspace of tq_b8_continue for the same sizes. 0 on bad
+ * input. */
+size_t tq_b8_continue_workspace_size(const tq_config* cfg, int batch, int total_q, int max_q_len,
+                                     int max_seq_len);
+
+/* Device. Causal attention of chunks of queries whose keys and values are
+ * already stored, as tq_continue: query i of a chunk of q_len sits at position
+ * seq_lens[b] - q_len + i and sees positions 0 .. that one.
+ *   q, q_stride, q_dtype, out, out_dtype
+ *              as for tq_b8_decode, [total_q][n_q][d]; rows from
+ *              query_start[batch] to total_q are neither read nor written; a
+ *              query that sees no position, and one past max_q_len
+ *              (TQ_DEV_SEQ_TOO_LONG), gives zeros
+ *   max_seq_len  host; >= every seq_lens[b]: longer sequences are cut there, or at
+ *              bt_stride * block_size (TQ_DEV_SEQ_TOO_LONG)
+ *   workspace  device, >= tq_b8_continue_workspace_size bytes, 16-byte aligned,
+ *              any contents; calls that may overlap need one each
+ * batch, total_q or max_q_len == 0 is a no-op. */
+tq_status tq_b8_continue(const tq_config* cfg, const void* q, long long q_stride, int q_dtype,
+                         const int* query_start, int batch, int total_q, int max_q_len,
+                         const void* cache, long long num_blocks,
+                         const int* block_table, int bt_stride,
+                         const int* seq_lens, int max_seq_len, float scale,
+                         void* out, int out_dtype, void* workspace, size_t workspace_bytes,
                          unsigned int* dev_status, tq_stream_t stream);
 
 /* Host. Static description of a status code. */

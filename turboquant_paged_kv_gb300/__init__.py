@@ -15,9 +15,9 @@ import torch
 
 from . import _abi
 from ._abi import (PRESET_IDS, TQ_DEV_BLOCK_OUT_OF_RANGE, TQ_DEV_SEQ_TOO_LONG,  # noqa: F401
-                   TQ_DECODE_NOALLOC_SCRATCH_BYTES, TQ_DEV_SLOT_OUT_OF_RANGE, TQ_DEV_TIMEOUT,
+                   TQ_DECODE_NOALLOC_SCRATCH_BYTES, TQ_DEV_SLOT_OUT_OF_RANGE, TQ_DEV_TIMEOUT, TQ_DEV_NOT_FINITE,
                    TQ_DTYPE_BF16, TQ_DTYPE_F16, TQ_DTYPE_F32, TQ_ERR_WORKSPACE_TOO_SMALL,
-                   TQError, tq_codebook, tq_config, tq_layout, tq_prod_layout)
+                   TQError, tq_b8_layout, tq_codebook, tq_config, tq_layout, tq_prod_layout)
 
 
 
@@ -36,6 +36,8 @@ __all__ = ["make_config", "tq_build_codebook", "tq_layout_for", "tq_store", "tq_
            "tq_decode_partials", "tq_decode_reduce", "tq_decode_noalloc", "tq_decode_workspace_size",
            "tq_dequant", "tq_prod_layout_for", "tq_prod_store", "tq_prod_scores_workspace_size",
            "tq_prod_scores", "tq_continue_workspace_size", "tq_continue",
+           "tq_b8_layout_for", "tq_b8_store", "tq_b8_dequant", "tq_b8_decode_workspace_size", "tq_b8_decode",
+           "tq_b8_continue_workspace_size", "tq_b8_continue",
            "tq_status_string",
            "tq_version", "TQError", "lib_path"]
 
@@ -250,3 +252,152 @@ def tq_continue(cfg: tq_config, cb, q: torch.Tensor, query_start: torch.Tensor, 
         max_q_len, _ptr(cache), num_blocks, _ptr(block_table), block_table.shape[1], _ptr(seq_lens), max_seq_len,
         float(scale), _ptr(out), _DTYPES[out.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(),
         _ptr(dev_status), _stream(stream)))
+
+
+# ---- 8-bit cache with a scale per block and head (e4m3_blk, int8_blk) ----------
+
+def tq_b8_layout_for(cfg: tq_config) -> tq_b8_layout:
+    lay = tq_b8_layout()
+    _abi.check("tq_b8_layout_for", _LIB.tq_b8_layout_for(ctypes.byref(cfg), ctypes.byref(lay)))
+    return lay
+
+
+def _b8_rows(name: str, t: torch.Tensor, heads: int, d: int) -> int:
+    """Checks a [rows, heads, d] tensor whose rows may be a stride apart (a slice
+    of a fused projection's output); returns that stride in elements."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError(f"{name} must be [rows, {heads}, {d}] float16 or bfloat16, got {tuple(t.shape)} {t.dtype}")
+    s0, s1, s2 = t.stride()
+    if t.shape[0] == 0:
+        return heads * d
+    if s2 != 1 or (s1 != d and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {(s0, s1, s2)}")
+    return s0 if t.shape[0] > 1 else heads * d
+
+
+def _b8_common(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, others, stream) -> None:
+    """What every call on the cache has in common: index tensors, and one device,
+    the current one (the library launches there)."""
+    if cache.dtype != torch.uint8 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 tensor")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 [batch, blocks] with contiguous rows")
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens must be a contiguous int32 vector")
+    if block_table.shape[0] < seq_lens.shape[0]:
+        raise ValueError("block_table has fewer rows than seq_lens has entries")
+    if not cache.is_cuda:
+        raise ValueError("the tensors must be on a CUDA device")
+    dev = cache.get_device()
+    for t in (block_table, seq_lens, *others):
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the tensors must be on one CUDA device")
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    if stream is not None and stream.device_index != dev:
+        raise ValueError("the stream must be one of the tensors' device")
+
+
+def _b8_table(block_table: torch.Tensor) -> int:
+    """The distance of the table's rows, which may be longer than what the view shows."""
+    if block_table.shape[0] > 1 and block_table.stride(0) != block_table.shape[1]:
+        raise ValueError("block_table must be contiguous")
+    return block_table.shape[1]
+
+
+def _b8_starts(query_start: torch.Tensor, seq_lens: torch.Tensor) -> None:
+    if query_start.dtype != torch.int32 or not query_start.is_contiguous() or query_start.numel() != seq_lens.shape[0] + 1:
+        raise ValueError("query_start must be a contiguous int32 vector of batch + 1 entries")
+
+
+def _b8_out(name: str, t: torch.Tensor, shape) -> None:
+    if t.dtype not in _DTYPES or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float16, bfloat16 or float32 tensor of shape {tuple(shape)}")
+
+
+def _b8_blocks(cfg: tq_config, cache: torch.Tensor, num_blocks: int | None) -> int:
+    have = cache.numel() // tq_b8_layout_for(cfg).block_bytes
+    if num_blocks is None:
+        return have
+    if num_blocks > have:
+        raise ValueError(f"cache holds {have} blocks, not {num_blocks}")
+    return num_blocks
+
+
+def tq_b8_store(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query_start: torch.Tensor, max_q_len: int,
+                cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, num_blocks: int | None = None,
+                dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise chunks of new tokens into the cache: key, value [total_q, n_kv, d]
+    f16/bf16 (rows may be a stride apart); rows query_start[b] ..
+    query_start[b + 1] - 1 become the last positions of sequence b; seq_lens
+    [batch] int32 are the lengths with the chunk."""
+    ks = _b8_rows("key", key, cfg.num_kv_heads, cfg.head_dim)
+    vs = _b8_rows("value", value, cfg.num_kv_heads, cfg.head_dim)
+    if key.dtype != value.dtype or key.shape[0] != value.shape[0]:
+        raise ValueError("key and value must have one dtype and one number of rows")
+    _b8_starts(query_start, seq_lens)
+    _b8_common(cache, block_table, seq_lens, (key, value, query_start, dev_status), stream)
+    _abi.check("tq_b8_store", _LIB.tq_b8_store(
+        ctypes.byref(cfg), _ptr(key), ks, _ptr(value), vs, _DTYPES[key.dtype], _ptr(query_start), seq_lens.shape[0],
+        key.shape[0], max_q_len, _ptr(cache), _b8_blocks(cfg, cache, num_blocks), _ptr(block_table),
+        _b8_table(block_table), _ptr(seq_lens), _ptr(dev_status), _stream(stream)))
+
+
+def tq_b8_dequant(cfg: tq_config, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                  max_seq_len: int, key_out: torch.Tensor, value_out: torch.Tensor, num_blocks: int | None = None,
+                  dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """key_out, value_out [B, max_seq_len, n_kv, d] (f16, bf16 or f32), written in full."""
+    shape = (seq_lens.shape[0], max_seq_len, cfg.num_kv_heads, cfg.head_dim)
+    _b8_out("key_out", key_out, shape)
+    _b8_out("value_out", value_out, shape)
+    if value_out.dtype != key_out.dtype:
+        raise ValueError("key_out and value_out must have the same dtype")
+    _b8_common(cache, block_table, seq_lens, (key_out, value_out, dev_status), stream)
+    _abi.check("tq_b8_dequant", _LIB.tq_b8_dequant(
+        ctypes.byref(cfg), _ptr(cache), _b8_blocks(cfg, cache, num_blocks), _ptr(block_table), _b8_table(block_table),
+        _ptr(seq_lens), seq_lens.shape[0], max_seq_len, _ptr(key_out), _ptr(value_out), _DTYPES[key_out.dtype],
+        _ptr(dev_status), _stream(stream)))
+
+
+def tq_b8_decode_workspace_size(cfg: tq_config, batch: int, max_seq_len: int) -> int:
+    return int(_LIB.tq_b8_decode_workspace_size(ctypes.byref(cfg), batch, max_seq_len))
+
+
+def tq_b8_decode(cfg: tq_config, q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                 seq_lens: torch.Tensor, max_seq_len: int, out: torch.Tensor, workspace: torch.Tensor,
+                 scale: float = 0.0, num_blocks: int | None = None, dev_status: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """q [B, n_q, d] f16/bf16 (rows may be a stride apart); out [B, n_q, d]; seq_lens [B] int32."""
+    qs = _b8_rows("q", q, cfg.num_q_heads, cfg.head_dim)
+    _b8_out("out", out, q.shape)
+    if q.shape[0] != seq_lens.shape[0]:
+        raise ValueError("q must have one row per sequence")
+    _b8_common(cache, block_table, seq_lens, (q, out, workspace, dev_status), stream)
+    _abi.check("tq_b8_decode", _LIB.tq_b8_decode(
+        ctypes.byref(cfg), _ptr(q), qs, _DTYPES[q.dtype], _ptr(cache), _b8_blocks(cfg, cache, num_blocks),
+        _ptr(block_table), _b8_table(block_table), _ptr(seq_lens), q.shape[0], max_seq_len, float(scale), _ptr(out),
+        _DTYPES[out.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
+        _stream(stream)))
+
+
+def tq_b8_continue_workspace_size(cfg: tq_config, batch: int, total_q: int, max_q_len: int, max_seq_len: int) -> int:
+    return int(_LIB.tq_b8_continue_workspace_size(ctypes.byref(cfg), batch, total_q, max_q_len, max_seq_len))
+
+
+def tq_b8_continue(cfg: tq_config, q: torch.Tensor, query_start: torch.Tensor, max_q_len: int, cache: torch.Tensor,
+                   block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, out: torch.Tensor,
+                   workspace: torch.Tensor, scale: float = 0.0, num_blocks: int | None = None,
+                   dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of chunks whose keys and values are stored: q [total_q,
+    n_q, d] f16/bf16 (rows may be a stride apart), query_start int32 [batch + 1],
+    seq_lens int32 [batch] (lengths with the chunk), out [total_q, n_q, d]; rows
+    of out from query_start[batch] on are left as they are."""
+    qs = _b8_rows("q", q, cfg.num_q_heads, cfg.head_dim)
+    _b8_out("out", out, q.shape)
+    _b8_starts(query_start, seq_lens)
+    _b8_common(cache, block_table, seq_lens, (q, query_start, out, workspace, dev_status), stream)
+    _abi.check("tq_b8_continue", _LIB.tq_b8_continue(
+        ctypes.byref(cfg), _ptr(q), qs, _DTYPES[q.dtype], _ptr(query_start), seq_lens.shape[0], q.shape[0], max_q_len,
+        _ptr(cache), _b8_blocks(cfg, cache, num_blocks), _ptr(block_table), _b8_table(block_table), _ptr(seq_lens),
+        max_seq_len, float(scale), _ptr(out), _DTYPES[out.dtype], _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))

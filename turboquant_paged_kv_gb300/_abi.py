@@ -23,8 +23,11 @@ TQ_PRESET_4BIT_NC = 1
 TQ_PRESET_K3V4_NC = 2
 TQ_PRESET_3BIT_NC = 3
 TQ_PRESET_PROD3 = 4
+TQ_PRESET_E4M3_BLK = 5
+TQ_PRESET_INT8_BLK = 6
 PRESET_IDS = {"k8v4": TQ_PRESET_K8V4, "4bit_nc": TQ_PRESET_4BIT_NC,
-              "k3v4_nc": TQ_PRESET_K3V4_NC, "3bit_nc": TQ_PRESET_3BIT_NC, "prod3": TQ_PRESET_PROD3}
+              "k3v4_nc": TQ_PRESET_K3V4_NC, "3bit_nc": TQ_PRESET_3BIT_NC, "prod3": TQ_PRESET_PROD3,
+              "e4m3_blk": TQ_PRESET_E4M3_BLK, "int8_blk": TQ_PRESET_INT8_BLK}
 
 TQ_DTYPE_F16 = 0
 TQ_DTYPE_BF16 = 1
@@ -34,12 +37,15 @@ TQ_DEV_SLOT_OUT_OF_RANGE = 1
 TQ_DEV_BLOCK_OUT_OF_RANGE = 2
 TQ_DEV_SEQ_TOO_LONG = 4
 TQ_DEV_TIMEOUT = 8
+TQ_DEV_NOT_FINITE = 16
 
 # every function tq.h declares (checked by the ABI tests)
 EXPORTED = ("tq_build_codebook", "tq_layout_for", "tq_store", "tq_decode_workspace_size",
             "tq_decode", "tq_decode_append", "tq_decode_partials", "tq_decode_reduce", "tq_decode_noalloc",
             "tq_dequant", "tq_prod_layout_for", "tq_prod_store", "tq_prod_scores_workspace_size",
-            "tq_prod_scores", "tq_continue_workspace_size", "tq_continue", "tq_status_string", "tq_version")
+            "tq_prod_scores", "tq_continue_workspace_size", "tq_continue", "tq_b8_layout_for", "tq_b8_store",
+            "tq_b8_dequant", "tq_b8_decode_workspace_size", "tq_b8_decode", "tq_b8_continue_workspace_size",
+            "tq_b8_continue", "tq_status_string", "tq_version")
 
 TQ_DECODE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -66,6 +72,12 @@ class tq_prod_layout(ctypes.Structure):
                 ("k_off", ctypes.c_int), ("k_row_bytes", ctypes.c_int),
                 ("sign_off", ctypes.c_int), ("sign_row_bytes", ctypes.c_int),
                 ("norm_off", ctypes.c_int), ("rnorm_off", ctypes.c_int), ("block_bytes", ctypes.c_longlong)]
+
+
+class tq_b8_layout(ctypes.Structure):
+    _fields_ = [("code_limit", ctypes.c_int), ("is_int8", ctypes.c_int), ("tile_tokens", ctypes.c_int),
+                ("tile_bytes", ctypes.c_int), ("k_off", ctypes.c_int), ("v_off", ctypes.c_int),
+                ("scale_off", ctypes.c_int), ("block_bytes", ctypes.c_longlong)]
 
 
 class tq_codebook(ctypes.Structure):
@@ -105,6 +117,16 @@ _SIGS = {
     "tq_continue_workspace_size": (_sz, [ctypes.POINTER(tq_config), _i, _i]),
     "tq_continue": (_i, [ctypes.POINTER(tq_config), ctypes.POINTER(tq_codebook), _vp, _i, _vp, _i, _i, _i, _vp, _ll,
                          _vp, _i, _vp, _i, _f, _vp, _i, _vp, _sz, _vp, _vp]),
+    "tq_b8_layout_for": (_i, [ctypes.POINTER(tq_config), ctypes.POINTER(tq_b8_layout)]),
+    "tq_b8_store": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _vp, _ll, _i, _vp, _i, _i, _i, _vp, _ll, _vp, _i, _vp,
+                         _vp, _vp]),
+    "tq_b8_dequant": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _vp, _i, _vp, _i, _i, _vp, _vp, _i, _vp, _vp]),
+    "tq_b8_decode_workspace_size": (_sz, [ctypes.POINTER(tq_config), _i, _i]),
+    "tq_b8_decode": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _i, _vp, _ll, _vp, _i, _vp, _i, _i, _f, _vp, _i, _vp,
+                          _sz, _vp, _vp]),
+    "tq_b8_continue_workspace_size": (_sz, [ctypes.POINTER(tq_config), _i, _i, _i, _i]),
+    "tq_b8_continue": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _i, _vp, _i, _i, _i, _vp, _ll, _vp, _i, _vp, _i, _f,
+                            _vp, _i, _vp, _sz, _vp, _vp]),
     "tq_status_string": (ctypes.c_char_p, [_i]),
     "tq_version": (_i, []),
 }

@@ -18,6 +18,8 @@ bool preset_info(int preset, PresetInfo* out) {
     case TQ_PRESET_K3V4_NC: *out = {3, 4, false, true}; return true;
     case TQ_PRESET_3BIT_NC: *out = {3, 3, false, true}; return true;
     case TQ_PRESET_PROD3:   *out = {2, 0, false, false}; return true;   // keys only: its own layout
+    case TQ_PRESET_E4M3_BLK:
+    case TQ_PRESET_INT8_BLK: *out = {8, 0, false, false}; return true;  // 8-bit blocks: their own layout
     default: return false;
   }
 }
@@ -58,6 +60,28 @@ tq_status make_layout(const tq_config* cfg, tq_layout* out) {
   L.tile_bytes = L.vzero_off + 2 * kTileTokens;
   if (L.tile_bytes != kTileTokens * L.slot_bytes) return TQ_ERR_INVALID_ARG;
   L.block_bytes = static_cast<long long>(bs) * cfg->num_kv_heads * L.slot_bytes;
+  *out = L;
+  return TQ_OK;
+}
+
+tq_status make_b8_layout(const tq_config* cfg, tq_b8_layout* out) {
+  if (!cfg || !out) return TQ_ERR_INVALID_ARG;
+  if (cfg->preset != TQ_PRESET_E4M3_BLK && cfg->preset != TQ_PRESET_INT8_BLK) return TQ_ERR_INVALID_ARG;
+  if (cfg->head_dim <= 0 || cfg->block_size <= 0 || cfg->num_kv_heads <= 0) return TQ_ERR_INVALID_ARG;
+  if ((cfg->flags & ~TQ_FLAG_INDICES_READY) || cfg->partition_tokens != 0) return TQ_ERR_INVALID_ARG;
+  if (cfg->head_dim != 128 || cfg->num_kv_heads > 4096) return TQ_ERR_UNSUPPORTED;
+  const int bs = cfg->block_size;
+  if (bs != 16 && bs != 32 && bs != 64 && bs != 128) return TQ_ERR_UNSUPPORTED;
+  tq_b8_layout L;
+  std::memset(&L, 0, sizeof(L));
+  L.is_int8 = cfg->preset == TQ_PRESET_INT8_BLK;
+  L.code_limit = L.is_int8 ? 127 : 448;
+  L.tile_tokens = kTileTokens;
+  L.tile_bytes = kTileTokens * 2 * 128;
+  L.v_off = kTileTokens * 128;
+  const long long tiles = static_cast<long long>(cfg->num_kv_heads) * (bs / kTileTokens) * L.tile_bytes;
+  L.scale_off = static_cast<int>(tiles);   // at most 4096 heads x 32 KB
+  L.block_bytes = tiles + (8ll * cfg->num_kv_heads + 127) / 128 * 128;
   *out = L;
   return TQ_OK;
 }
@@ -122,6 +146,8 @@ tq_status tq_build_codebook(int head_dim, int bits, tq_codebook* out) {
 }
 
 tq_status tq_layout_for(const tq_config* cfg, tq_layout* out) { return tq::make_layout(cfg, out); }
+
+tq_status tq_b8_layout_for(const tq_config* cfg, tq_b8_layout* out) { return tq::make_b8_layout(cfg, out); }
 
 const char* tq_status_string(int status) {
   switch (status) {

@@ -21,6 +21,10 @@ bool preset_info(int preset, PresetInfo* out);
 // Fills the layout; returns TQ_OK or an error for bad/unsupported shapes.
 tq_status make_layout(const tq_config* cfg, tq_layout* out);
 
+// Fills the layout of the 8-bit cache with block scales, with the checks that
+// every tq_b8_* entry point shares.
+tq_status make_b8_layout(const tq_config* cfg, tq_b8_layout* out);
+
 // Shared argument checks.
 inline bool aligned16(const void* p) { return (reinterpret_cast<unsigned long long>(p) & 15ull) == 0; }
 inline int effective_partition(const tq_config* cfg) {
