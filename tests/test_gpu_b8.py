@@ -501,7 +501,8 @@ def test_continue_device_errors(tq, q_len):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("gain", [lambda j: 10.0 ** (j % 7 - 3), lambda j: 1e-28, lambda j: 1e30])
+@pytest.mark.parametrize("gain", [lambda j: 10.0 ** (j % 7 - 3), lambda j: 1e-28, lambda j: 1e30,
+                                  lambda j: 2.0 ** (60 if j % 2 else -60)])
 def test_continue_blocks_of_very_different_value_scales(tq, fmt, gain):
     c = Case(tq, fmt, 64, 4, 1, [400], seed=42).fill([400], gain)
     q = c.draw(150, 4)

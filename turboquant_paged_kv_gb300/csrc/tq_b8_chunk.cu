@@ -1,0 +1,597 @@
+// Chunks of queries against the 8-bit cache with block scales, on tcgen05
+// tensor cores.
+//
+//   out_i = sum_p softmax_p(scale s_k(p) q_i . k_p) s_v(p) v_p, p <= position of i
+//
+// One CTA serves 256 rows, the query heads of one KV head of 256 / group
+// consecutive queries, in two tiles of 128 rows, against 128 positions at a
+// time:
+//   S_t = Q_t K^T        tcgen05.mma, A and B from shared memory
+//   P_t = 8 p s_v / 2^sigma   one row per thread, S read from tensor memory
+//   O_t += P_t V         A = P_t from tensor memory (it takes S_t's place), B = V
+// The codes are exact in fp16; a query row is scaled by a power of two that
+// brings its largest magnitude to 2^14, so the scores are sums of exact
+// products. The block scales enter with the softmax: s_k multiplies a group of
+// 16 columns, log2(s_v) is added to the exponent, and the denominator takes
+// each group's sum times 2^sigma / (8 s_v). P is rounded once, to fp16 (half a
+// step is 2^-11; no step below 2^-24, which is 2^-27 sigma / s_v of the largest
+// weight). sigma follows the largest s_v of the positions at hand: it moves, and
+// the accumulators are rescaled, when that leaves 2^+-4 of it.
+//
+// Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread a row, no
+// shuffles), 8-11 expand codes from global memory into the two-stage fp16
+// operand buffers (128-byte swizzle, the same image for K, read as a K-major
+// operand, and V, read as an MN-major one), 12 issues the products: of the two
+// tiles in turn, so one tile's products run while the other's softmax does.
+// The running maximum moves in steps of 2^8 at least, so the accumulators are
+// rescaled (by the softmax warps, in tensor memory) almost never. S_t(i + 1) is
+// issued after O_t += P_t(i) V, so a complete S_t(i + 1) also says that the
+// accumulators of step i are at rest.
+// Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the CTA.
+#include "tq_attn.cuh"
+#include "tq_b8_chunk.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kRows = 256;             // of a CTA: two tiles of 128
+constexpr int kCols = 128;             // positions a step
+constexpr int kThreads = 512;
+constexpr float kStep = 8.f;           // the running maximum moves in steps of at least this, log2 units
+constexpr uint32_t kTileOp = 32768;    // a 128 x 128 fp16 operand: two halves of 64 columns, 128 bytes a row
+constexpr uint32_t kHalfOp = 16384;
+constexpr uint32_t kOffK = 2 * kTileOp, kOffV = 4 * kTileOp, kOffBar = 6 * kTileOp;
+constexpr uint32_t kSmem = kOffBar + 256 + 1024;   // and room to align to 1024
+// tensor memory columns
+constexpr uint32_t kColS = 0, kColO = 256;
+
+// barriers, 8 bytes each from kOffBar
+enum { kQFull, kKFull0, kKFull1, kVFull0, kVFull1, kKEmpty0, kKEmpty1, kVEmpty0, kVEmpty1, kSFull0, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kBars };
+
+// shared-memory operand descriptors: 128-byte swizzle, 8-row groups 1024 bytes apart
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {   // the halves of 64 columns kHalfOp apart
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (static_cast<uint64_t>(kHalfOp >> 4) << 16) | (64ull << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// f16 x f16 -> f32, M = 128, N = 128
+constexpr uint32_t kIdescQK = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);   // B is MN-major
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_smem_async() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// 32 columns of this warp's 32 rows, one row a lane
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+template <typename TO>
+__device__ __forceinline__ void write4(TO* dst, float4 v) {
+  if constexpr (std::is_same<TO, float>::value) {
+    *reinterpret_cast<float4*>(dst) = v;
+  } else if constexpr (std::is_same<TO, __half>::value) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
+// Where a CTA stands.
+struct Work {
+  int seq, h, row0, rows_q;   // sequence, KV head, first query of the chunk that is served, how many are
+  int q0;                     // row of that query in q and out
+  int pos0;                   // its position (may be negative)
+  int limit;                  // positions that may be read
+  int tile0, tiles;           // steps of 128 positions: [tile0, tile0 + tiles)
+};
+
+template <bool INT8>
+__device__ __forceinline__ void expand_rows(const uint4 x, uint32_t row_at, int c, int r7) {
+  // 16 codes of group c of a row -> 32 bytes: two 16-byte groups of the operand's half c / 4
+  uint4 lo, hi;
+  codes_to_half2<INT8>(x.x, lo.x, lo.y);
+  codes_to_half2<INT8>(x.y, lo.z, lo.w);
+  codes_to_half2<INT8>(x.z, hi.x, hi.y);
+  codes_to_half2<INT8>(x.w, hi.z, hi.w);
+  const uint32_t at = row_at + (c >> 2) * kHalfOp;
+  const int g = 2 * (c & 3);
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at + ((g ^ r7) << 4)), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w) : "memory");
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at + (((g + 1) ^ r7) << 4)), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w) : "memory");
+}
+
+template <typename TQ, typename TO, bool INT8>
+__global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs a) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ uint32_t s_tmem;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 1023u) & ~1023u;
+  const uint32_t bars = base + kOffBar;
+  auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // the latest queries of a chunk see the most: they go first
+  Work w;
+  const int per = kRows / a.group;   // queries of a CTA
+  const int x = blockIdx.x / a.splits, z = blockIdx.x - x * a.splits;
+  const int tile_q = static_cast<int>(gridDim.x) / a.splits - 1 - x;
+  w.h = blockIdx.y;
+  w.seq = blockIdx.z;
+  const int raw0 = ld_dep_s32(a.query_start + w.seq), raw1 = ld_dep_s32(a.query_start + w.seq + 1);
+  const int raw_len = max(ld_dep_s32(a.seq_lens + w.seq), 0);
+  const int qs = min(max(raw0, 0), a.total_q);
+  const int n = min(max(raw1, qs), a.total_q) - qs;
+  const int served = min(n, a.max_q_len);
+  w.limit = min(raw_len, min(a.max_seq_len, a.cap));
+  if (tile_q == 0 && z == 0 && w.h == 0 && threadIdx.x == 0 && n > 0 &&
+      (n > a.max_q_len || raw_len > min(a.max_seq_len, a.cap)))
+    b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
+  const int heads0 = w.h * a.group;
+  if (tile_q == 0 && z == 0 && n > served) {   // queries past max_q_len: zeros
+    const long long count = static_cast<long long>(n - served) * a.group * (kB8D / 4);
+    for (long long i = threadIdx.x; i < count; i += kThreads) {
+      const long long r = i / (kB8D / 4);
+      write4<TO>(static_cast<TO*>(a.out) + ((qs + served + r / a.group) * a.n_q + heads0 + r % a.group) * kB8D + 4 * (i % (kB8D / 4)),
+                 make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  }
+  w.row0 = tile_q * per;
+  w.rows_q = min(per, served - w.row0);
+  if (w.rows_q <= 0) return;
+  w.q0 = qs + w.row0;
+  w.pos0 = raw_len - n + w.row0;
+  const int seen = min(w.pos0 + w.rows_q, w.limit);   // positions that the last query sees
+  const int all_tiles = seen > 0 ? (seen + kCols - 1) / kCols : 0;
+  w.tile0 = min(z * a.split_tiles, all_tiles);
+  w.tiles = min(a.split_tiles, all_tiles - w.tile0);
+  const int rows = w.rows_q * a.group;
+  const int halves = rows > 128 ? 2 : 1;   // row tiles at work
+
+  if (w.tiles == 0) {   // nothing to see here
+    if (a.splits == 1) {
+      for (int i = threadIdx.x; i < rows * (kB8D / 4); i += kThreads) {
+        const int r = i / (kB8D / 4);
+        write4<TO>(static_cast<TO*>(a.out) + (static_cast<long long>(w.q0 + r / a.group) * a.n_q + heads0 + r % a.group) * kB8D + 4 * (i % (kB8D / 4)),
+                   make_float4(0.f, 0.f, 0.f, 0.f));
+      }
+    } else if (threadIdx.x < rows) {
+      const int r = threadIdx.x;
+      a.rec_lse[(static_cast<long long>(w.q0 + r / a.group) * a.n_q + heads0 + r % a.group) * a.splits + z] = -INFINITY;
+    }
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(kQFull), 4 * halves);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kKFull0 + i), 4);
+      mbar_init(bar(kVFull0 + i), 4);
+      mbar_init(bar(kKEmpty0 + i), 1);
+      mbar_init(bar(kVEmpty0 + i), 1);
+      mbar_init(bar(kSFull0 + i), 1);
+      mbar_init(bar(kPFull0 + i), 4);
+      mbar_init(bar(kODone0 + i), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 12) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&s_tmem))) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  auto wait = [&](int b, uint32_t parity) {   // false: give up
+    if (mbar_wait(bar(b), parity)) return true;
+    b8_flag(a.status, TQ_DEV_TIMEOUT);
+    return false;
+  };
+  auto warp_wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };   // one answer for the warp
+  const int tiles = w.tiles;
+  const int* table = a.block_table + static_cast<long long>(w.seq) * a.c.bt_stride;
+  const int shift = a.c.log2_bs - 4;
+
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
+    const int t = warp >> 2;
+    if (t < halves) {
+      // this thread's row: a query head; its scaled fp16 copy becomes a row of A
+      const int r = threadIdx.x;   // 0 .. 255
+      const bool live = r < rows;
+      const int qi = r / a.group, head = heads0 + r - qi * a.group;
+      float down = 0.f;
+      {
+        const uint32_t row_at = base + t * kTileOp + (r & 127) * 128;
+        const TQ* src = static_cast<const TQ*>(a.q) + (w.q0 + qi) * a.q_stride + static_cast<long long>(head) * kB8D;
+        uint4 v[16];
+        uint32_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          v[i] = live ? ld_dep_u32x4(src + 8 * i) : make_uint4(0, 0, 0, 0);
+          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        }
+        const uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+        float amax;
+        if constexpr (std::is_same<TQ, __nv_bfloat16>::value) amax = __uint_as_float(m << 16);
+        else amax = half2_to_float2(m).x;
+        // 2^k with amax 2^k in [2^14, 2^15)
+        const int k = min(max(14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), -112), 112);
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
+        down = a.qscale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const uint32_t ws[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float2 f;
+            if constexpr (std::is_same<TQ, __nv_bfloat16>::value) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&ws[j]));
+            else f = half2_to_float2(ws[j]);
+            o[j] = pack_half2(f.x * up, f.y * up);
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(row_at + (i >> 3) * kHalfOp + (((i & 7) ^ (r & 7)) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+        }
+        fence_smem_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kQFull));
+      }
+      const int vis = live ? max(min(w.pos0 + qi + 1, w.limit), 0) : 0;   // positions that this row sees
+      const int vis_least = __reduce_min_sync(0xffffffffu, live ? vis : 0x7fffffff);
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t t_s = tmem + lanes + kColS + t * 128, t_o = tmem + lanes + kColO + t * 128;
+
+      // lanes 0-7 hold the scales of the step's 8 groups of 16 positions; the
+      // next step's are on their way meanwhile
+      auto group_block = [&](int i) {   // block id of this lane's group of step i; -2: behind the end
+        const int g16 = (w.tile0 + i) * 8 + (lane & 7);
+        return i < tiles && g16 * 16 < w.limit ? ld_dep_s32(table + (g16 >> shift)) : -2;
+      };
+      auto group_scales = [&](int blk) {
+        return a.c.good(blk) ? ld_dep_u32x2(a.c.scales(blk, w.h)) : make_uint2(0u, 0u);
+      };
+      int blk = group_block(0);
+      uint2 sc = group_scales(blk);
+      int blk_next = group_block(1);
+      float m = -1e30f, l = 0.f, sigma = 0.f, sigma_max = -INFINITY;
+      bool ok = true;
+      for (int i = 0; i < tiles; ++i) {
+        const bool bad = sc.x == 0u;   // a scale is never 0
+        if (bad && blk != -2 && t == 0 && warp == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
+        const unsigned bad_groups = __ballot_sync(0xffffffffu, bad) & 0xffu;
+        const float my_sk = bad ? 1.f : __uint_as_float(sc.x);
+        const float my_lv = bad ? 0.f : log2f(__uint_as_float(sc.y));
+        float top = bad ? -INFINITY : my_lv;
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        blk = blk_next;
+        sc = group_scales(blk);
+        blk_next = group_block(i + 2);
+        float moved = 0.f;   // what sigma falls by
+        if (top != -INFINITY && !(fabsf(top - sigma) <= 4.f && sigma_max != -INFINITY)) {
+          sigma_max = fmaxf(sigma_max, top);
+          const float next = fmaxf(rintf(top), rintf(sigma_max) - 64.f);
+          moved = sigma - next;
+          sigma = next;
+        }
+
+        if (!(ok = warp_wait(kSFull0 + t, i & 1))) break;
+        fence_after();
+        float s[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
+        wait_ld();
+        const int at = (w.tile0 + i) * kCols;
+        if (bad_groups || at + kCols > vis_least) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (at + c >= vis || (bad_groups >> (c >> 4) & 1)) s[c] = -INFINITY;
+        }
+        float f[8], mx = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          f[g] = __shfl_sync(0xffffffffu, my_sk, g) * down;
+          float y = s[16 * g];
+#pragma unroll
+          for (int c = 1; c < 16; ++c) y = fmaxf(y, s[16 * g + c]);
+          mx = fmaxf(mx, y * f[g]);
+        }
+        const bool grow = mx > m + kStep;
+        if (__any_sync(0xffffffffu, grow) || moved != 0.f) {
+          const float u = grow ? mx : m;
+          const float el = ex2(m - u);
+          const float e = ex2(m - u + moved);
+          m = u;
+          l *= el;
+          if (i > 0) {
+            uint32_t o[32];
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32(t_o + 32 * c, o);
+              wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * e);
+              tmem_st32(t_o + 32 * c, o);
+            }
+          }
+        }
+        uint32_t p[64];
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          // log2(8 s_v / 2^sigma); below -100 the group's values vanish next to the
+          // others', and its weights still count
+          const float lv = fmaxf(__shfl_sync(0xffffffffu, my_lv, g) - sigma + 3.f, -100.f);
+          const float add = lv - m;
+          float sum = 0.f;
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            const float p0 = ex2(fmaf(s[16 * g + c], f[g], add)), p1 = ex2(fmaf(s[16 * g + c + 1], f[g], add));
+            sum += p0 + p1;
+            p[8 * g + c / 2] = pack_half2(p0, p1);
+          }
+          l = fmaf(sum, ex2(-lv), l);
+        }
+        tmem_st32(t_s, p);
+        tmem_st32(t_s + 32, p + 32);
+        wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull0 + t));
+      }
+      if (ok && warp_wait(kODone0 + t, 0)) {
+        fence_after();
+        const float scale = l > 0.f ? ex2(sigma - 3.f) / l : (l == 0.f ? 0.f : l);   // NaN stays
+        const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + head;
+        const bool whole = a.splits == 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(t_o + 32 * c, o);
+          wait_ld();
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              float4 y = make_float4(__uint_as_float(o[j]) * scale, __uint_as_float(o[j + 1]) * scale,
+                                     __uint_as_float(o[j + 2]) * scale, __uint_as_float(o[j + 3]) * scale);
+              if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (whole) write4<TO>(static_cast<TO*>(a.out) + orow * kB8D + 32 * c + j, y);
+              else *reinterpret_cast<float4*>(a.rec_o + (orow * a.splits + z) * kB8D + 32 * c + j) = y;
+            }
+          }
+        }
+        if (live && !whole) a.rec_lse[orow * a.splits + z] = l == 0.f ? -INFINITY : m + __log2f(l);
+      }
+    }
+  } else if (warp < 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    // 32 positions a warp and step: 8 loads of 16 codes a lane for the keys, 8 for the values
+    const int cw = warp - 8, rs = lane >> 2, cc = lane & 3;
+    auto load = [&](int i, int kv, uint4* x) {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {   // 16 positions of one block each
+        const int g16 = (w.tile0 + i) * 8 + 2 * cw + half;
+        int blk = -1;
+        if (i < tiles && g16 * 16 < w.limit) blk = ld_dep_s32(table + (g16 >> shift));
+        const bool good = a.c.good(blk);
+        const uint8_t* src = a.c.tile(good ? blk : 0, w.h, g16) + kv * kB8HalfBytes;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = 8 * (k >> 1) + rs, c = 4 * (k & 1) + cc;
+          x[4 * half + k] = make_uint4(0, 0, 0, 0);
+          if (good && g16 * 16 + row < w.limit) x[4 * half + k] = ld_dep_u32x4(src + row * kB8D + ((c ^ (row & 7)) << 4));
+        }
+      }
+    };
+    auto store = [&](uint32_t op, const uint4* x) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int row = 32 * cw + 8 * (k >> 1) + rs;
+        expand_rows<INT8>(x[k], op + row * 128, 4 * (k & 1) + cc, row & 7);
+      }
+    };
+    uint4 x[8], y[8];
+    load(0, 0, x);
+    load(0, 1, y);
+    bool ok = true;
+    for (int i = 0; i < tiles && ok; ++i) {
+      const int st = i & 1;
+      const uint32_t free_phase = ((i >> 1) & 1) ^ 1;
+      if (!(ok = warp_wait(kKEmpty0 + st, free_phase))) break;
+      store(base + kOffK + st * kTileOp, x);
+      fence_smem_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kKFull0 + st));
+      load(i + 1, 0, x);
+      if (!(ok = warp_wait(kVEmpty0 + st, free_phase))) break;
+      store(base + kOffV + st * kTileOp, y);
+      fence_smem_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kVFull0 + st));
+      load(i + 1, 1, y);
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    if (warp == 12 && lane == 0) {
+      auto qk = [&](int t, int st) {
+        const uint32_t q_at = base + t * kTileOp, k_at = base + kOffK + st * kTileOp;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t off = (k >> 2) * kHalfOp + (k & 3) * 32;
+          mma_ss(tmem + kColS + t * 128, desc_k_major(q_at + off), desc_k_major(k_at + off), kIdescQK, k > 0);
+        }
+        mma_commit(bar(kSFull0 + t));
+      };
+      bool ok = wait(kQFull, 0) && wait(kKFull0, 0);
+      if (ok) {
+        fence_after();
+        for (int t = 0; t < halves; ++t) qk(t, 0);
+        mma_commit(bar(kKEmpty0));
+      }
+      for (int i = 0; i < tiles && ok; ++i) {
+        const int st = i & 1, nst = st ^ 1;
+        const bool more = i + 1 < tiles;
+        for (int t = 0; t < halves && ok; ++t) {
+          ok = wait(kPFull0 + t, i & 1);
+          if (ok && t == 0) ok = wait(kVFull0 + st, (i >> 1) & 1);
+          if (!ok) break;
+          fence_after();
+          const uint32_t v_at = base + kOffV + st * kTileOp;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + 8 * k, desc_mn_major(v_at + 2048 * k), kIdescPV, i > 0 || k > 0);
+          if (more) {
+            if (t == 0 && !(ok = wait(kKFull0 + nst, ((i + 1) >> 1) & 1))) break;
+            fence_after();
+            qk(t, nst);
+          } else {
+            mma_commit(bar(kODone0 + t));
+          }
+        }
+        if (ok && more) {
+          mma_commit(bar(kVEmpty0 + st));
+          mma_commit(bar(kKEmpty0 + nst));
+        }
+      }
+    }
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 12) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+  }
+}
+
+// One warp per (query row, query head): merges the splits.
+template <typename TO>
+__global__ void __launch_bounds__(256) b8_chunk_merge_kernel(const B8ChunkArgs a) {
+  const int lane = threadIdx.x & 31;
+  const long long orow = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  grid_dep_wait();
+  grid_dep_launch();
+  if (orow >= static_cast<long long>(a.total_q) * a.n_q) return;
+  const int i = static_cast<int>(orow / a.n_q);
+  int lo = 0, hi = a.batch;   // the last sequence that starts at or before row i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ld_dep_s32(a.query_start + mid) <= i) lo = mid;
+    else hi = mid;
+  }
+  const int q0 = ld_dep_s32(a.query_start + lo), q1 = ld_dep_s32(a.query_start + lo + 1);
+  if (i < q0 || i >= q1 || i - q0 >= a.max_q_len) return;   // no records: behind the last sequence, or zeros already
+  float m = -INFINITY;
+  for (int z = 0; z < a.splits; ++z) m = fmaxf(m, ld_dep_f32(a.rec_lse + orow * a.splits + z));
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int z = 0; z < a.splits; ++z) {
+    const float lse = ld_dep_f32(a.rec_lse + orow * a.splits + z);
+    if (lse == -INFINITY) continue;
+    const float e = exp2f(lse - m);
+    const float4 x = ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + (orow * a.splits + z) * kB8D) + lane);
+    l += e;
+    o.x = fmaf(e, x.x, o.x);
+    o.y = fmaf(e, x.y, o.y);
+    o.z = fmaf(e, x.z, o.z);
+    o.w = fmaf(e, x.w, o.w);
+  }
+  const float r = l == 0.f ? 0.f : 1.f / l;
+  write4<TO>(static_cast<TO*>(a.out) + orow * kB8D + 4 * lane, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
+}
+
+template <typename TQ, typename TO, bool INT8>
+cudaError_t launch(const B8ChunkArgs& a, const B8ChunkPlan& p, cudaStream_t s) {
+  auto* kernel = b8_chunk_kernel<TQ, TO, INT8>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (err != cudaSuccess) return err;
+  err = launch_pdl(kernel, dim3(p.q_tiles * p.splits, a.c.n_kv, a.batch), dim3(kThreads), kSmem, s, a);
+  if (err != cudaSuccess || p.splits == 1) return err;
+  const long long rows = static_cast<long long>(a.total_q) * a.n_q;
+  return launch_pdl(b8_chunk_merge_kernel<TO>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a);
+}
+
+template <typename TQ, typename TO>
+cudaError_t launch_format(const B8ChunkArgs& a, const B8ChunkPlan& p, bool is_int8, cudaStream_t s) {
+  return is_int8 ? launch<TQ, TO, true>(a, p, s) : launch<TQ, TO, false>(a, p, s);
+}
+
+template <typename TQ>
+cudaError_t launch_out(const B8ChunkArgs& a, const B8ChunkPlan& p, bool is_int8, int out_dtype, cudaStream_t s) {
+  if (out_dtype == TQ_DTYPE_F32) return launch_format<TQ, float>(a, p, is_int8, s);
+  if (out_dtype == TQ_DTYPE_F16) return launch_format<TQ, __half>(a, p, is_int8, s);
+  return launch_format<TQ, __nv_bfloat16>(a, p, is_int8, s);
+}
+
+}  // namespace
+
+B8ChunkPlan b8_chunk_plan(const tq_config* cfg, int batch, int total_q, int max_q_len, int max_seq_len) {
+  constexpr int kSms = 152;
+  B8ChunkPlan p;
+  const int per = kRows / (cfg->num_q_heads / cfg->num_kv_heads);
+  const int longest = max_q_len < total_q ? max_q_len : total_q;
+  p.q_tiles = longest > 0 ? (longest + per - 1) / per : 1;
+  const int tiles = max_seq_len > 0 ? static_cast<int>((static_cast<long long>(max_seq_len) + kCols - 1) / kCols) : 1;
+  const long long ctas = static_cast<long long>(p.q_tiles) * cfg->num_kv_heads * batch;
+  // fewer CTAs than SMs: the history is split, two steps a part at least
+  long long splits = ctas > 0 ? kSms / ctas : 1;
+  if (splits > tiles / 2) splits = tiles / 2;
+  if (splits > 32) splits = 32;
+  if (splits < 1) splits = 1;
+  p.split_tiles = static_cast<int>((tiles + splits - 1) / splits);
+  p.splits = (tiles + p.split_tiles - 1) / p.split_tiles;
+  const size_t rows = static_cast<size_t>(total_q) * cfg->num_q_heads;
+  p.workspace = p.splits == 1 ? 16 : (rows * p.splits * (kB8D + 1) * sizeof(float) + 15) / 16 * 16;
+  return p;
+}
+
+cudaError_t b8_chunk_launch(B8ChunkArgs a, const B8ChunkPlan& p, bool is_int8, int q_dtype, int out_dtype,
+                            void* workspace, cudaStream_t s) {
+  a.splits = p.splits;
+  a.split_tiles = p.split_tiles;
+  a.rec_o = static_cast<float*>(workspace);
+  a.rec_lse = a.rec_o + static_cast<size_t>(a.total_q) * a.n_q * p.splits * kB8D;
+  return q_dtype == TQ_DTYPE_BF16 ? launch_out<__nv_bfloat16>(a, p, is_int8, out_dtype, s)
+                                  : launch_out<__half>(a, p, is_int8, out_dtype, s);
+}
+
+}  // namespace tq
