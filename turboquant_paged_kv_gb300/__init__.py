@@ -10,6 +10,7 @@ raises ImportError if the library is not built (there is no fallback path).
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -262,10 +263,13 @@ def tq_b8_layout_for(cfg: tq_config) -> tq_b8_layout:
     return lay
 
 
+_B8_TYPES = (torch.float16, torch.bfloat16)
+
+
 def _b8_rows(name: str, t: torch.Tensor, heads: int, d: int) -> int:
     """Checks a [rows, heads, d] tensor whose rows may be a stride apart (a slice
     of a fused projection's output); returns that stride in elements."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d or t.dtype not in (torch.float16, torch.bfloat16):
+    if t.dtype not in _B8_TYPES or t.dim() != 3 or t.shape[1:] != (heads, d):
         raise ValueError(f"{name} must be [rows, {heads}, {d}] float16 or bfloat16, got {tuple(t.shape)} {t.dtype}")
     s0, s1, s2 = t.stride()
     if t.shape[0] == 0:
@@ -275,34 +279,43 @@ def _b8_rows(name: str, t: torch.Tensor, heads: int, d: int) -> int:
     return s0 if t.shape[0] > 1 else heads * d
 
 
-def _b8_common(cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor, others, stream) -> None:
-    """What every call on the cache has in common: index tensors, and one device,
-    the current one (the library launches there)."""
+def _b8_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: torch.Tensor, seq_lens: torch.Tensor,
+               others, stream) -> tuple:
+    """What every call on the cache has in common: index tensors, one device, the
+    current one (the library launches there), and the cache's size. Returns
+    (num_blocks, row length of the table, raw stream)."""
     if cache.dtype != torch.uint8 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous uint8 tensor")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [batch, blocks] with contiguous rows")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 matrix [batch, blocks]")
     if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or not seq_lens.is_contiguous():
         raise ValueError("seq_lens must be a contiguous int32 vector")
-    if block_table.shape[0] < seq_lens.shape[0]:
+    rows, width = block_table.shape
+    if rows < seq_lens.shape[0]:
         raise ValueError("block_table has fewer rows than seq_lens has entries")
-    if not cache.is_cuda:
-        raise ValueError("the tensors must be on a CUDA device")
     dev = cache.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be on a CUDA device")
     for t in (block_table, seq_lens, *others):
         if t is not None and t.get_device() != dev:
             raise ValueError("the tensors must be on one CUDA device")
     if dev != torch.cuda.current_device():
         raise ValueError("the tensors must be on the current CUDA device")
-    if stream is not None and stream.device_index != dev:
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device_index != dev:
         raise ValueError("the stream must be one of the tensors' device")
+    have = cache.numel() // _b8_block_bytes(cfg.preset, cfg.head_dim, cfg.block_size, cfg.num_kv_heads)
+    if num_blocks is None:
+        num_blocks = have
+    elif num_blocks > have:
+        raise ValueError(f"cache holds {have} blocks, not {num_blocks}")
+    return num_blocks, width, stream.cuda_stream
 
 
-def _b8_table(block_table: torch.Tensor) -> int:
-    """The distance of the table's rows, which may be longer than what the view shows."""
-    if block_table.shape[0] > 1 and block_table.stride(0) != block_table.shape[1]:
-        raise ValueError("block_table must be contiguous")
-    return block_table.shape[1]
+@functools.lru_cache(maxsize=256)
+def _b8_block_bytes(preset: int, head_dim: int, block_size: int, num_kv_heads: int) -> int:
+    return tq_b8_layout_for(make_config(preset, num_kv_heads, num_kv_heads, head_dim, block_size)).block_bytes
 
 
 def _b8_starts(query_start: torch.Tensor, seq_lens: torch.Tensor) -> None:
@@ -310,18 +323,18 @@ def _b8_starts(query_start: torch.Tensor, seq_lens: torch.Tensor) -> None:
         raise ValueError("query_start must be a contiguous int32 vector of batch + 1 entries")
 
 
-def _b8_out(name: str, t: torch.Tensor, shape) -> None:
-    if t.dtype not in _DTYPES or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _b8_out(name: str, t: torch.Tensor, shape) -> int:
+    if t.dtype not in _DTYPES or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float16, bfloat16 or float32 tensor of shape {tuple(shape)}")
+    return _DTYPES[t.dtype]
 
 
-def _b8_blocks(cfg: tq_config, cache: torch.Tensor, num_blocks: int | None) -> int:
-    have = cache.numel() // tq_b8_layout_for(cfg).block_bytes
-    if num_blocks is None:
-        return have
-    if num_blocks > have:
-        raise ValueError(f"cache holds {have} blocks, not {num_blocks}")
-    return num_blocks
+def _b8_status(t):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or t.numel() < 1:
+        raise ValueError("dev_status must be an int32 tensor")
+    return t.data_ptr()
 
 
 def tq_b8_store(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query_start: torch.Tensor, max_q_len: int,
@@ -336,11 +349,12 @@ def tq_b8_store(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query_st
     if key.dtype != value.dtype or key.shape[0] != value.shape[0]:
         raise ValueError("key and value must have one dtype and one number of rows")
     _b8_starts(query_start, seq_lens)
-    _b8_common(cache, block_table, seq_lens, (key, value, query_start, dev_status), stream)
-    _abi.check("tq_b8_store", _LIB.tq_b8_store(
-        ctypes.byref(cfg), _ptr(key), ks, _ptr(value), vs, _DTYPES[key.dtype], _ptr(query_start), seq_lens.shape[0],
-        key.shape[0], max_q_len, _ptr(cache), _b8_blocks(cfg, cache, num_blocks), _ptr(block_table),
-        _b8_table(block_table), _ptr(seq_lens), _ptr(dev_status), _stream(stream)))
+    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (key, value, query_start, dev_status), stream)
+    st = _LIB.tq_b8_store(cfg, key.data_ptr(), ks, value.data_ptr(), vs, _DTYPES[key.dtype], query_start.data_ptr(),
+                          seq_lens.shape[0], key.shape[0], max_q_len, cache.data_ptr(), nb, block_table.data_ptr(), width,
+                          seq_lens.data_ptr(), _b8_status(dev_status), raw)
+    if st:
+        raise TQError("tq_b8_store", st)
 
 
 def tq_b8_dequant(cfg: tq_config, cache: torch.Tensor, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -348,15 +362,14 @@ def tq_b8_dequant(cfg: tq_config, cache: torch.Tensor, block_table: torch.Tensor
                   dev_status: torch.Tensor | None = None, stream=None) -> None:
     """key_out, value_out [B, max_seq_len, n_kv, d] (f16, bf16 or f32), written in full."""
     shape = (seq_lens.shape[0], max_seq_len, cfg.num_kv_heads, cfg.head_dim)
-    _b8_out("key_out", key_out, shape)
-    _b8_out("value_out", value_out, shape)
-    if value_out.dtype != key_out.dtype:
+    out_type = _b8_out("key_out", key_out, shape)
+    if _b8_out("value_out", value_out, shape) != out_type:
         raise ValueError("key_out and value_out must have the same dtype")
-    _b8_common(cache, block_table, seq_lens, (key_out, value_out, dev_status), stream)
-    _abi.check("tq_b8_dequant", _LIB.tq_b8_dequant(
-        ctypes.byref(cfg), _ptr(cache), _b8_blocks(cfg, cache, num_blocks), _ptr(block_table), _b8_table(block_table),
-        _ptr(seq_lens), seq_lens.shape[0], max_seq_len, _ptr(key_out), _ptr(value_out), _DTYPES[key_out.dtype],
-        _ptr(dev_status), _stream(stream)))
+    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (key_out, value_out, dev_status), stream)
+    st = _LIB.tq_b8_dequant(cfg, cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(), shape[0],
+                            max_seq_len, key_out.data_ptr(), value_out.data_ptr(), out_type, _b8_status(dev_status), raw)
+    if st:
+        raise TQError("tq_b8_dequant", st)
 
 
 def tq_b8_decode_workspace_size(cfg: tq_config, batch: int, max_seq_len: int) -> int:
@@ -369,15 +382,15 @@ def tq_b8_decode(cfg: tq_config, q: torch.Tensor, cache: torch.Tensor, block_tab
                  stream=None) -> None:
     """q [B, n_q, d] f16/bf16 (rows may be a stride apart); out [B, n_q, d]; seq_lens [B] int32."""
     qs = _b8_rows("q", q, cfg.num_q_heads, cfg.head_dim)
-    _b8_out("out", out, q.shape)
+    out_type = _b8_out("out", out, q.shape)
     if q.shape[0] != seq_lens.shape[0]:
         raise ValueError("q must have one row per sequence")
-    _b8_common(cache, block_table, seq_lens, (q, out, workspace, dev_status), stream)
-    _abi.check("tq_b8_decode", _LIB.tq_b8_decode(
-        ctypes.byref(cfg), _ptr(q), qs, _DTYPES[q.dtype], _ptr(cache), _b8_blocks(cfg, cache, num_blocks),
-        _ptr(block_table), _b8_table(block_table), _ptr(seq_lens), q.shape[0], max_seq_len, float(scale), _ptr(out),
-        _DTYPES[out.dtype], _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status),
-        _stream(stream)))
+    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (q, out, workspace, dev_status), stream)
+    st = _LIB.tq_b8_decode(cfg, q.data_ptr(), qs, _DTYPES[q.dtype], cache.data_ptr(), nb, block_table.data_ptr(), width,
+                           seq_lens.data_ptr(), q.shape[0], max_seq_len, scale, out.data_ptr(), out_type,
+                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _b8_status(dev_status), raw)
+    if st:
+        raise TQError("tq_b8_decode", st)
 
 
 def tq_b8_continue_workspace_size(cfg: tq_config, batch: int, total_q: int, max_q_len: int, max_seq_len: int) -> int:
@@ -393,11 +406,12 @@ def tq_b8_continue(cfg: tq_config, q: torch.Tensor, query_start: torch.Tensor, m
     seq_lens int32 [batch] (lengths with the chunk), out [total_q, n_q, d]; rows
     of out from query_start[batch] on are left as they are."""
     qs = _b8_rows("q", q, cfg.num_q_heads, cfg.head_dim)
-    _b8_out("out", out, q.shape)
+    out_type = _b8_out("out", out, q.shape)
     _b8_starts(query_start, seq_lens)
-    _b8_common(cache, block_table, seq_lens, (q, query_start, out, workspace, dev_status), stream)
-    _abi.check("tq_b8_continue", _LIB.tq_b8_continue(
-        ctypes.byref(cfg), _ptr(q), qs, _DTYPES[q.dtype], _ptr(query_start), seq_lens.shape[0], q.shape[0], max_q_len,
-        _ptr(cache), _b8_blocks(cfg, cache, num_blocks), _ptr(block_table), _b8_table(block_table), _ptr(seq_lens),
-        max_seq_len, float(scale), _ptr(out), _DTYPES[out.dtype], _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _ptr(dev_status), _stream(stream)))
+    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (q, query_start, out, workspace, dev_status), stream)
+    st = _LIB.tq_b8_continue(cfg, q.data_ptr(), qs, _DTYPES[q.dtype], query_start.data_ptr(), seq_lens.shape[0], q.shape[0],
+                             max_q_len, cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(),
+                             max_seq_len, scale, out.data_ptr(), out_type, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _b8_status(dev_status), raw)
+    if st:
+        raise TQError("tq_b8_continue", st)

@@ -23,10 +23,12 @@
 // operand buffers (128-byte swizzle, the same image for K, read as a K-major
 // operand, and V, read as an MN-major one), 12 issues the products: of the two
 // tiles in turn, so one tile's products run while the other's softmax does.
-// The running maximum moves in steps of 2^8 at least, so the accumulators are
-// rescaled (by the softmax warps, in tensor memory) almost never. S_t(i + 1) is
-// issued after O_t += P_t(i) V, so a complete S_t(i + 1) also says that the
-// accumulators of step i are at rest.
+// No maximum is sought in the common case: the weights are taken with the
+// maximum so far, and a row of which some P would not fit in fp16 shows in its
+// sums of 16; only then the row's new maximum is found, and what was accumulated
+// (by the softmax warps, in tensor memory) and the step's earlier P are
+// rescaled. S_t(i + 1) is issued after O_t += P_t(i) V, so a complete S_t(i + 1)
+// also says that the accumulators of step i are at rest.
 // Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the CTA.
 #include "tq_attn.cuh"
 #include "tq_b8_chunk.cuh"
@@ -37,7 +39,7 @@ namespace {
 constexpr int kRows = 256;             // of a CTA: two tiles of 128
 constexpr int kCols = 128;             // positions a step
 constexpr int kThreads = 512;
-constexpr float kStep = 8.f;           // the running maximum moves in steps of at least this, log2 units
+constexpr float kMost = 60000.f;       // sums of 16 P up to this: every P fits in fp16
 constexpr uint32_t kTileOp = 32768;    // a 128 x 128 fp16 operand: two halves of 64 columns, 128 bytes a row
 constexpr uint32_t kHalfOp = 16384;
 constexpr uint32_t kOffK = 2 * kTileOp, kOffV = 4 * kTileOp, kOffBar = 6 * kTileOp;
@@ -60,6 +62,11 @@ __device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr) {   // the halv
 constexpr uint32_t kIdescQK = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);
 constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);   // B is MN-major
 
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
@@ -71,6 +78,23 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
       : "memory");
+}
+// two fp32 operations at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(bar) : "memory");
@@ -101,6 +125,38 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// *p where pred, else zeros: loads into preset registers, so that nothing waits
+// for the value here (a select on what was loaded would).
+__device__ __forceinline__ uint2 ld_or_zero2(const void* p, bool pred) {
+  uint2 v = make_uint2(0u, 0u);
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %3, 0;\n @q ld.global.cg.v2.b32 {%0, %1}, [%2];\n}\n"
+               : "+r"(v.x), "+r"(v.y)
+               : "l"(p), "r"(static_cast<unsigned>(pred)));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_or_zero4(const void* p, bool pred) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %5, 0;\n @q ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+               : "l"(p), "r"(static_cast<unsigned>(pred)));
+  return v;
 }
 
 template <typename TO>
@@ -142,7 +198,8 @@ template <typename TQ, typename TO, bool INT8>
 __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs a) {
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float4 s_groups[8][8];   // each softmax warp's: the step's groups of 16 positions
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 1023u) & ~1023u;
   const uint32_t bars = base + kOffBar;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
@@ -220,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
   auto wait = [&](int b, uint32_t parity) {   // false: give up
     if (mbar_wait(bar(b), parity)) return true;
     b8_flag(a.status, TQ_DEV_TIMEOUT);
@@ -232,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
   const int shift = a.c.log2_bs - 4;
 
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
     const int t = warp >> 2;
     if (t < halves) {
       // this thread's row: a query head; its scaled fp16 copy becomes a row of A
@@ -284,10 +341,11 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       // next step's are on their way meanwhile
       auto group_block = [&](int i) {   // block id of this lane's group of step i; -2: behind the end
         const int g16 = (w.tile0 + i) * 8 + (lane & 7);
-        return i < tiles && g16 * 16 < w.limit ? ld_dep_s32(table + (g16 >> shift)) : -2;
+        return ldg_or(table + (g16 >> shift), i < tiles && g16 * 16 < w.limit, -2);
       };
       auto group_scales = [&](int blk) {
-        return a.c.good(blk) ? ld_dep_u32x2(a.c.scales(blk, w.h)) : make_uint2(0u, 0u);
+        const bool good = a.c.good(blk);
+        return ld_or_zero2(a.c.scales(good ? blk : 0, w.h), good);
       };
       int blk = group_block(0);
       uint2 sc = group_scales(blk);
@@ -298,81 +356,114 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
         const bool bad = sc.x == 0u;   // a scale is never 0
         if (bad && blk != -2 && t == 0 && warp == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
         const unsigned bad_groups = __ballot_sync(0xffffffffu, bad) & 0xffu;
-        const float my_sk = bad ? 1.f : __uint_as_float(sc.x);
-        const float my_lv = bad ? 0.f : log2f(__uint_as_float(sc.y));
+        const float my_lv = bad ? 0.f : __log2f(__uint_as_float(sc.y));
         float top = bad ? -INFINITY : my_lv;
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-        blk = blk_next;
-        sc = group_scales(blk);
-        blk_next = group_block(i + 2);
-        float moved = 0.f;   // what sigma falls by
+        float by_o = 1.f;   // what the accumulators take
         if (top != -INFINITY && !(fabsf(top - sigma) <= 4.f && sigma_max != -INFINITY)) {
           sigma_max = fmaxf(sigma_max, top);
           const float next = fmaxf(rintf(top), rintf(sigma_max) - 64.f);
-          moved = sigma - next;
+          by_o = ex2(sigma - next);
           sigma = next;
         }
+        if (lane < 8) {
+          // s_k, log2(8 s_v / 2^sigma) and the inverse of what that stands for; below
+          // -100 the group's values vanish next to the others', its weights still count
+          const float lv = fmaxf(my_lv - sigma + 3.f, -100.f);
+          s_groups[warp][lane] = make_float4(bad ? 1.f : __uint_as_float(sc.x), lv, ex2(-lv), 0.f);
+        }
+        __syncwarp();
+        blk = blk_next;
+        sc = group_scales(blk);
+        blk_next = group_block(i + 2);
 
         if (!(ok = warp_wait(kSFull0 + t, i & 1))) break;
         fence_after();
-        float s[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, reinterpret_cast<uint32_t*>(s) + 32 * c);
-        wait_ld();
         const int at = (w.tile0 + i) * kCols;
-        if (bad_groups || at + kCols > vis_least) {
+        const bool masked = bad_groups || at + kCols > vis_least;
+        float sums = 0.f;
+        float two[2][32];   // 32 columns of S; the next 32 are on their way
+        tmem_ld32(t_s, reinterpret_cast<uint32_t*>(two[0]));
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (at + c >= vis || (bad_groups >> (c >> 4) & 1)) s[c] = -INFINITY;
-        }
-        float f[8], mx = -INFINITY;
+        for (int c = 0; c < 4; ++c) {
+          float* s = two[c & 1];
+          wait_ld();
+          if (c < 3) tmem_ld32(t_s + 32 * (c + 1), reinterpret_cast<uint32_t*>(two[(c + 1) & 1]));
+          if (masked) {
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          f[g] = __shfl_sync(0xffffffffu, my_sk, g) * down;
-          float y = s[16 * g];
+            for (int j = 0; j < 32; ++j)
+              if (at + 32 * c + j >= vis || (bad_groups >> (2 * c + (j >> 4)) & 1)) s[j] = -INFINITY;
+          }
+          const float4 g0 = s_groups[warp][2 * c], g1 = s_groups[warp][2 * c + 1];
+          const float f0 = g0.x * down, f1 = g1.x * down;
+          uint32_t p[16];
+          float sum0, sum1;
+          // With the maximum so far; a row of which some P would not fit in fp16 shows
+          // in its sums, takes its new maximum and goes again.
+          for (int go = 0;; ++go) {
+            const float a0 = g0.y - m, a1 = g1.y - m;
+            float2 x0 = make_float2(0.f, 0.f), x1 = x0;
 #pragma unroll
-          for (int c = 1; c < 16; ++c) y = fmaxf(y, s[16 * g + c]);
-          mx = fmaxf(mx, y * f[g]);
-        }
-        const bool grow = mx > m + kStep;
-        if (__any_sync(0xffffffffu, grow) || moved != 0.f) {
-          const float u = grow ? mx : m;
-          const float el = ex2(m - u);
-          const float e = ex2(m - u + moved);
-          m = u;
-          l *= el;
-          if (i > 0) {
-            uint32_t o[32];
+            for (int j = 0; j < 16; j += 2) {
+              float2 y0 = fma2(make_float2(s[j], s[j + 1]), make_float2(f0, f0), make_float2(a0, a0));
+              float2 y1 = fma2(make_float2(s[16 + j], s[17 + j]), make_float2(f1, f1), make_float2(a1, a1));
+              y0.x = ex2(y0.x);
+              y0.y = ex2(y0.y);
+              y1.x = ex2(y1.x);
+              y1.y = ex2(y1.y);
+              x0 = add2(x0, y0);
+              x1 = add2(x1, y1);
+              p[j / 2] = pack_half2(y0.x, y0.y);
+              p[8 + j / 2] = pack_half2(y1.x, y1.y);
+            }
+            sum0 = x0.x + x0.y;
+            sum1 = x1.x + x1.y;
+            const bool over = !(fmaxf(sum0, sum1) <= kMost && sum0 + sum1 >= 0.f);   // NaN too
+            if (go || !__any_sync(0xffffffffu, over)) break;
+            float mx = -INFINITY, my = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              mx = fmaxf(mx, s[j]);
+              my = fmaxf(my, s[16 + j]);
+            }
+            const float u = over ? fmaxf(m, fmaxf(mx * f0, my * f1)) : m;
+            const float e = ex2(m - u);
+            m = u;
+            l *= e;
+            sums *= e;
+            by_o *= e;
+            wait_st();
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32(t_o + 32 * c, o);
+            for (int d = 0; d < c; ++d) {   // the P of this step that are there already
+              uint32_t q[16];
+              tmem_ld16(t_s + 16 * d, q);
               wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * e);
-              tmem_st32(t_o + 32 * c, o);
+              for (int j = 0; j < 16; ++j) {
+                const float2 y = half2_to_float2(q[j]);
+                q[j] = pack_half2(y.x * e, y.y * e);
+              }
+              tmem_st16(t_s + 16 * d, q);
             }
           }
+          sums = fmaf(sum0, g0.z, sums);
+          sums = fmaf(sum1, g1.z, sums);
+          tmem_st16(t_s + 16 * c, p);
         }
-        uint32_t p[64];
+        l += sums;
+        if (i > 0 && __any_sync(0xffffffffu, by_o != 1.f)) {
+          uint32_t o[32];
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(t_o + 32 * c, o);
+            wait_ld();
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          // log2(8 s_v / 2^sigma); below -100 the group's values vanish next to the
-          // others', and its weights still count
-          const float lv = fmaxf(__shfl_sync(0xffffffffu, my_lv, g) - sigma + 3.f, -100.f);
-          const float add = lv - m;
-          float sum = 0.f;
-#pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            const float p0 = ex2(fmaf(s[16 * g + c], f[g], add)), p1 = ex2(fmaf(s[16 * g + c + 1], f[g], add));
-            sum += p0 + p1;
-            p[8 * g + c / 2] = pack_half2(p0, p1);
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by_o);
+            tmem_st32(t_o + 32 * c, o);
           }
-          l = fmaf(sum, ex2(-lv), l);
         }
-        tmem_st32(t_s, p);
-        tmem_st32(t_s + 32, p + 32);
         wait_st();
         fence_before();
         __syncwarp();
@@ -403,22 +494,26 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       }
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;\n");
     // 32 positions a warp and step: 8 loads of 16 codes a lane for the keys, 8 for the values
     const int cw = warp - 8, rs = lane >> 2, cc = lane & 3;
-    auto load = [&](int i, int kv, uint4* x) {
+    // block ids of the warp's two groups of 16 positions (-1: behind the end)
+    auto blocks = [&](int i) {
+      const int g16 = (w.tile0 + i) * 8 + 2 * cw;
+      return make_int2(ldg_or(table + (g16 >> shift), i < tiles && g16 * 16 < w.limit, -1),
+                       ldg_or(table + ((g16 + 1) >> shift), i < tiles && g16 * 16 + 16 < w.limit, -1));
+    };
+    auto load = [&](int i, int2 id, int kv, uint4* x) {
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {   // 16 positions of one block each
+      for (int half = 0; half < 2; ++half) {
         const int g16 = (w.tile0 + i) * 8 + 2 * cw + half;
-        int blk = -1;
-        if (i < tiles && g16 * 16 < w.limit) blk = ld_dep_s32(table + (g16 >> shift));
+        const int blk = half ? id.y : id.x;
         const bool good = a.c.good(blk);
         const uint8_t* src = a.c.tile(good ? blk : 0, w.h, g16) + kv * kB8HalfBytes;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = 8 * (k >> 1) + rs, c = 4 * (k & 1) + cc;
-          x[4 * half + k] = make_uint4(0, 0, 0, 0);
-          if (good && g16 * 16 + row < w.limit) x[4 * half + k] = ld_dep_u32x4(src + row * kB8D + ((c ^ (row & 7)) << 4));
+          x[4 * half + k] = ld_or_zero4(src + row * kB8D + ((c ^ (row & 7)) << 4), good && g16 * 16 + row < w.limit);
         }
       }
     };
@@ -430,8 +525,9 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       }
     };
     uint4 x[8], y[8];
-    load(0, 0, x);
-    load(0, 1, y);
+    int2 id = blocks(0), id_next = blocks(1);   // a step's ids are there before its codes are asked for
+    load(0, id, 0, x);
+    load(0, id, 1, y);
     bool ok = true;
     for (int i = 0; i < tiles && ok; ++i) {
       const int st = i & 1;
@@ -441,55 +537,70 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       fence_smem_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kKFull0 + st));
-      load(i + 1, 0, x);
+      id = id_next;
+      id_next = blocks(i + 2);
+      load(i + 1, id, 0, x);
       if (!(ok = warp_wait(kVEmpty0 + st, free_phase))) break;
       store(base + kOffV + st * kTileOp, y);
       fence_smem_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kVFull0 + st));
-      load(i + 1, 1, y);
+      load(i + 1, id, 1, y);
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
-    if (warp == 12 && lane == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+    if (warp == 12) {
+      // The whole warp walks the steps, so that descriptors and addresses stay in
+      // uniform registers (issued from a branch that one lane takes, a product cost
+      // 75 to 200 cycles of moves); one lane, always the same, issues.
+      const bool leader = elect_one();
       auto qk = [&](int t, int st) {
-        const uint32_t q_at = base + t * kTileOp, k_at = base + kOffK + st * kTileOp;
+        const uint64_t q_at = desc_k_major(base + t * kTileOp), k_at = desc_k_major(base + kOffK + st * kTileOp);
+        const uint32_t d = tmem + kColS + t * 128;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint32_t off = (k >> 2) * kHalfOp + (k & 3) * 32;
-          mma_ss(tmem + kColS + t * 128, desc_k_major(q_at + off), desc_k_major(k_at + off), kIdescQK, k > 0);
+          const uint64_t off = ((k >> 2) * kHalfOp + (k & 3) * 32) >> 4;
+          mma_ss(d, q_at + off, k_at + off, kIdescQK, k > 0);
         }
         mma_commit(bar(kSFull0 + t));
       };
-      bool ok = wait(kQFull, 0) && wait(kKFull0, 0);
+      bool ok = warp_wait(kQFull, 0) && warp_wait(kKFull0, 0);
       if (ok) {
         fence_after();
-        for (int t = 0; t < halves; ++t) qk(t, 0);
-        mma_commit(bar(kKEmpty0));
+        if (leader) {
+          for (int t = 0; t < halves; ++t) qk(t, 0);
+          mma_commit(bar(kKEmpty0));
+        }
+        __syncwarp();
       }
       for (int i = 0; i < tiles && ok; ++i) {
         const int st = i & 1, nst = st ^ 1;
         const bool more = i + 1 < tiles;
-        for (int t = 0; t < halves && ok; ++t) {
-          ok = wait(kPFull0 + t, i & 1);
-          if (ok && t == 0) ok = wait(kVFull0 + st, (i >> 1) & 1);
-          if (!ok) break;
+        for (int t = 0; t < halves; ++t) {
+          if (!(ok = warp_wait(kPFull0 + t, i & 1))) break;
+          if (t == 0 && !(ok = warp_wait(kVFull0 + st, (i >> 1) & 1))) break;
           fence_after();
-          const uint32_t v_at = base + kOffV + st * kTileOp;
+          if (leader) {
+            const uint64_t v_at = desc_mn_major(base + kOffV + st * kTileOp);
+            const uint32_t d = tmem + kColO + t * 128, p = tmem + kColS + t * 128;
+            mma_ts(d, p, v_at, kIdescPV, i > 0);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tmem + kColO + t * 128, tmem + kColS + t * 128 + 8 * k, desc_mn_major(v_at + 2048 * k), kIdescPV, i > 0 || k > 0);
-          if (more) {
-            if (t == 0 && !(ok = wait(kKFull0 + nst, ((i + 1) >> 1) & 1))) break;
-            fence_after();
-            qk(t, nst);
-          } else {
-            mma_commit(bar(kODone0 + t));
+            for (int k = 1; k < 8; ++k) mma_ts(d, p + 8 * k, v_at + (2048 >> 4) * k, kIdescPV, true);
+            if (!more) mma_commit(bar(kODone0 + t));
           }
-        }
-        if (ok && more) {
-          mma_commit(bar(kVEmpty0 + st));
-          mma_commit(bar(kKEmpty0 + nst));
+          __syncwarp();
+          if (more) {
+            if (t == 0 && !(ok = warp_wait(kKFull0 + nst, ((i + 1) >> 1) & 1))) break;
+            fence_after();
+            if (leader) {
+              qk(t, nst);
+              if (t + 1 == halves) {
+                mma_commit(bar(kVEmpty0 + st));
+                mma_commit(bar(kKEmpty0 + nst));
+              }
+            }
+            __syncwarp();
+          }
         }
       }
     }

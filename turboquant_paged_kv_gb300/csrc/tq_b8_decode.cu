@@ -4,7 +4,8 @@
 //   out = sum_p softmax_p(scale s_k(p) q . k_p) s_v(p) v_p
 //
 // Work split. The 16-position tiles of all (query row, KV head) pairs form one
-// line, cut evenly over the warps of a grid of one CTA per SM. A warp writes,
+// line, cut evenly over the warps of a grid of one CTA per SM (neighbouring
+// parts to different SMs; with fewer tiles than warps, a tile each). A warp writes,
 // for every pair that it touches, one partial record (its normalised output
 // and log-sum-exp for the pair's query heads) at index pair + warp, unique as
 // both run upwards; a second kernel merges a pair's records by their
@@ -158,11 +159,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
   const int g = lane >> 2, t = lane & 3;
   if (!a.early_indices) grid_dep_wait();
 
-  const long long wid = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long wid = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
   long long total, before;
   bool too_long;
   count_tiles(a, 0, lane, &total, &before, &too_long);
-  const long long x0 = total * wid / a.warps, x1 = total * (wid + 1) / a.warps;
+  const long long nw = min(static_cast<long long>(a.warps), total);   // warps with work
+  const long long x0 = wid < nw ? total * wid / nw : 0, x1 = wid < nw ? total * (wid + 1) / nw : 0;
   int todo = static_cast<int>(x1 - x0);
   Place put = {}, get = {};   // next tile to load, next tile to use
   if (todo > 0) put = find_tile(a, x0, lane);
@@ -440,8 +442,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) b8_merge_kernel(const B8Spli
     if (warp == 0) write4<TO>(out, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
-  // owners of the pair's first and last tile: warp w owns [total w / warps, total (w + 1) / warps)
-  const long long nw = a.warps;
+  // owners of the pair's first and last tile: warp w owns [total w / nw, total (w + 1) / nw)
+  const long long nw = min(static_cast<long long>(a.warps), total);
   const long long w0 = ((x0 + 1) * nw - 1) / total, w1 = ((x0 + tiles) * nw - 1) / total;
   const long long pair = static_cast<long long>(row) * a.n_kv + h;
   float m = -INFINITY, l = 0.f;
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) b8_merge_kernel(const B8Spli
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const long long v = w + i * kMergeWarps;
-      const bool ok = v <= w1 && (total >= nw || total * v / nw != total * (v + 1) / nw);   // a warp without tiles has no record
+      const bool ok = v <= w1;
       const long long rec = (pair + v) * a.group + gg;
       lse[i] = ok ? ld_dep_f32(a.rec_lse + rec) : -INFINITY;
       x[i] = ok ? ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kB8D) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
