@@ -147,7 +147,11 @@ def test_continue_refusals(tq):
     assert cont(cfg=tq.make_config("int8_blk", 32, 2)) == _abi.TQ_ERR_UNSUPPORTED
     for bad in (dict(q=ODD), dict(out=ODD), dict(ws=ODD), dict(cache=ODD), dict(qs=ODD4), dict(lens=ODD4)):
         assert cont(**bad) == _abi.TQ_ERR_MISALIGNED, bad
-    assert cont(size=16) == _abi.TQ_ERR_WORKSPACE_TOO_SMALL
+    assert cont(size=0) == _abi.TQ_ERR_WORKSPACE_TOO_SMALL
+    # one chunk over a long history is split over CTAs: records of d + 1 floats a query head and part
+    split = tq.tq_b8_continue_workspace_size(base, 1, 10, 10, 4096)
+    assert split % 16 == 0 and split // (10 * 24 * 129 * 4) >= 2
+    assert cont(batch=1, mql=10, max_len=4096, size=split - 16) == _abi.TQ_ERR_WORKSPACE_TOO_SMALL
     assert tq.tq_b8_continue_workspace_size(base, -1, 10, 8, 64) == 0
 
 

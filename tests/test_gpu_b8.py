@@ -489,6 +489,23 @@ def test_continue_rows_without_positions_and_padding(tq, q_len):
     assert not got[q_len - 1].any() and got[q_len - 2].any() and np.all(got[starts[-1]:] == 123.0)
 
 
+@pytest.mark.parametrize("hist,dtype", [(20, "bf16"), (2000, "bf16"), (20, "f32")])
+def test_continue_output_on_16_bytes(tq, hist, dtype):
+    """out and workspace may lie on any 16 bytes (whole and split histories)."""
+    c = Case(tq, "int8_blk", 32, 4, 1, [hist + 40], seed=44).fill([hist + 40])
+    cache, table, lens = c.gpu()
+    q = c.draw(40, 4)
+    n = 40 * 4 * 128
+    room = torch.empty(n + 16, dtype=DT[dtype], device="cuda")
+    ws = torch.empty(tq.tq_b8_continue_workspace_size(c.cfg, 1, 40, 40, hist + 40) + 16, dtype=torch.uint8, device="cuda")
+    off = 16 // room.element_size()
+    assert room.data_ptr() % 32 == 0 and ws.data_ptr() % 32 == 0
+    out = room[off:off + n].view(40, 4, 128)
+    starts = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
+    tq.tq_b8_continue(c.cfg, q.cuda(), starts, 40, cache, table, lens, hist + 40, out, ws[16:])
+    check_continue(c, q, out.float().cpu().numpy().astype(np.float64), [0, 40], [hist + 40], dtype, rows=6)
+
+
 @pytest.mark.parametrize("q_len", [4, 140])
 def test_continue_device_errors(tq, q_len):
     c = Case(tq, "e4m3_blk", 16, 4, 1, [200], seed=41).fill([200])

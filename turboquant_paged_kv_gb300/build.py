@@ -42,8 +42,7 @@ def _deps():
     return _sources() + [os.path.join(CSRC, "tq_internal.h"), os.path.join(CSRC, "tq_launch.cuh"),
                          os.path.join(CSRC, "tq_vec.cuh"), os.path.join(CSRC, "tq_attn.cuh"),
                          os.path.join(CSRC, "tq_prod.cuh"), os.path.join(CSRC, "tq_store.cuh"),
-                         os.path.join(CSRC, "tq_b8.cuh"), os.path.join(CSRC, "tq_b8_decode.cuh"),
-                         os.path.join(CSRC, "tq_b8_chunk.cuh"),
+                         os.path.join(CSRC, "tq_b8.cuh"), os.path.join(CSRC, "tq_b8_chunk.cuh"),
                          os.path.join(INCLUDE, "tq.h"),
                          os.path.abspath(__file__)]
 

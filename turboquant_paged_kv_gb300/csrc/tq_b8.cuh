@@ -95,6 +95,23 @@ __device__ __forceinline__ uint32_t floats_to_codes(float a, float b, float c, f
   }
 }
 
+// *p where pred, else zeros: loads into preset registers, so that nothing waits
+// for the value here (a select on what was loaded would).
+__device__ __forceinline__ uint2 ld_or_zero2(const void* p, bool pred) {
+  uint2 v = make_uint2(0u, 0u);
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %3, 0;\n @q ld.global.cg.v2.b32 {%0, %1}, [%2];\n}\n"
+               : "+r"(v.x), "+r"(v.y)
+               : "l"(p), "r"(static_cast<unsigned>(pred)));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_or_zero4(const void* p, bool pred) {
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %5, 0;\n @q ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+               : "l"(p), "r"(static_cast<unsigned>(pred)));
+  return v;
+}
+
 __device__ __forceinline__ void b8_flag(unsigned int* status, unsigned int bit) {
   if (status) atomicOr(status, bit);
 }

@@ -42,7 +42,7 @@ __device__ __forceinline__ float2 pair_to_floats(uint32_t w) {
 __device__ __forceinline__ float tame(float y, float limit) { return isnan(y) ? 0.f : fminf(fmaxf(y, -limit), limit); }
 
 template <typename T, bool INT8>
-__global__ void __launch_bounds__(kThreads) b8_store_kernel(const StoreArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) b8_store_kernel(const StoreArgs a) {
   constexpr float kLimit = INT8 ? 127.f : 448.f;
   constexpr uint32_t kInf = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
   __shared__ uint32_t s_max[kThreads / 32];
@@ -70,17 +70,10 @@ __global__ void __launch_bounds__(kThreads) b8_store_kernel(const StoreArgs a) {
   const int j = (lo >> a.c.log2_bs) + jj;
   const long long p0 = static_cast<long long>(j) << a.c.log2_bs;   // position of the block's row 0
   bool active = p0 < end;
-  int blk = -1;
-  if (active) {
-    blk = ld_dep_s32(a.block_table + static_cast<long long>(b) * a.c.bt_stride + j);
-    if (!a.c.good(blk)) {
-      active = false;
-      if (lane == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
-    }
-  }
+  int blk = -1;   // asked for now, looked at after the rows have been asked for
+  if (active) blk = ld_dep_s32(a.block_table + static_cast<long long>(b) * a.c.bt_stride + j);
   const int first = static_cast<int>(max(static_cast<long long>(lo) - p0, 0ll));   // rows [first, last) are new
-  const int last = active ? static_cast<int>(min(static_cast<long long>(end) - p0, 1ll << a.c.log2_bs)) : 0;
-  const bool held = active && first > 0;
+  const int last = static_cast<int>(min(max(static_cast<long long>(end) - p0, 0ll), 1ll << a.c.log2_bs));
 
   // this warp's rows: 16 (warp's place in the unit) .. + 15, lane: row parity and 8 coordinates
   const int c8 = lane & 15;
@@ -93,9 +86,13 @@ __global__ void __launch_bounds__(kThreads) b8_store_kernel(const StoreArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 2 * i;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r >= first && r < last) x[i] = ld_dep_u32x4(src + r * stride);
+    x[i] = ld_or_zero4(src + r * stride, r >= first && r < last);
   }
+  if (active && !a.c.good(blk)) {
+    active = false;
+    if (lane == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
+  }
+  const bool held = active && first > 0;
   uint8_t* base = const_cast<uint8_t*>(a.c.base);
   float* scale_at = nullptr;
   float s_old = 0.f;

@@ -142,23 +142,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
-// *p where pred, else zeros: loads into preset registers, so that nothing waits
-// for the value here (a select on what was loaded would).
-__device__ __forceinline__ uint2 ld_or_zero2(const void* p, bool pred) {
-  uint2 v = make_uint2(0u, 0u);
-  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %3, 0;\n @q ld.global.cg.v2.b32 {%0, %1}, [%2];\n}\n"
-               : "+r"(v.x), "+r"(v.y)
-               : "l"(p), "r"(static_cast<unsigned>(pred)));
-  return v;
-}
-__device__ __forceinline__ uint4 ld_or_zero4(const void* p, bool pred) {
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  asm volatile("{\n .reg .pred q;\n setp.ne.u32 q, %5, 0;\n @q ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
-               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
-               : "l"(p), "r"(static_cast<unsigned>(pred)));
-  return v;
-}
-
 template <typename TO>
 __device__ __forceinline__ void write4(TO* dst, float4 v) {
   if constexpr (std::is_same<TO, float>::value) {
@@ -171,13 +154,52 @@ __device__ __forceinline__ void write4(TO* dst, float4 v) {
   }
 }
 
-// Where a CTA stands.
+// 32 bytes, at once where the address allows it (one answer for the grid).
+__device__ __forceinline__ void store32(void* dst, const uint32_t* v, bool wide) {
+  if (!wide) {
+    static_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    return;
+  }
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+// 32 numbers of a row.
+template <typename TO>
+__device__ __forceinline__ void write32(TO* dst, const float* y, bool wide) {
+  if constexpr (std::is_same<TO, float>::value) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __float_as_uint(y[8 * i + j]);
+      store32(dst + 8 * i, v, wide);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (std::is_same<TO, __half>::value) {
+          v[j] = pack_half2(y[16 * i + 2 * j], y[16 * i + 2 * j + 1]);
+        } else {
+          const __nv_bfloat162 x = __floats2bfloat162_rn(y[16 * i + 2 * j], y[16 * i + 2 * j + 1]);
+          v[j] = *reinterpret_cast<const uint32_t*>(&x);
+        }
+      }
+      store32(dst + 16 * i, v, wide);
+    }
+  }
+}
+
+// What a CTA does.
 struct Work {
-  int seq, h, row0, rows_q;   // sequence, KV head, first query of the chunk that is served, how many are
-  int q0;                     // row of that query in q and out
-  int pos0;                   // its position (may be negative)
-  int limit;                  // positions that may be read
-  int tile0, tiles;           // steps of 128 positions: [tile0, tile0 + tiles)
+  int seq, h, z;        // sequence (-1: nothing), KV head, part of the history
+  int q0, rows;         // row of its first query in q and out; rows of A, its queries' heads
+  int pos0;             // position of that query (may be negative)
+  int limit;            // positions that may be read
+  int tile0, tiles;     // steps of 128 positions: [tile0, tile0 + tiles)
+  int zero0, zeros;     // queries that nobody serves
 };
 
 template <bool INT8>
@@ -198,67 +220,18 @@ template <typename TQ, typename TO, bool INT8>
 __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs a) {
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
+  __shared__ Work s_work;
   __shared__ float4 s_groups[8][8];   // each softmax warp's: the step's groups of 16 positions
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 1023u) & ~1023u;
   const uint32_t bars = base + kOffBar;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
-  grid_dep_wait();
-  grid_dep_launch();
-
-  // the latest queries of a chunk see the most: they go first
-  Work w;
-  const int per = kRows / a.group;   // queries of a CTA
-  const int x = blockIdx.x / a.splits, z = blockIdx.x - x * a.splits;
-  const int tile_q = static_cast<int>(gridDim.x) / a.splits - 1 - x;
-  w.h = blockIdx.y;
-  w.seq = blockIdx.z;
-  const int raw0 = ld_dep_s32(a.query_start + w.seq), raw1 = ld_dep_s32(a.query_start + w.seq + 1);
-  const int raw_len = max(ld_dep_s32(a.seq_lens + w.seq), 0);
-  const int qs = min(max(raw0, 0), a.total_q);
-  const int n = min(max(raw1, qs), a.total_q) - qs;
-  const int served = min(n, a.max_q_len);
-  w.limit = min(raw_len, min(a.max_seq_len, a.cap));
-  if (tile_q == 0 && z == 0 && w.h == 0 && threadIdx.x == 0 && n > 0 &&
-      (n > a.max_q_len || raw_len > min(a.max_seq_len, a.cap)))
-    b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
-  const int heads0 = w.h * a.group;
-  if (tile_q == 0 && z == 0 && n > served) {   // queries past max_q_len: zeros
-    const long long count = static_cast<long long>(n - served) * a.group * (kB8D / 4);
-    for (long long i = threadIdx.x; i < count; i += kThreads) {
-      const long long r = i / (kB8D / 4);
-      write4<TO>(static_cast<TO*>(a.out) + ((qs + served + r / a.group) * a.n_q + heads0 + r % a.group) * kB8D + 4 * (i % (kB8D / 4)),
-                 make_float4(0.f, 0.f, 0.f, 0.f));
-    }
-  }
-  w.row0 = tile_q * per;
-  w.rows_q = min(per, served - w.row0);
-  if (w.rows_q <= 0) return;
-  w.q0 = qs + w.row0;
-  w.pos0 = raw_len - n + w.row0;
-  const int seen = min(w.pos0 + w.rows_q, w.limit);   // positions that the last query sees
-  const int all_tiles = seen > 0 ? (seen + kCols - 1) / kCols : 0;
-  w.tile0 = min(z * a.split_tiles, all_tiles);
-  w.tiles = min(a.split_tiles, all_tiles - w.tile0);
-  const int rows = w.rows_q * a.group;
-  const int halves = rows > 128 ? 2 : 1;   // row tiles at work
-
-  if (w.tiles == 0) {   // nothing to see here
-    if (a.splits == 1) {
-      for (int i = threadIdx.x; i < rows * (kB8D / 4); i += kThreads) {
-        const int r = i / (kB8D / 4);
-        write4<TO>(static_cast<TO*>(a.out) + (static_cast<long long>(w.q0 + r / a.group) * a.n_q + heads0 + r % a.group) * kB8D + 4 * (i % (kB8D / 4)),
-                   make_float4(0.f, 0.f, 0.f, 0.f));
-      }
-    } else if (threadIdx.x < rows) {
-      const int r = threadIdx.x;
-      a.rec_lse[(static_cast<long long>(w.q0 + r / a.group) * a.n_q + heads0 + r % a.group) * a.splits + z] = -INFINITY;
-    }
-    return;
-  }
-
-  if (threadIdx.x == 0) {
-    mbar_init(bar(kQFull), 4 * halves);
+  // Barriers and tensor memory need nothing of the kernel before; one warp finds the
+  // work meanwhile. CTAs: (tile of a chunk's queries, KV head, part of the history),
+  // the last fastest; sequence by sequence, and the latest queries of a chunk, which
+  // see the most, first.
+  if (threadIdx.x == 32) {
+    mbar_init(bar(kQFull), 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kKFull0 + i), 4);
       mbar_init(bar(kVFull0 + i), 4);
@@ -274,10 +247,91 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&s_tmem))) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
+  const int per = kRows / a.group;   // queries of a CTA
+  grid_dep_wait();
+  grid_dep_launch();
+  if (warp == 0) {
+    int x = blockIdx.x / a.splits;
+    const int z = blockIdx.x - x * a.splits, h = x % a.c.n_kv;
+    x /= a.c.n_kv;
+    int seq = -1, qs = 0, n = 0, tile_q = 0, raw_len = 0;
+    for (int b0 = 0; b0 < a.batch && seq < 0; b0 += 32) {   // 32 sequences at a time
+      const int b = b0 + lane;
+      const int at0 = min(max(ldg_or(a.query_start + b, b < a.batch, 0), 0), a.total_q);
+      const int at1 = min(max(ldg_or(a.query_start + b + 1, b < a.batch, 0), at0), a.total_q);
+      const int len = ldg_or(a.seq_lens + b, b < a.batch, 0);
+      const int mine = (min(at1 - at0, a.max_q_len) + per - 1) / per;
+      int inc = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, x < inc);
+      if (here) {
+        const int src = __ffs(here) - 1;
+        seq = b0 + src;
+        qs = __shfl_sync(0xffffffffu, at0, src);
+        n = __shfl_sync(0xffffffffu, at1, src) - qs;
+        raw_len = max(__shfl_sync(0xffffffffu, len, src), 0);
+        tile_q = __shfl_sync(0xffffffffu, inc, src) - 1 - x;
+      }
+      x -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      Work w;
+      w.seq = seq;
+      w.h = h;
+      w.z = z;
+      w.limit = min(raw_len, min(a.max_seq_len, a.cap));
+      const int served = min(n, a.max_q_len);
+      w.zero0 = qs + served;
+      w.zeros = tile_q == 0 && z == 0 ? n - served : 0;   // queries past max_q_len
+      if (tile_q == 0 && z == 0 && h == 0 && n > 0 && (n > a.max_q_len || raw_len > min(a.max_seq_len, a.cap)))
+        b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
+      w.q0 = qs + tile_q * per;
+      w.rows = min(per, served - tile_q * per) * a.group;
+      w.pos0 = raw_len - n + tile_q * per;
+      const int seen = min(w.pos0 + min(per, served - tile_q * per), w.limit);   // positions that the last query sees
+      const int all_tiles = seen > 0 ? (seen + kCols - 1) / kCols : 0;
+      w.tile0 = min(z * a.split_tiles, all_tiles);
+      w.tiles = min(a.split_tiles, all_tiles - w.tile0);
+      s_work = w;
+    }
+  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+  const Work w = s_work;
+  auto leave = [&]() {   // all of the CTA
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+  };
+  if (w.seq < 0) return leave();
+  const int heads0 = w.h * a.group, rows = w.rows, z = w.z;
+  const int halves = rows > 128 ? 2 : 1;   // row tiles at work
+  const unsigned by_group = (65536u + a.group - 1) / a.group;   // row / group for rows below 256, group <= 8
+  auto query_of = [&](int row) { return static_cast<int>(row * by_group >> 16); };
+  auto zero_rows = [&](int q0, int count) {   // `count` queries from q0 on, this KV head's part
+    const long long all = static_cast<long long>(count) * a.group * (kB8D / 4);
+    for (long long i = threadIdx.x; i < all; i += kThreads) {
+      const long long r = i / (kB8D / 4);
+      write4<TO>(static_cast<TO*>(a.out) + ((q0 + r / a.group) * a.n_q + heads0 + r % a.group) * kB8D + 4 * (i % (kB8D / 4)),
+                 make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+  };
+  if (w.zeros) zero_rows(w.zero0, w.zeros);
+  if (w.tiles == 0) {   // nothing to see here
+    if (a.splits == 1) {
+      zero_rows(w.q0, rows / a.group);
+    } else if (threadIdx.x < rows) {
+      const int r = threadIdx.x;
+      a.rec_lse[(static_cast<long long>(w.q0 + r / a.group) * a.n_q + heads0 + r % a.group) * a.splits + z] = -INFINITY;
+    }
+    return leave();
+  }
   auto wait = [&](int b, uint32_t parity) {   // false: give up
     if (mbar_wait(bar(b), parity)) return true;
     b8_flag(a.status, TQ_DEV_TIMEOUT);
@@ -291,23 +345,35 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 152;\n");
     const int t = warp >> 2;
-    if (t < halves) {
-      // this thread's row: a query head; its scaled fp16 copy becomes a row of A
-      const int r = threadIdx.x;   // 0 .. 255
+    if (t >= halves) {
+      if (lane == 0) mbar_arrive(bar(kQFull));
+    } else {
+      // The queries of 32 rows (a row: a query head) go to their places in A as they
+      // are, half a warp a row; then each row is scaled and rounded to fp16 in place, a
+      // thread a row.
+      const uint32_t a_at = base + t * kTileOp;
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int r = t * 128 + (warp & 3) * 32 + 2 * i + (lane >> 4), c = lane & 15;
+        const int qi = query_of(r), head = heads0 + r - qi * a.group;
+        const TQ* src = static_cast<const TQ*>(a.q) + (r < rows ? (w.q0 + qi) * a.q_stride + static_cast<long long>(head) * kB8D + 8 * c : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(a_at + (r & 127) * 128 + (c >> 3) * kHalfOp + (((c & 7) ^ (r & 7)) << 4)), "l"(src), "r"(r < rows ? 16 : 0) : "memory");
+      }
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
+      __syncwarp();
+      const int r = threadIdx.x;   // this thread's row, 0 .. 255
       const bool live = r < rows;
-      const int qi = r / a.group, head = heads0 + r - qi * a.group;
-      float down = 0.f;
+      const int qi = query_of(r), head = heads0 + r - qi * a.group;
+      float down;
       {
-        const uint32_t row_at = base + t * kTileOp + (r & 127) * 128;
-        const TQ* src = static_cast<const TQ*>(a.q) + (w.q0 + qi) * a.q_stride + static_cast<long long>(head) * kB8D;
-        uint4 v[16];
-        uint32_t m2 = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          v[i] = live ? ld_dep_u32x4(src + 8 * i) : make_uint4(0, 0, 0, 0);
-          m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
+        const uint32_t row_at = a_at + (r & 127) * 128;
+        uint32_t m = 0;
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          const uint4 v = lds128(row_at + (c >> 3) * kHalfOp + (((c & 7) ^ (r & 7)) << 4));
+          m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
         }
-        const uint32_t m = max(m2 & 0xffffu, m2 >> 16);
+        m = max(m & 0xffffu, m >> 16);
         float amax;
         if constexpr (std::is_same<TQ, __nv_bfloat16>::value) amax = __uint_as_float(m << 16);
         else amax = half2_to_float2(m).x;
@@ -315,9 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
         const int k = min(max(14 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), -112), 112);
         const float up = __uint_as_float(static_cast<uint32_t>(127 + k) << 23);
         down = a.qscale * __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t ws[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t at = row_at + (c >> 3) * kHalfOp + (((c & 7) ^ (r & 7)) << 4);
+          const uint4 v = lds128(at);
+          const uint32_t ws[4] = {v.x, v.y, v.z, v.w};
           uint32_t o[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -326,12 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
             else f = half2_to_float2(ws[j]);
             o[j] = pack_half2(f.x * up, f.y * up);
           }
-          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(row_at + (i >> 3) * kHalfOp + (((i & 7) ^ (r & 7)) << 4)), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(at), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]) : "memory");
         }
-        fence_smem_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kQFull));
       }
+      fence_smem_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kQFull));
       const int vis = live ? max(min(w.pos0 + qi + 1, w.limit), 0) : 0;   // positions that this row sees
       const int vis_least = __reduce_min_sync(0xffffffffu, live ? vis : 0x7fffffff);
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -472,22 +540,20 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       if (ok && warp_wait(kODone0 + t, 0)) {
         fence_after();
         const float scale = l > 0.f ? ex2(sigma - 3.f) / l : (l == 0.f ? 0.f : l);   // NaN stays
-        const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + head;
         const bool whole = a.splits == 1;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.rec_o)) & 31) == 0;
+        const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + head;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {   // 32 bytes a store: whole sectors, though a row a thread
           uint32_t o[32];
           tmem_ld32(t_o + 32 * c, o);
           wait_ld();
-          if (live) {
+          float y[32];
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              float4 y = make_float4(__uint_as_float(o[j]) * scale, __uint_as_float(o[j + 1]) * scale,
-                                     __uint_as_float(o[j + 2]) * scale, __uint_as_float(o[j + 3]) * scale);
-              if (l == 0.f) y = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (whole) write4<TO>(static_cast<TO*>(a.out) + orow * kB8D + 32 * c + j, y);
-              else *reinterpret_cast<float4*>(a.rec_o + (orow * a.splits + z) * kB8D + 32 * c + j) = y;
-            }
+          for (int j = 0; j < 32; ++j) y[j] = l == 0.f ? 0.f : __uint_as_float(o[j]) * scale;
+          if (live) {
+            if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kB8D + 32 * c, y, wide);
+            else write32<float>(a.rec_o + (orow * a.splits + z) * kB8D + 32 * c, y, wide);
           }
         }
         if (live && !whole) a.rec_lse[orow * a.splits + z] = l == 0.f ? -INFINITY : m + __log2f(l);
@@ -606,12 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
     }
     __syncwarp();
   }
-  fence_before();
-  __syncthreads();
-  fence_after();
-  if (warp == 12) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
-  }
+  leave();
 }
 
 // One warp per (query row, query head): merges the splits.
@@ -655,7 +716,7 @@ cudaError_t launch(const B8ChunkArgs& a, const B8ChunkPlan& p, cudaStream_t s) {
   auto* kernel = b8_chunk_kernel<TQ, TO, INT8>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(kernel, dim3(p.q_tiles * p.splits, a.c.n_kv, a.batch), dim3(kThreads), kSmem, s, a);
+  err = launch_pdl(kernel, dim3(static_cast<unsigned>(p.q_tiles * a.c.n_kv * p.splits)), dim3(kThreads), kSmem, s, a);
   if (err != cudaSuccess || p.splits == 1) return err;
   const long long rows = static_cast<long long>(a.total_q) * a.n_q;
   return launch_pdl(b8_chunk_merge_kernel<TO>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a);
@@ -680,11 +741,16 @@ B8ChunkPlan b8_chunk_plan(const tq_config* cfg, int batch, int total_q, int max_
   B8ChunkPlan p;
   const int per = kRows / (cfg->num_q_heads / cfg->num_kv_heads);
   const int longest = max_q_len < total_q ? max_q_len : total_q;
-  p.q_tiles = longest > 0 ? (longest + per - 1) / per : 1;
+  // tiles of queries: a full one for every `per` rows at most, and one more for every
+  // chunk; as many for every sequence as the longest chunk has at most
+  const long long most = static_cast<long long>(batch) * ((longest + per - 1) / per);
+  p.q_tiles = static_cast<long long>(total_q) / per + (batch < total_q ? batch : total_q);
+  if (p.q_tiles > most) p.q_tiles = most;
+  if (p.q_tiles < 1) p.q_tiles = 1;
   const int tiles = max_seq_len > 0 ? static_cast<int>((static_cast<long long>(max_seq_len) + kCols - 1) / kCols) : 1;
-  const long long ctas = static_cast<long long>(p.q_tiles) * cfg->num_kv_heads * batch;
+  const long long ctas = p.q_tiles * cfg->num_kv_heads;
   // fewer CTAs than SMs: the history is split, two steps a part at least
-  long long splits = ctas > 0 ? kSms / ctas : 1;
+  long long splits = kSms / ctas;
   if (splits > tiles / 2) splits = tiles / 2;
   if (splits > 32) splits = 32;
   if (splits < 1) splits = 1;

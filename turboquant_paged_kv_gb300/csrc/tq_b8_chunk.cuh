@@ -21,7 +21,8 @@ struct B8ChunkArgs {
 
 // How the history is split over CTAs, and the workspace that takes.
 struct B8ChunkPlan {
-  int q_tiles, splits, split_tiles;
+  long long q_tiles;   // at most
+  int splits, split_tiles;
   size_t workspace;
 };
 B8ChunkPlan b8_chunk_plan(const tq_config* cfg, int batch, int total_q, int max_q_len, int max_seq_len);

@@ -3,23 +3,6 @@
 #include <climits>
 
 #include "tq_b8_chunk.cuh"
-#include "tq_b8_decode.cuh"
-
-namespace tq {
-namespace {
-
-#ifndef TQ_B8_CHUNK_MIN
-#define TQ_B8_CHUNK_MIN 32
-#endif
-// Rows (queries x query heads of a KV head) of the longest chunk from which on
-// the tensor-core kernel serves the call.
-bool takes_chunk_kernel(const tq_config* cfg, int total_q, int max_q_len) {
-  const long long longest = max_q_len < total_q ? max_q_len : total_q;
-  return longest * (cfg->num_q_heads / cfg->num_kv_heads) >= TQ_B8_CHUNK_MIN;
-}
-
-}  // namespace
-}  // namespace tq
 
 extern "C" {
 
@@ -28,8 +11,7 @@ size_t tq_b8_continue_workspace_size(const tq_config* cfg, int batch, int total_
   tq_b8_layout L;
   if (make_b8_layout(cfg, &L) != TQ_OK || batch < 0 || total_q < 0 || max_q_len < 0 || max_seq_len < 0) return 0;
   if (b8_heads(cfg) != TQ_OK) return 0;
-  if (takes_chunk_kernel(cfg, total_q, max_q_len)) return b8_chunk_plan(cfg, batch, total_q, max_q_len, max_seq_len).workspace;
-  return b8_split_workspace(cfg, total_q);
+  return b8_chunk_plan(cfg, batch, total_q, max_q_len, max_seq_len).workspace;
 }
 
 tq_status tq_b8_continue(const tq_config* cfg, const void* q, long long q_stride, int q_dtype, const int* query_start,
@@ -53,37 +35,10 @@ tq_status tq_b8_continue(const tq_config* cfg, const void* q, long long q_stride
   if (workspace_bytes < tq_b8_continue_workspace_size(cfg, batch, total_q, max_q_len, max_seq_len))
     return TQ_ERR_WORKSPACE_TOO_SMALL;
   if (static_cast<long long>(total_q) * cfg->num_q_heads > INT_MAX) return TQ_ERR_UNSUPPORTED;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (takes_chunk_kernel(cfg, total_q, max_q_len)) {
-    if (batch > 65535) return TQ_ERR_UNSUPPORTED;
-    B8ChunkArgs c = {};
-    c.c = b8_cache(cfg, L, cache, num_blocks, bt_stride);
-    c.q = q;
-    c.q_stride = q_stride;
-    c.block_table = block_table;
-    c.seq_lens = seq_lens;
-    c.query_start = query_start;
-    c.status = dev_status;
-    c.out = out;
-    c.batch = batch;
-    c.total_q = total_q;
-    c.max_q_len = max_q_len;
-    c.n_q = cfg->num_q_heads;
-    c.group = cfg->num_q_heads / cfg->num_kv_heads;
-    c.max_seq_len = max_seq_len;
-    c.cap = b8_cap(cfg, bt_stride);
-    c.qscale = b8_qscale(scale);
-    const B8ChunkPlan p = b8_chunk_plan(cfg, batch, total_q, max_q_len, max_seq_len);
-    return b8_chunk_launch(c, p, L.is_int8, q_dtype, out_dtype, workspace, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
-  }
-  B8SplitArgs a = {};
-  a.cache = static_cast<const uint8_t*>(cache);
-  a.num_blocks = num_blocks;
-  a.block_bytes = L.block_bytes;
-  a.scale_off = L.scale_off;
-  a.n_kv = cfg->num_kv_heads;
-  a.log2_bs = b8_log2(cfg->block_size);
-  a.bt_stride = bt_stride;
+  const B8ChunkPlan p = b8_chunk_plan(cfg, batch, total_q, max_q_len, max_seq_len);
+  if (p.q_tiles * cfg->num_kv_heads * p.splits > INT_MAX) return TQ_ERR_UNSUPPORTED;
+  B8ChunkArgs a = {};
+  a.c = b8_cache(cfg, L, cache, num_blocks, bt_stride);
   a.q = q;
   a.q_stride = q_stride;
   a.block_table = block_table;
@@ -91,16 +46,15 @@ tq_status tq_b8_continue(const tq_config* cfg, const void* q, long long q_stride
   a.query_start = query_start;
   a.status = dev_status;
   a.out = out;
-  a.rows = total_q;
   a.batch = batch;
+  a.total_q = total_q;
+  a.max_q_len = max_q_len;
   a.n_q = cfg->num_q_heads;
   a.group = cfg->num_q_heads / cfg->num_kv_heads;
   a.max_seq_len = max_seq_len;
-  a.max_q_len = max_q_len;
   a.cap = b8_cap(cfg, bt_stride);
-  a.early_indices = (cfg->flags & TQ_FLAG_INDICES_READY) != 0;
   a.qscale = b8_qscale(scale);
-  const cudaError_t err = b8_split_launch(a, L.is_int8, q_dtype, out_dtype, workspace, s);
+  const cudaError_t err = b8_chunk_launch(a, p, L.is_int8, q_dtype, out_dtype, workspace, reinterpret_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 

@@ -3,7 +3,7 @@
 //
 //   out = sum_p softmax_p(scale s_k(p) q . k_p) s_v(p) v_p
 //
-// Work split. The 16-position tiles of all (query row, KV head) pairs form one
+// Work split. The 16-position tiles of all (sequence, KV head) pairs form one
 // line, cut evenly over the warps of a grid of one CTA per SM (neighbouring
 // parts to different SMs; with fewer tiles than warps, a tile each). A warp writes,
 // for every pair that it touches, one partial record (its normalised output
@@ -31,10 +31,25 @@
 #include <climits>
 
 #include "tq_attn.cuh"
-#include "tq_b8_decode.cuh"
+#include "tq_b8.cuh"
 
 namespace tq {
 namespace {
+
+struct B8SplitArgs {
+  const uint8_t* cache;
+  long long num_blocks, block_bytes;
+  int scale_off, n_kv, log2_bs, bt_stride;
+  const void* q;
+  long long q_stride;
+  const int *block_table, *seq_lens;
+  unsigned int* status;
+  void* out;
+  float *rec_o, *rec_lse;   // [records][group][d], [records][group] (log2 units)
+  int rows, n_q, group, max_seq_len, cap, warps;   // rows: sequences; warps: of the whole split grid
+  int early_indices;
+  float qscale;             // softmax scale * log2(e)
+};
 
 constexpr int kWarps = 12;         // a CTA
 constexpr int kStages = 4;         // tiles in a warp's ring
@@ -44,45 +59,24 @@ constexpr int kSmem = kWarps * kStages * (kB8TileBytes + 16);
 constexpr float kStep = 8.f;       // the running maximum moves in steps of at least this, log2 units
 static_assert(kB8MaxCtas * kWarps <= kMaxWarps, "workspace");
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+// (codes are read once: they leave L2 to the tables, queries and records)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "l"(policy) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
 
-// Row i of the line: its sequence and how many positions it sees.
-__device__ __forceinline__ void row_of(const B8SplitArgs& a, int i, int* seq, int* len, bool* too_long) {
-  const int limit = min(a.max_seq_len, a.cap);
-  *too_long = false;
-  if (!a.query_start) {
-    const int raw = ld_dep_s32(a.seq_lens + i);
-    *seq = i;
-    *len = min(max(raw, 0), limit);
-    *too_long = raw > limit;
-    return;
-  }
-  int lo = 0, hi = a.batch;   // the last sequence that starts at or before row i
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ld_dep_s32(a.query_start + mid) <= i) lo = mid;
-    else hi = mid;
-  }
-  const int q0 = ld_dep_s32(a.query_start + lo), q1 = ld_dep_s32(a.query_start + lo + 1);
-  *seq = lo;
-  *len = 0;
-  if (i < q0 || i >= q1) return;   // behind the last sequence
-  const int raw = ld_dep_s32(a.seq_lens + lo);
-  *too_long = raw > limit || i - q0 >= a.max_q_len;
-  if (i - q0 < a.max_q_len) *len = static_cast<int>(min(max(static_cast<long long>(raw) - q1 + i + 1, 0ll), static_cast<long long>(limit)));
+// How many positions sequence i sees.
+__device__ __forceinline__ int length_of(const B8SplitArgs& a, int i, bool* too_long) {
+  const int limit = min(a.max_seq_len, a.cap), raw = ld_dep_s32(a.seq_lens + i);
+  *too_long = raw > limit;
+  return min(max(raw, 0), limit);
 }
 
 // A place in the line.
 struct Place {
-  int row, h, t, tiles, len, seq;
+  int row, h, t, tiles, len;
 };
 __device__ __forceinline__ void next_tile(const B8SplitArgs& a, Place& p) {
   if (++p.t < p.tiles) return;
@@ -92,62 +86,70 @@ __device__ __forceinline__ void next_tile(const B8SplitArgs& a, Place& p) {
   bool too_long;
   do {
     if (++p.row >= a.rows) return;
-    row_of(a, p.row, &p.seq, &p.len, &too_long);
+    p.len = length_of(a, p.row, &too_long);
     p.tiles = (p.len + kB8Rows - 1) / kB8Rows;
   } while (p.tiles == 0);
 }
 
-// Tiles of all rows, and before row `upto`, times n_kv (a warp's lanes together).
-__device__ __forceinline__ void count_tiles(const B8SplitArgs& a, int upto, int lane, long long* total, long long* before, bool* too_long) {
+// The rows of a group of 32, one a lane.
+struct Rows {
+  int len, tiles;
+  bool too_long;
+};
+__device__ __forceinline__ Rows rows_of(const B8SplitArgs& a, int i) {
+  Rows r = {0, 0, false};
+  if (i < a.rows) r.len = length_of(a, i, &r.too_long);
+  r.tiles = (r.len + kB8Rows - 1) / kB8Rows;
+  return r;
+}
+
+// Tiles of all rows, and before row `upto`, times n_kv (a warp's lanes
+// together); `first` keeps the first 32 rows.
+__device__ __forceinline__ void count_tiles(const B8SplitArgs& a, int upto, int lane, long long* total, long long* before,
+                                            bool* too_long, Rows* first) {
   long long all = 0, bf = 0;
   bool tl = false;
   for (int i0 = 0; i0 < a.rows; i0 += 32) {
-    const int i = i0 + lane;
-    int seq, len = 0;
-    bool t = false;
-    if (i < a.rows) row_of(a, i, &seq, &len, &t);
-    tl |= t;
-    const int nt = (len + kB8Rows - 1) / kB8Rows;
-    all += nt;
-    bf += i < upto ? nt : 0;
-  }
-  for (int o = 1; o < 32; o <<= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    bf += __shfl_xor_sync(0xffffffffu, bf, o);
+    const Rows r = rows_of(a, i0 + lane);
+    if (i0 == 0) *first = r;
+    tl |= r.too_long;
+    all += __reduce_add_sync(0xffffffffu, r.tiles);
+    bf += __reduce_add_sync(0xffffffffu, i0 + lane < upto ? r.tiles : 0);
   }
   *total = all * a.n_kv;
   *before = bf * a.n_kv;
   *too_long = __any_sync(0xffffffffu, tl);
 }
 
+// x / y; most lines are short enough for 32 bits.
+__device__ __forceinline__ long long divide(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
 // The place of tile x of the line (x < total).
-__device__ __forceinline__ Place find_tile(const B8SplitArgs& a, long long x, int lane) {
+__device__ __forceinline__ Place find_tile(const B8SplitArgs& a, long long x, int lane, const Rows& first) {
   Place p = {};
   long long before = 0;
   for (int i0 = 0; i0 < a.rows; i0 += 32) {
-    const int i = i0 + lane;
-    int seq = 0, len = 0;
-    bool t;
-    if (i < a.rows) row_of(a, i, &seq, &len, &t);
-    const int nt = (len + kB8Rows - 1) / kB8Rows;
-    long long inc = nt;
+    const Rows r = i0 == 0 ? first : rows_of(a, i0 + lane);
+    int inc = r.tiles;   // a group of 32 rows holds less than 2^32 tiles
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const unsigned m = __ballot_sync(0xffffffffu, x < (before + inc) * a.n_kv);
+    const unsigned m = __ballot_sync(0xffffffffu, x < (before + static_cast<unsigned>(inc)) * a.n_kv);
     if (m) {
       const int src = __ffs(m) - 1;
-      const long long rest = x - (before + __shfl_sync(0xffffffffu, inc - nt, src)) * a.n_kv;
+      const long long rest = x - (before + static_cast<unsigned>(__shfl_sync(0xffffffffu, inc - r.tiles, src))) * a.n_kv;
       p.row = i0 + src;
-      p.tiles = __shfl_sync(0xffffffffu, nt, src);
-      p.len = __shfl_sync(0xffffffffu, len, src);
-      p.seq = __shfl_sync(0xffffffffu, seq, src);
-      p.h = static_cast<int>(rest / p.tiles);
+      p.tiles = __shfl_sync(0xffffffffu, r.tiles, src);
+      p.len = __shfl_sync(0xffffffffu, r.len, src);
+      p.h = static_cast<int>(divide(rest, p.tiles));
       p.t = static_cast<int>(rest - static_cast<long long>(p.h) * p.tiles);
       return p;
     }
-    before += __shfl_sync(0xffffffffu, inc, 31);
+    before += static_cast<unsigned>(__shfl_sync(0xffffffffu, inc, 31));
   }
   return p;
 }
@@ -162,12 +164,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
   const long long wid = static_cast<long long>(warp) * gridDim.x + blockIdx.x;
   long long total, before;
   bool too_long;
-  count_tiles(a, 0, lane, &total, &before, &too_long);
+  Rows first;
+  count_tiles(a, 0, lane, &total, &before, &too_long, &first);
   const long long nw = min(static_cast<long long>(a.warps), total);   // warps with work
-  const long long x0 = wid < nw ? total * wid / nw : 0, x1 = wid < nw ? total * (wid + 1) / nw : 0;
+  const long long x0 = wid < nw ? divide(total * wid, nw) : 0, x1 = wid < nw ? divide(total * (wid + 1), nw) : 0;
   int todo = static_cast<int>(x1 - x0);
   Place put = {}, get = {};   // next tile to load, next tile to use
-  if (todo > 0) put = find_tile(a, x0, lane);
+  if (todo > 0) put = find_tile(a, x0, lane, first);
   get = put;
   if (a.early_indices) grid_dep_wait();
   grid_dep_launch();
@@ -177,10 +180,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
   const B8Cache c = {a.cache, a.num_blocks, a.block_bytes, a.scale_off, a.n_kv, a.log2_bs, a.bt_stride};
   const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(s_ring)) + warp * kStages * kB8TileBytes;
   const uint32_t tail = static_cast<uint32_t>(__cvta_generic_to_shared(s_ring)) + kWarps * kStages * kB8TileBytes +
-                        warp * kStages * 16;   // a stage's scales: key, value (negative: bad block)
+                        warp * kStages * 16;   // a stage's scales: key, value of two heads (negative: bad block)
+  const uint64_t policy = evict_first_policy();
   int to_put = todo, put_stage = 0;
   auto table_at = [&](const Place& p) {
-    return a.block_table + static_cast<long long>(p.seq) * a.bt_stride + (p.t >> (a.log2_bs - 4));
+    return a.block_table + static_cast<long long>(p.row) * a.bt_stride + (p.t >> (a.log2_bs - 4));
   };
   int blk = ld_dep_s32(table_at(put));
   auto put_one = [&]() {
@@ -189,10 +193,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
       if (c.good(blk)) {
         const uint8_t* src = c.tile(blk, put.h, put.t) + lane * 16;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) cp_async16(dst + i * 512, src + i * 512);
-        if (lane == 0) cp_async8(sdst, c.scales(blk, put.h));
+        for (int i = 0; i < 8; ++i) cp_async16(dst + i * 512, src + i * 512, policy);
+        // the scales of heads h & ~1, h | 1: 16 bytes, since only those go past L1, which may
+        // hold what stood there before the kernel in front of this one
+        if (lane == 0) cp_async16(sdst, c.scales(blk, put.h & ~1), policy);
       } else if (lane == 0) {
         sts64(sdst, make_uint2(0xbf800000u, 0xbf800000u));
+        sts64(sdst + 8, make_uint2(0xbf800000u, 0xbf800000u));
         b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
       }
       if (--to_put > 0) {
@@ -217,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
     __syncwarp();
     put_one();
     const uint32_t kt = ring + stage * kB8TileBytes;
-    const uint2 sw = lds64(tail + stage * 16);
+    const uint2 sw = lds64(tail + stage * 16 + 8 * (get.h & 1));
     const float s_k = __uint_as_float(sw.x), s_v = __uint_as_float(sw.y);
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
@@ -427,24 +434,26 @@ __global__ void __launch_bounds__(kMergeWarps * 32) b8_merge_kernel(const B8Spli
   // launch go only after its own wait: they may be read before this one's
   long long total, before;
   bool too_long;
-  count_tiles(a, row, lane, &total, &before, &too_long);
-  int seq, len;
-  row_of(a, row, &seq, &len, &too_long);
+  Rows first;
+  count_tiles(a, row, lane, &total, &before, &too_long, &first);
+  int len;
+  if (row < 32) {
+    len = __shfl_sync(0xffffffffu, first.len, row & 31);
+  } else {
+    len = length_of(a, row, &too_long);
+  }
   const int tiles = (len + kB8Rows - 1) / kB8Rows;
   const long long x0 = before + static_cast<long long>(h) * tiles;
   TO* out = static_cast<TO*>(a.out) + (static_cast<long long>(row) * a.n_q + qh) * kB8D + 4 * lane;
-  bool mine = true;   // rows behind the last sequence are left alone
-  if (a.query_start) mine = row < ld_dep_s32(a.query_start + a.batch) && row >= ld_dep_s32(a.query_start);
   grid_dep_wait();
   grid_dep_launch();
-  if (!mine) return;
   if (tiles == 0) {
     if (warp == 0) write4<TO>(out, make_float4(0.f, 0.f, 0.f, 0.f));
     return;
   }
   // owners of the pair's first and last tile: warp w owns [total w / nw, total (w + 1) / nw)
   const long long nw = min(static_cast<long long>(a.warps), total);
-  const long long w0 = ((x0 + 1) * nw - 1) / total, w1 = ((x0 + tiles) * nw - 1) / total;
+  const long long w0 = divide((x0 + 1) * nw - 1, total), w1 = divide((x0 + tiles) * nw - 1, total);
   const long long pair = static_cast<long long>(row) * a.n_kv + h;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -505,8 +514,6 @@ cudaError_t launch_split(const B8SplitArgs& a, int ctas, cudaStream_t s) {
   return launch_pdl(kernel, dim3(ctas), dim3(kWarps * 32), kSmem, s, a);
 }
 
-}  // namespace
-
 size_t b8_split_workspace(const tq_config* cfg, long long rows) {
   const int group = cfg->num_q_heads / cfg->num_kv_heads;
   const size_t records = static_cast<size_t>(rows) * cfg->num_kv_heads + kMaxWarps;
@@ -532,6 +539,7 @@ cudaError_t b8_split_launch(B8SplitArgs a, bool is_int8, int q_dtype, int out_dt
   return launch_pdl(b8_merge_kernel<__nv_bfloat16>, grid, block, 0, s, a);
 }
 
+}  // namespace
 }  // namespace tq
 
 extern "C" {
@@ -576,7 +584,6 @@ tq_status tq_b8_decode(const tq_config* cfg, const void* q, long long q_stride, 
   a.status = dev_status;
   a.out = out;
   a.rows = batch;
-  a.batch = batch;
   a.n_q = cfg->num_q_heads;
   a.group = cfg->num_q_heads / cfg->num_kv_heads;
   a.max_seq_len = max_seq_len;
