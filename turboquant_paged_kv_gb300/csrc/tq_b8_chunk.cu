@@ -452,14 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
         const int at = (w.tile0 + i) * kCols;
         const bool masked = bad_groups || at + kCols > vis_least;
         float sums = 0.f;
-        float two[2][32];   // 32 columns of S; the next 32 are on their way
-        tmem_ld32(t_s, reinterpret_cast<uint32_t*>(two[0]));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float* s = two[c & 1];
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {   // rolled: unrolled, the code does not stay in the instruction cache
+          float s[32];
+          tmem_ld32(t_s + 32 * c, reinterpret_cast<uint32_t*>(s));
           wait_ld();
-          if (c < 3) tmem_ld32(t_s + 32 * (c + 1), reinterpret_cast<uint32_t*>(two[(c + 1) & 1]));
-          if (masked) {
+          if (__builtin_expect(masked, 0)) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (at + 32 * c + j >= vis || (bad_groups >> (2 * c + (j >> 4)) & 1)) s[j] = -INFINITY;
@@ -489,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
             sum0 = x0.x + x0.y;
             sum1 = x1.x + x1.y;
             const bool over = !(fmaxf(sum0, sum1) <= kMost && sum0 + sum1 >= 0.f);   // NaN too
-            if (go || !__any_sync(0xffffffffu, over)) break;
+            if (__builtin_expect(go || !__any_sync(0xffffffffu, over), 1)) break;
             float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -521,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
           tmem_st16(t_s + 16 * c, p);
         }
         l += sums;
-        if (i > 0 && __any_sync(0xffffffffu, by_o != 1.f)) {
+        if (__builtin_expect(i > 0 && __any_sync(0xffffffffu, by_o != 1.f), 0)) {
           uint32_t o[32];
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
