@@ -302,15 +302,17 @@ def _b8_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: tor
     if dev != torch.cuda.current_device():
         raise ValueError("the tensors must be on the current CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream()
+        raw = torch._C._cuda_getCurrentRawStream(dev)   # what torch.cuda.current_stream() wraps
     elif stream.device_index != dev:
         raise ValueError("the stream must be one of the tensors' device")
+    else:
+        raw = stream.cuda_stream
     have = cache.numel() // _b8_block_bytes(cfg.preset, cfg.head_dim, cfg.block_size, cfg.num_kv_heads)
     if num_blocks is None:
         num_blocks = have
     elif num_blocks > have:
         raise ValueError(f"cache holds {have} blocks, not {num_blocks}")
-    return num_blocks, width, stream.cuda_stream
+    return num_blocks, width, raw
 
 
 @functools.lru_cache(maxsize=256)

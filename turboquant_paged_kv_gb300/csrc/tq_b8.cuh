@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "tq_internal.h"
@@ -134,6 +135,30 @@ inline tq_status b8_stride(long long* stride, long long row) {
   if (*stride == 0) *stride = row;
   return *stride < row || *stride % 8 ? TQ_ERR_INVALID_ARG : TQ_OK;
 }
+// What a device is asked for once: its SM count, and that a kernel may take `smem`
+// bytes of dynamic shared memory (`done`: a bit a device, one word a kernel).
+inline cudaError_t b8_current_device(int* dev, int* sms) {
+  static std::atomic<int> known[64];
+  cudaError_t err = cudaGetDevice(dev);
+  if (err != cudaSuccess) return err;
+  int n = *dev < 64 ? known[*dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev);
+    if (err != cudaSuccess) return err;
+    if (*dev < 64) known[*dev].store(n, std::memory_order_relaxed);
+  }
+  *sms = n;
+  return cudaSuccess;
+}
+template <typename Kernel>
+cudaError_t b8_allow_smem(Kernel* kernel, int smem, int dev, std::atomic<unsigned long long>* done) {
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (done->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (err == cudaSuccess) done->fetch_or(bit, std::memory_order_relaxed);
+  return err;
+}
+
 // Softmax scale in log2 units.
 inline float b8_qscale(float scale) {
   const float s = scale > 0.f ? scale : 0.08838834764831845f;   // 1 / sqrt(128)

@@ -711,10 +711,12 @@ __global__ void __launch_bounds__(256) b8_chunk_merge_kernel(const B8ChunkArgs a
 
 template <typename TQ, typename TO, bool INT8>
 cudaError_t launch(const B8ChunkArgs& a, const B8ChunkPlan& p, cudaStream_t s) {
-  auto* kernel = b8_chunk_kernel<TQ, TO, INT8>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err == cudaSuccess) err = b8_allow_smem(b8_chunk_kernel<TQ, TO, INT8>, kSmem, dev, &done);
   if (err != cudaSuccess) return err;
-  err = launch_pdl(kernel, dim3(static_cast<unsigned>(p.q_tiles * a.c.n_kv * p.splits)), dim3(kThreads), kSmem, s, a);
+  err = launch_pdl(b8_chunk_kernel<TQ, TO, INT8>, dim3(static_cast<unsigned>(p.q_tiles * a.c.n_kv * p.splits)), dim3(kThreads), kSmem, s, a);
   if (err != cudaSuccess || p.splits == 1) return err;
   const long long rows = static_cast<long long>(a.total_q) * a.n_q;
   return launch_pdl(b8_chunk_merge_kernel<TO>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, s, a);

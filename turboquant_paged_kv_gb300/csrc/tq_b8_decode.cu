@@ -506,12 +506,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) b8_merge_kernel(const B8Spli
   write4<TO>(out, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
 }
 
-template <typename TQ, bool INT8>
-cudaError_t launch_split(const B8SplitArgs& a, int ctas, cudaStream_t s) {
-  auto* kernel = a.group > 4 ? b8_split_kernel<TQ, INT8, true> : b8_split_kernel<TQ, INT8, false>;
-  const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <typename TQ, bool INT8, bool WIDE>
+cudaError_t launch_split(const B8SplitArgs& a, int ctas, int dev, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t err = b8_allow_smem(b8_split_kernel<TQ, INT8, WIDE>, kSmem, dev, &done);
   if (err != cudaSuccess) return err;
-  return launch_pdl(kernel, dim3(ctas), dim3(kWarps * 32), kSmem, s, a);
+  return launch_pdl(b8_split_kernel<TQ, INT8, WIDE>, dim3(ctas), dim3(kWarps * 32), kSmem, s, a);
+}
+template <typename TQ>
+cudaError_t launch_split(const B8SplitArgs& a, bool is_int8, int ctas, int dev, cudaStream_t s) {
+  if (a.group > 4) return is_int8 ? launch_split<TQ, true, true>(a, ctas, dev, s) : launch_split<TQ, false, true>(a, ctas, dev, s);
+  return is_int8 ? launch_split<TQ, true, false>(a, ctas, dev, s) : launch_split<TQ, false, false>(a, ctas, dev, s);
 }
 
 size_t b8_split_workspace(const tq_config* cfg, long long rows) {
@@ -522,16 +527,14 @@ size_t b8_split_workspace(const tq_config* cfg, long long rows) {
 
 cudaError_t b8_split_launch(B8SplitArgs a, bool is_int8, int q_dtype, int out_dtype, void* workspace, cudaStream_t s) {
   int dev = 0, sms = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t err = b8_current_device(&dev, &sms);
   if (err != cudaSuccess) return err;
   const int ctas = sms < kB8MaxCtas ? sms : kB8MaxCtas;
   a.warps = ctas * kWarps;
   const size_t records = static_cast<size_t>(a.rows) * a.n_kv + kMaxWarps;
   a.rec_o = static_cast<float*>(workspace);
   a.rec_lse = a.rec_o + records * a.group * kB8D;
-  if (q_dtype == TQ_DTYPE_BF16) err = is_int8 ? launch_split<__nv_bfloat16, true>(a, ctas, s) : launch_split<__nv_bfloat16, false>(a, ctas, s);
-  else err = is_int8 ? launch_split<__half, true>(a, ctas, s) : launch_split<__half, false>(a, ctas, s);
+  err = q_dtype == TQ_DTYPE_BF16 ? launch_split<__nv_bfloat16>(a, is_int8, ctas, dev, s) : launch_split<__half>(a, is_int8, ctas, dev, s);
   if (err != cudaSuccess) return err;
   const dim3 grid(static_cast<unsigned>(a.rows) * static_cast<unsigned>(a.n_q)), block(kMergeWarps * 32);
   if (out_dtype == TQ_DTYPE_F32) return launch_pdl(b8_merge_kernel<float>, grid, block, 0, s, a);
