@@ -472,6 +472,36 @@ def test_continue_long(tq, q_len, hist, group, n_kv):
     check_continue(c, q, got, [0, q_len], [q_len + hist], "f32", rows=16)
 
 
+@pytest.mark.parametrize("fmt,batch", [("int8_blk", 90), ("e4m3_blk", 77), ("int8_blk", 500)])
+def test_continue_many_chunks(tq, fmt, batch):
+    """More (chunk, head) units than fit one wave, the last ones split over the
+    history (180 = 152 + 28, 154 = 152 + 2; 1000 are not split), lengths from one
+    position on, empty chunks between; all sequences share their blocks."""
+    c = Case(tq, fmt, 32, 8, 2, [700], seed=batch).fill([700])
+    c.table = np.repeat(c.table, batch, 0)
+    q_lens = c.rng.integers(1, 4, batch)
+    if batch == 500:
+        q_lens[c.rng.permutation(batch)[:100]] = 0
+    lens = np.maximum(c.rng.integers(1, 701, batch), q_lens)
+    c.lens = lens.astype(np.int32)
+    starts = starts_of(q_lens)
+    q = c.draw(int(starts[-1]), 8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, starts, lens, status=status)
+    assert int(status) == 0
+    k, v = c.kv(0, 700)
+    floors = np.abs(v)
+    s = np.array([[o8.scale(c.f, c.cache, int(c.table[0, p // 32]), h, 1) for h in range(2)] for p in range(700)])[..., None]
+    floors = np.cumsum(floors * s.max(0) / s, 0) * 2.0 ** -24     # at most: s_max of all positions
+    for b in range(batch):
+        for i in range(int(q_lens[b])):
+            seen = int(lens[b]) - int(q_lens[b]) + i + 1
+            row = int(starts[b]) + i
+            ref, size, reach = o8.attend(q[row].double().numpy(), k[:seen], v[:seen], SCALE)
+            tol = tolerance(ref, size, reach, seen, "f32", np.repeat(floors[seen - 1], 4, 0), single_p=True)
+            assert np.all(np.abs(got[row] - ref) <= tol), (b, i, seen)
+
+
 @pytest.mark.parametrize("q_len", [5, 150])
 def test_continue_rows_without_positions_and_padding(tq, q_len):
     """Queries before position 0, past max_q_len and behind the last sequence."""
@@ -525,6 +555,49 @@ def test_continue_blocks_of_very_different_value_scales(tq, fmt, gain):
     q = c.draw(150, 4)
     got = run_continue(c, q, [0, 150], [400])
     check_continue(c, q, got, [0, 150], [400], "f32", rows=12)
+
+
+def test_continue_on_streams_and_in_graphs(tq):
+    """As for the decode: two streams, then a captured call replayed with other
+    starts, lengths and queries in padded tensors; the same call gives the same bits."""
+    c = Case(tq, "int8_blk", 16, 8, 2, [900] * 3, seed=60).fill([900] * 3)
+    cache, table, _ = c.gpu()
+    rows, msl = 64, 900
+    calls = []
+    for starts, lens in (([0, 20, 20, 55], [900, 3, 500]), ([0, 1, 40, 64], [7, 899, 64])):
+        q = c.draw(rows, 8)
+        calls.append((q, starts, lens, q.cuda(), torch.tensor(starts, dtype=torch.int32, device="cuda"),
+                      torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                      torch.full((rows, 8, 128), 123.0, dtype=torch.float32, device="cuda"),
+                      torch.empty(tq.tq_b8_continue_workspace_size(c.cfg, 3, rows, 48, msl), dtype=torch.uint8, device="cuda"),
+                      torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _, _, _, q, starts, lens, out, ws, stream in calls:
+        with torch.cuda.stream(stream):
+            tq.tq_b8_continue(c.cfg, q, starts, 48, cache, table, lens, msl, out, ws)
+    torch.cuda.synchronize()
+    for q, starts, lens, _, _, _, out, _, _ in calls:
+        got = out.cpu().numpy().astype(np.float64)
+        check_continue(c, q, got, starts, lens, "f32", rows=5)
+        assert np.all(got[starts[-1]:] == 123.0)
+    q, _, _, q_d, starts_d, lens_d, out, ws, _ = calls[0]
+    first = out.clone()
+    tq.tq_b8_continue(c.cfg, q_d, starts_d, 48, cache, table, lens_d, msl, out, ws)
+    assert torch.equal(first, out)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tq.tq_b8_continue(c.cfg, q_d, starts_d, 48, cache, table, lens_d, msl, out, ws)
+    for starts, lens in (([0, 48, 49, 60], [48, 800, 333]), ([0, 0, 0, 5], [10, 20, 700]), ([0, 0, 0, 0], [1, 2, 3])):
+        fresh = c.draw(rows, 8)
+        q_d.copy_(fresh)
+        starts_d.copy_(torch.tensor(starts, dtype=torch.int32))
+        lens_d.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(123.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.cpu().numpy().astype(np.float64)
+        check_continue(c, fresh, got, starts, lens, "f32", rows=5)
+        assert np.all(got[starts[-1]:] == 123.0)
 
 
 # ---------------------------------------------------------------- together

@@ -14,15 +14,19 @@ struct B8ChunkArgs {
   const int *block_table, *seq_lens, *query_start;
   unsigned int* status;
   void* out;
-  float *rec_o, *rec_lse;   // [total_q][n_q][splits][d], [total_q][n_q][splits] (log2 units), for splits > 1
-  int batch, total_q, max_q_len, n_q, group, max_seq_len, cap, splits, split_tiles;
+  // for units that are split: how many there are and in how many parts, then each one's
+  // first row, rows and first head; a part's records, [parts][part_rows][d] and
+  // [parts][part_rows] (log2 units)
+  int4* split_units;
+  float *rec_o, *rec_lse;
+  int batch, total_q, max_q_len, n_q, group, max_seq_len, cap, may_split, part_rows;
   float qscale;             // softmax scale * log2(e)
 };
 
-// How the history is split over CTAs, and the workspace that takes.
+// The grid, and the workspace that split histories take.
 struct B8ChunkPlan {
-  long long q_tiles;   // at most
-  int splits, split_tiles;
+  long long units;   // (tile of queries, KV head), at most
+  int may_split, part_rows;
   size_t workspace;
 };
 B8ChunkPlan b8_chunk_plan(const tq_config* cfg, int batch, int total_q, int max_q_len, int max_seq_len);

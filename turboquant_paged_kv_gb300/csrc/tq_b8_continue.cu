@@ -36,7 +36,7 @@ tq_status tq_b8_continue(const tq_config* cfg, const void* q, long long q_stride
     return TQ_ERR_WORKSPACE_TOO_SMALL;
   if (static_cast<long long>(total_q) * cfg->num_q_heads > INT_MAX) return TQ_ERR_UNSUPPORTED;
   const B8ChunkPlan p = b8_chunk_plan(cfg, batch, total_q, max_q_len, max_seq_len);
-  if (p.q_tiles * cfg->num_kv_heads * p.splits > INT_MAX) return TQ_ERR_UNSUPPORTED;
+  if (p.units > INT_MAX - 4096) return TQ_ERR_UNSUPPORTED;
   B8ChunkArgs a = {};
   a.c = b8_cache(cfg, L, cache, num_blocks, bt_stride);
   a.q = q;
