@@ -177,6 +177,10 @@ def test_binding_refusals(tq):
         tq.tq_b8_store(cfg, q, kv, starts, 1, cache, table, lens)
     with pytest.raises(ValueError, match="contiguous"):
         tq.tq_b8_store(cfg, torch.zeros((2, 4, 256), dtype=torch.bfloat16)[..., ::2], kv, starts, 1, cache, table, lens)
+    with pytest.raises(ValueError, match="overlap"):     # one row for all of them
+        tq.tq_b8_store(cfg, kv[:1].expand(2, 4, 128), kv, starts, 1, cache, table, lens)
+    with pytest.raises(ValueError, match="overlap"):
+        tq.tq_b8_decode(cfg, q[:1].expand(2, 16, 128), cache, table, lens, 64, out, ws)
     with pytest.raises(ValueError, match="one dtype"):
         tq.tq_b8_store(cfg, kv.half(), kv, starts, 1, cache, table, lens)
     with pytest.raises(ValueError, match="query_start"):

@@ -414,6 +414,28 @@ def test_decode_on_streams_and_in_graphs(tq):
             check_decode(c, fresh, out[0].cpu().numpy().astype(np.float64), "f32", lens=new)
 
 
+def test_refusals_with_tensors_on_the_gpu(tq):
+    """What the CPU tests cannot reach because a host tensor is refused first."""
+    c = Case(tq, "int8_blk", 16, 4, 1, [20, 20], seed=70).fill([20, 20])
+    cache, table, lens = c.gpu()
+    q = c.draw(2, 4).cuda()
+    out = torch.full_like(q, 5.0)
+    n = tq.tq_b8_decode_workspace_size(c.cfg, 2, 20)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for bad, match in ((dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)), "workspace"),
+                       (dict(workspace=ws.cpu()), "one CUDA device"), (dict(seq_lens=lens.cpu()), "one CUDA device"),
+                       (dict(num_blocks=c.blocks + 1), "blocks"), (dict(dev_status=torch.zeros(1, device="cuda")), "dev_status")):
+        args = dict(cfg=c.cfg, q=q, cache=cache, block_table=table, seq_lens=lens, max_seq_len=20, out=out, workspace=ws)
+        with pytest.raises(ValueError, match=match):
+            tq.tq_b8_decode(**{**args, **bad})
+    with pytest.raises(tq.TQError, match="workspace"):
+        tq.tq_b8_decode(c.cfg, q, cache, table, lens, 20, out, ws[:n - 16])
+    with pytest.raises(tq.TQError, match="misaligned"):
+        tq.tq_b8_decode(c.cfg, q, cache, table, lens, 20, out, torch.empty(n + 8, dtype=torch.uint8, device="cuda")[8:])
+    torch.cuda.synchronize()
+    assert torch.all(out == 5.0)
+
+
 # ---------------------------------------------------------------- chunks
 
 
@@ -598,6 +620,47 @@ def test_continue_on_streams_and_in_graphs(tq):
         got = out.cpu().numpy().astype(np.float64)
         check_continue(c, fresh, got, starts, lens, "f32", rows=5)
         assert np.all(got[starts[-1]:] == 123.0)
+
+
+def test_offsets_past_32_bits(tq):
+    """The same sequences in a small cache and behind the first 4 GB of a large one
+    give the same bits, written, read back and attended to; and an output of more
+    than 2^31 elements is filled to its end."""
+    n_q, n_kv, lens = 16, 8, [300, 77]
+    cfg = tq.make_config("e4m3_blk", n_q, n_kv, block_size=128)
+    bb = tq.tq_b8_layout_for(cfg).block_bytes
+    far = (1 << 32) // bb + 3
+    c = Case(tq, "e4m3_blk", 128, n_q, n_kv, lens, seed=80)
+    key, value, q = c.draw(377, n_kv).cuda(), c.draw(377, n_kv).cuda(), c.draw(377, n_q).cuda()
+    starts = torch.tensor([0, 300, 377], dtype=torch.int32, device="cuda")
+    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    results = []
+    for base in (0, far):
+        cache = torch.empty((base + 8) * bb, dtype=torch.uint8, device="cuda")
+        table = torch.tensor([[4, 1, 6], [2, 0, 0]], dtype=torch.int32, device="cuda") + base
+        tq.tq_b8_store(cfg, key, value, starts, 300, cache, table, lens_d)
+        k = torch.empty((2, 300, n_kv, 128), dtype=torch.float32, device="cuda")
+        v = torch.empty_like(k)
+        tq.tq_b8_dequant(cfg, cache, table, lens_d, 300, k, v)
+        one = torch.empty((2, n_q, 128), dtype=torch.float32, device="cuda")
+        ws = torch.empty(max(tq.tq_b8_decode_workspace_size(cfg, 2, 300), tq.tq_b8_continue_workspace_size(cfg, 2, 377, 300, 300)),
+                         dtype=torch.uint8, device="cuda")
+        tq.tq_b8_decode(cfg, q[:2].contiguous(), cache, table, lens_d, 300, one, ws)
+        many = torch.empty((377, n_q, 128), dtype=torch.float32, device="cuda")
+        tq.tq_b8_continue(cfg, q, starts, 300, cache, table, lens_d, 300, many, ws)
+        results.append((k, v, one, many))
+        if base == 0:
+            small, small_table = cache, table
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
+    del cache, results
+    long = (1 << 31) // (n_kv * 128) + 1001
+    k = torch.full((1, long, n_kv, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, 3.0)
+    tq.tq_b8_dequant(cfg, small, small_table[1:, :1].contiguous(), lens_d[1:], long, k, v)
+    assert k[0, :77].any() and v[0, 76].any()
+    for x in (k, v):
+        assert not x[0, 77:100].any() and not x[0, -5000:].any() and int(torch.count_nonzero(x[0, 100:].view(torch.int16))) == 0
 
 
 # ---------------------------------------------------------------- together

@@ -276,7 +276,11 @@ def _b8_rows(name: str, t: torch.Tensor, heads: int, d: int) -> int:
         return heads * d
     if s2 != 1 or (s1 != d and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {(s0, s1, s2)}")
-    return s0 if t.shape[0] > 1 else heads * d
+    if t.shape[0] == 1:
+        return heads * d
+    if s0 < heads * d:
+        raise ValueError(f"{name}: the rows must not overlap, got strides {(s0, s1, s2)}")
+    return s0
 
 
 def _b8_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -329,6 +333,12 @@ def _b8_out(name: str, t: torch.Tensor, shape) -> int:
     if t.dtype not in _DTYPES or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float16, bfloat16 or float32 tensor of shape {tuple(shape)}")
     return _DTYPES[t.dtype]
+
+
+def _b8_workspace(t: torch.Tensor) -> int:
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.numel() * t.element_size()
 
 
 def _b8_status(t):
@@ -390,7 +400,7 @@ def tq_b8_decode(cfg: tq_config, q: torch.Tensor, cache: torch.Tensor, block_tab
     nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (q, out, workspace, dev_status), stream)
     st = _LIB.tq_b8_decode(cfg, q.data_ptr(), qs, _DTYPES[q.dtype], cache.data_ptr(), nb, block_table.data_ptr(), width,
                            seq_lens.data_ptr(), q.shape[0], max_seq_len, scale, out.data_ptr(), out_type,
-                           workspace.data_ptr(), workspace.numel() * workspace.element_size(), _b8_status(dev_status), raw)
+                           workspace.data_ptr(), _b8_workspace(workspace), _b8_status(dev_status), raw)
     if st:
         raise TQError("tq_b8_decode", st)
 
@@ -414,6 +424,6 @@ def tq_b8_continue(cfg: tq_config, q: torch.Tensor, query_start: torch.Tensor, m
     st = _LIB.tq_b8_continue(cfg, q.data_ptr(), qs, _DTYPES[q.dtype], query_start.data_ptr(), seq_lens.shape[0], q.shape[0],
                              max_q_len, cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(),
                              max_seq_len, scale, out.data_ptr(), out_type, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _b8_status(dev_status), raw)
+                             _b8_workspace(workspace), _b8_status(dev_status), raw)
     if st:
         raise TQError("tq_b8_continue", st)
