@@ -53,7 +53,7 @@ struct B8SplitArgs {
 
 constexpr int kWarps = 12;         // a CTA
 constexpr int kStages = 4;         // tiles in a warp's ring
-constexpr int kB8MaxCtas = 340;    // grid cap: sizes the workspace without a device query
+constexpr int kB8MaxCtas = 256;    // grid cap: sizes the workspace without a device query
 constexpr int kMaxWarps = 4096;    // partial records beside one per pair
 constexpr int kSmem = kWarps * kStages * (kB8TileBytes + 16);
 constexpr float kStep = 8.f;       // the running maximum moves in steps of at least this, log2 units
@@ -220,14 +220,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
   bool fresh = true;
   int stage = 0;
   for (; todo > 0; --todo) {
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    put_one();
-    const uint32_t kt = ring + stage * kB8TileBytes;
-    const uint2 sw = lds64(tail + stage * 16 + 8 * (get.h & 1));
-    const float s_k = __uint_as_float(sw.x), s_v = __uint_as_float(sw.y);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
-
     if (fresh) {   // a new (row, head) pair: its query heads
       fresh = false;
       const int head = WIDE ? g : g & 3;
@@ -271,6 +263,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
       l0 = l1 = 0.f;
       sigma = inv_sigma = sigma_max = 0.f;   // no reference yet
     }
+
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    put_one();
+    const uint32_t kt = ring + stage * kB8TileBytes;
+    const uint2 sw = lds64(tail + stage * 16 + 8 * (get.h & 1));
+    const float s_k = __uint_as_float(sw.x), s_v = __uint_as_float(sw.y);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
 
     if (s_k > 0.f) {   // a good block
       // S = K . Q^T
@@ -419,14 +419,13 @@ __device__ __forceinline__ void write4(TO* dst, float4 v) {
   }
 }
 
-// A CTA of 4 warps per (row, query head): the records of the pair are those of
-// the warps whose parts of the line meet it; warp k takes every fourth one,
-// four at a time, a lane 4 coordinates.
-constexpr int kMergeWarps = 4;
-template <typename TO>
-__global__ void __launch_bounds__(kMergeWarps * 32) b8_merge_kernel(const B8SplitArgs a) {
-  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
-  __shared__ float4 s_o[kMergeWarps][32];
+// A CTA of WARPS warps per (sequence, query head): the records of the pair are
+// those of the warps whose parts of the line meet it; warp k takes every
+// WARPS-th one, four at a time, a lane 4 coordinates.
+template <typename TO, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) b8_merge_kernel(const B8SplitArgs a) {
+  __shared__ float s_m[WARPS], s_l[WARPS];
+  __shared__ float4 s_o[WARPS][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x / a.n_q, qh = blockIdx.x - row * a.n_q;
   const int h = qh / a.group, gg = qh - h * a.group;
@@ -457,12 +456,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) b8_merge_kernel(const B8Spli
   const long long pair = static_cast<long long>(row) * a.n_kv + h;
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (long long w = w0 + warp; w <= w1; w += 4 * kMergeWarps) {
+  for (long long w = w0 + warp; w <= w1; w += 4 * WARPS) {
     float lse[4];
     float4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const long long v = w + i * kMergeWarps;
+      const long long v = w + i * WARPS;
       const bool ok = v <= w1;
       const long long rec = (pair + v) * a.group + gg;
       lse[i] = ok ? ld_dep_f32(a.rec_lse + rec) : -INFINITY;
@@ -489,7 +488,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) b8_merge_kernel(const B8Spli
   __syncthreads();
   if (warp) return;
 #pragma unroll
-  for (int k = 1; k < kMergeWarps; ++k) {
+  for (int k = 1; k < WARPS; ++k) {
     const float mk = s_m[k];
     if (mk == -INFINITY) continue;
     const float u = fmaxf(m, mk);
@@ -519,6 +518,17 @@ cudaError_t launch_split(const B8SplitArgs& a, bool is_int8, int ctas, int dev, 
   return is_int8 ? launch_split<TQ, true, false>(a, ctas, dev, s) : launch_split<TQ, false, false>(a, ctas, dev, s);
 }
 
+template <typename TO>
+cudaError_t launch_merge(const B8SplitArgs& a, long long records_each, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(a.rows) * static_cast<unsigned>(a.n_q));
+  // the whole decode: 4 x 131072 (59 records) 170.3 us with 4 warps, 166.7 with 16; one sequence
+  // of 301 (19 records) 6.39 with 4, 6.15 with 8; 32 x 4096 (9 records) 50.0 with 4, 51.5 with 8,
+  // 57.3 with 16
+  if (records_each > 32) return launch_pdl(b8_merge_kernel<TO, 16>, grid, dim3(16 * 32), 0, s, a);
+  if (records_each > 16) return launch_pdl(b8_merge_kernel<TO, 8>, grid, dim3(8 * 32), 0, s, a);
+  return launch_pdl(b8_merge_kernel<TO, 4>, grid, dim3(4 * 32), 0, s, a);
+}
+
 size_t b8_split_workspace(const tq_config* cfg, long long rows) {
   const int group = cfg->num_q_heads / cfg->num_kv_heads;
   const size_t records = static_cast<size_t>(rows) * cfg->num_kv_heads + kMaxWarps;
@@ -536,10 +546,13 @@ cudaError_t b8_split_launch(B8SplitArgs a, bool is_int8, int q_dtype, int out_dt
   a.rec_lse = a.rec_o + records * a.group * kB8D;
   err = q_dtype == TQ_DTYPE_BF16 ? launch_split<__nv_bfloat16>(a, is_int8, ctas, dev, s) : launch_split<__half>(a, is_int8, ctas, dev, s);
   if (err != cudaSuccess) return err;
-  const dim3 grid(static_cast<unsigned>(a.rows) * static_cast<unsigned>(a.n_q)), block(kMergeWarps * 32);
-  if (out_dtype == TQ_DTYPE_F32) return launch_pdl(b8_merge_kernel<float>, grid, block, 0, s, a);
-  if (out_dtype == TQ_DTYPE_F16) return launch_pdl(b8_merge_kernel<__half>, grid, block, 0, s, a);
-  return launch_pdl(b8_merge_kernel<__nv_bfloat16>, grid, block, 0, s, a);
+  // records of a pair, if the lengths are alike: all of them in one round of loads
+  const long long tiles = (static_cast<long long>(a.max_seq_len) + kB8Rows - 1) / kB8Rows;
+  long long records_each = a.warps / (static_cast<long long>(a.rows) * a.n_kv) + 2;
+  if (records_each > tiles) records_each = tiles;
+  if (out_dtype == TQ_DTYPE_F32) return launch_merge<float>(a, records_each, s);
+  if (out_dtype == TQ_DTYPE_F16) return launch_merge<__half>(a, records_each, s);
+  return launch_merge<__nv_bfloat16>(a, records_each, s);
 }
 
 }  // namespace
