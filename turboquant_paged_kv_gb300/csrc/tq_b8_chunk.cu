@@ -30,6 +30,20 @@
 // rescaled. S_t(i + 1) is issued after O_t += P_t(i) V, so a complete S_t(i + 1)
 // also says that the accumulators of step i are at rest.
 // Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the CTA.
+//
+// Bound: tensor cores by its operations; measured, the softmax's latency beside
+// them. A step of 256 rows x 128 positions is 32 products of 64 cycles (2240
+// cycles with their commits) and takes about 3600: 7500 warp instructions, and
+// the shared-memory pipe nine tenths busy (operands, codes, tensor-memory
+// traffic). 4 chunks of about 2000 queries over up to 8192 positions, 32 query
+// heads: 695 us, 1219 TFLOP/s, 0.63 of a measured bf16 GEMM; 32 chunks of 128
+// over 4096: 257 us, 1083 TFLOP/s. What moved it: products issued from uniform
+// registers (from a branch that one lane takes, each cost 75 to 200 cycles), no
+// search for the maximum, and code small enough for the instruction cache (the
+// step's softmax rolled, the prologue and the epilogue short: 823 to 695 us).
+// Tried and slower: S in halves of 64 positions one half ahead, P handed over in
+// halves, an issuing warp for each tile (both tiles then fall into step), two
+// threads a row, eight expanding warps.
 #include "tq_attn.cuh"
 #include "tq_b8_chunk.cuh"
 
