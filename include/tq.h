@@ -469,7 +469,8 @@ tq_status tq_prod_scores(const tq_config* cfg, const tq_codebook* cb, const floa
  *   TQ_PRESET_INT8_BLK  code = int8, largest Q = 127
  * The tq_b8_* entry points use cfg->head_dim (128), block_size (16, 32, 64 or
  * 128), num_kv_heads, num_q_heads (attention: n_q % n_kv == 0 and
- * n_q / n_kv <= 8) and flags; partition_tokens must be 0.
+ * n_q / n_kv <= 8) and flags (TQ_FLAG_INDICES_READY, which tq_b8_decode alone
+ * heeds); partition_tokens must be 0.
  *
  * Cache: cache[num_blocks] of block_bytes each,
  *   tiles   [n_kv][block_size / 16][tile_bytes]: a tile holds 16 positions of
@@ -595,7 +596,8 @@ const char* tq_status_string(int status);
 int tq_version(void);
 
 #define TQ_ABI_VERSION 105   /* 1.01: tq_dequant; 1.02: 3bit_nc runs; 1.03: TurboQuant_prod (tq_prod_*);
-                                 1.04: tq_continue; 1.05: tq_decode_append */
+                                 1.04: tq_continue; 1.05: tq_decode_append
+                                 (tq_b8_*: added since, nothing else changed) */
 
 #ifdef __cplusplus
 }
