@@ -579,6 +579,22 @@ def test_continue_blocks_of_very_different_value_scales(tq, fmt, gain):
     check_continue(c, q, got, [0, 150], [400], "f32", rows=12)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("q_len,hist", [(37, 30), (150, 0), (6, 900)])
+@pytest.mark.parametrize("gain_k,gain_q,scale", [(0.0, 0.0, 0.0), (1e-12, 0.0, 0.0), (0.0, 1e-25, 0.0), (1.0, 1e-30, 0.0), (1e-20, 1e-20, 1e-20)])
+def test_scores_that_vanish(tq, fmt, q_len, hist, gain_k, gain_q, scale):
+    """Scores of nothing, or of so little that a block's factor is not a number of
+    fp32 any more: plain means of the values seen."""
+    n = q_len + hist
+    c = Case(tq, fmt, 16, 4, 1, [n], seed=46)
+    o8.store(c.f, c.cache, (c.draw(n, 1).float() * gain_k).numpy(), c.draw(n, 1).float().numpy(), [0, n], c.table, [n])
+    c.lens = np.array([n], dtype=np.int32)
+    q = c.draw(q_len, 4, gain=gain_q)
+    got = run_continue(c, q, [0, q_len], [n], scale=scale)
+    check_continue(c, q, got, [0, q_len], [n], "f32", rows=12, scale=scale or SCALE)
+    check_decode(c, q[:1], run_decode(c, q[:1], scale=scale), "f32", scale=scale or SCALE)
+
+
 def test_continue_on_streams_and_in_graphs(tq):
     """As for the decode: two streams, then a captured call replayed with other
     starts, lengths and queries in padded tensors; the same call gives the same bits."""

@@ -501,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
               if (at + 32 * c + j >= vis || (bad_groups >> (2 * c + (j >> 4)) & 1)) s[j] = -INFINITY;
           }
           const float4 g0 = s_groups[warp][2 * c], g1 = s_groups[warp][2 * c + 1];
-          const float f0 = g0.x * down, f1 = g1.x * down;
+          // never 0, which would make NaN of a masked place; below 2^-126 the scores vanish anyway (|s| < 2^31)
+          const float f0 = fmaxf(g0.x * down, 0x1p-126f), f1 = fmaxf(g1.x * down, 0x1p-126f);
           uint32_t p[16];
           float sum0, sum1;
           // With the maximum so far; a row of which some P would not fit in fp16 shows
