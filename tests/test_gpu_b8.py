@@ -541,6 +541,20 @@ def test_continue_rows_without_positions_and_padding(tq, q_len):
     assert not got[q_len - 1].any() and got[q_len - 2].any() and np.all(got[starts[-1]:] == 123.0)
 
 
+def test_continue_starts_that_go_backwards(tq):
+    """Not allowed, but nothing outside the rows is touched: more chunks than the
+    rows could hold in order, all of them the same one."""
+    batch, n, rows = 401, 600, 32
+    c = Case(tq, "int8_blk", 32, 32, 4, [n], seed=47).fill([n])
+    c.table = np.repeat(c.table, batch, 0)
+    starts = np.array([0, rows] * ((batch + 1) // 2), dtype=np.int32)
+    q = c.draw(rows + 5, 32)
+    got = run_continue(c, q, starts, [n] * batch)
+    assert np.all(got[rows:] == 123.0)
+    c.lens = np.array([n], dtype=np.int32)
+    check_continue(c, q, got, [0, rows], [n], "f32")
+
+
 @pytest.mark.parametrize("hist,dtype", [(20, "bf16"), (2000, "bf16"), (20, "f32")])
 def test_continue_output_on_16_bytes(tq, hist, dtype):
     """out and workspace may lie on any 16 bytes (whole and split histories)."""

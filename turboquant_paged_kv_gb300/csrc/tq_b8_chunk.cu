@@ -287,14 +287,15 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       for (int b0 = 0; b0 < a.batch; b0 += 32) tiles += __reduce_add_sync(0xffffffffu, tiles_of(a, b0 + lane, per).tiles);
       const int units = tiles * a.c.n_kv, rem = units % kParts;
       full = units - rem;
-      parts = rem ? kParts / rem : 1;
+      // starts that go backwards may name more units than the grid has CTAs for: no records then
+      parts = rem && units <= static_cast<int>(gridDim.x) - kParts ? kParts / rem : 1;
+      if (blockIdx.x == 0 && lane == 0) a.split_units[0] = make_int4(parts > 1 ? rem : 0, parts, 0, 0);
       if (parts > 1 && unit >= full) {
         part = (unit - full) % parts;
         unit = full + (unit - full) / parts;
       } else {
         parts = 1;
       }
-      if (blockIdx.x == 0 && lane == 0) a.split_units[0] = make_int4(rem && kParts / rem > 1 ? rem : 0, rem ? kParts / rem : 1, 0, 0);
     }
     int x = unit / a.c.n_kv;
     const int h = unit - x * a.c.n_kv;
