@@ -555,6 +555,28 @@ def test_continue_starts_that_go_backwards(tq):
     check_continue(c, q, got, [0, rows], [n], "f32")
 
 
+@pytest.mark.parametrize("room,stored", [(40, 0), (40, 16), (900, 64)])
+def test_blocks_that_nothing_was_stored_to(tq, room, stored):
+    """A zeroed cache's fresh blocks (the padding of a batch points there) are left
+    out without an error."""
+    c = Case(tq, "e4m3_blk", 16, 4, 2, [room], seed=48)
+    c.cache[:] = 0
+    c.fill([stored])
+    q = c.draw(3, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    chunk = run_continue(c, q, [0, 3], [room], status=status)
+    step = run_decode(c, q[:1], [room], status=status)
+    assert int(status) == 0
+    if stored:
+        k, v = c.kv(0, stored)
+        for i in range(3):
+            ref, size, reach = o8.attend(q[i].double().numpy(), k, v, SCALE)
+            assert np.all(np.abs(chunk[i] - ref) <= tolerance(ref, size, reach, stored, "f32", c.floor(0, stored, chunks=True), single_p=True))
+        check_decode(c, q[:1], step, "f32", [stored])
+    else:
+        assert not chunk.any() and not step.any()
+
+
 @pytest.mark.parametrize("hist,dtype", [(20, "bf16"), (2000, "bf16"), (20, "f32")])
 def test_continue_output_on_16_bytes(tq, hist, dtype):
     """out and workspace may lie on any 16 bytes (whole and split histories)."""

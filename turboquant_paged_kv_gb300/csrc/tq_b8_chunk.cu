@@ -460,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       float m = -1e30f, l = 0.f, sigma = 0.f, sigma_max = -INFINITY;
       bool ok = true;
       for (int i = 0; i < tiles; ++i) {
-        const bool bad = sc.x == 0u;   // a scale is never 0
-        if (bad && blk != -2 && t == 0 && warp == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
+        const bool bad = sc.x == 0u;   // a scale that was stored is never 0
+        if (bad && blk != -2 && t == 0 && warp == 0 && !a.c.good(blk)) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
         const unsigned bad_groups = __ballot_sync(0xffffffffu, bad) & 0xffu;
         const float my_lv = bad ? 0.f : __log2f(__uint_as_float(sc.y));
         float top = bad ? -INFINITY : my_lv;
