@@ -29,7 +29,8 @@
 // (by the softmax warps, in tensor memory) and the step's earlier P are
 // rescaled. S_t(i + 1) is issued after O_t += P_t(i) V, so a complete S_t(i + 1)
 // also says that the accumulators of step i are at rest.
-// Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the CTA.
+// Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the CTA,
+// after its products in flight.
 //
 // Bound: tensor cores by its operations; measured, the softmax's latency beside
 // them. A step of 256 rows x 128 positions is 32 products of 64 cycles (2240
@@ -63,7 +64,7 @@ constexpr uint32_t kSmem = kOffBar + 256 + 1024;   // and room to align to 1024
 constexpr uint32_t kColS = 0, kColO = 256;
 
 // barriers, 8 bytes each from kOffBar
-enum { kQFull, kKFull0, kKFull1, kVFull0, kVFull1, kKEmpty0, kKEmpty1, kVEmpty0, kVEmpty1, kSFull0, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kBars };
+enum { kQFull, kKFull0, kKFull1, kVFull0, kVFull1, kKEmpty0, kKEmpty1, kVEmpty0, kVEmpty1, kSFull0, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kEnd, kBars };
 
 // shared-memory operand descriptors: 128-byte swizzle, 8-row groups 1024 bytes apart
 __device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
@@ -271,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       mbar_init(bar(kPFull0 + i), 4);
       mbar_init(bar(kODone0 + i), 1);
     }
+    mbar_init(bar(kEnd), 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 12) {
@@ -706,6 +708,10 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
             __syncwarp();
           }
         }
+      }
+      if (!ok) {   // gave up: the products in flight come to rest before their memory goes
+        if (leader) mma_commit(bar(kEnd));
+        warp_wait(kEnd, 0);
       }
     }
     __syncwarp();
