@@ -550,7 +550,7 @@ size_t tq_b8_decode_workspace_size(const tq_config* cfg, int batch, int max_seq_
  * positions, as tq_decode (scale <= 0: 1 / sqrt(d); an empty sequence gives
  * zeros; positions of a bad block id are left out, and so, without an error, are
  * those of a block of a zeroed cache that nothing was stored to: its scales are
- * 0). Scores are fp32: one past its range does not come out right.
+ * 0). Scores are fp32; of magnitudes from 1e30 on they do not come out right.
  *   q          device [batch][n_q][d] of q_dtype (f16 or bf16), 16-byte
  *              aligned, rows q_stride elements apart (0: n_q * d; else
  *              >= n_q * d and a multiple of 8)

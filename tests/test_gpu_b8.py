@@ -555,6 +555,31 @@ def test_continue_starts_that_go_backwards(tq):
     check_continue(c, q, got, [0, rows], [n], "f32")
 
 
+@pytest.mark.parametrize("q_len,length,cut", [(140, 200, 150), (5, 900, 897), (20, 900, 500)])
+def test_continue_cuts_long_sequences(tq, q_len, length, cut):
+    """Queries keep their places; none sees a position from max_seq_len on."""
+    c = Case(tq, "e4m3_blk", 32, 4, 1, [length], seed=49).fill([length])
+    q = c.draw(q_len, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, [0, q_len], [length], status=status, max_len=cut)
+    assert int(status) == tq.TQ_DEV_SEQ_TOO_LONG
+    k, v = c.kv(0)
+    floor = c.floor(0, length, chunks=True)
+    for i in range(0, q_len, max(q_len // 20, 1)):
+        seen = min(length - q_len + i + 1, cut)
+        ref, size, reach = o8.attend(q[i].double().numpy(), k[:seen], v[:seen], SCALE)
+        assert np.all(np.abs(got[i] - ref) <= tolerance(ref, size, reach, seen, "f32", floor, single_p=True)), (i, seen)
+
+
+@pytest.mark.parametrize("gain", [lambda j: 0.0, lambda j: j % 3 == 1, lambda j: j < 2])
+def test_blocks_of_zero_values(tq, gain):
+    """Values of zero take their share of the weights (their scale is the smallest)."""
+    c = Case(tq, "int8_blk", 16, 4, 1, [600], seed=51).fill([600], gain)
+    q = c.draw(40, 4)
+    check_continue(c, q, run_continue(c, q, [0, 40], [600]), [0, 40], [600], "f32", rows=12)
+    check_decode(c, q[:1], run_decode(c, q[:1]), "f32")
+
+
 @pytest.mark.parametrize("room,stored", [(40, 0), (40, 16), (900, 64)])
 def test_blocks_that_nothing_was_stored_to(tq, room, stored):
     """A zeroed cache's fresh blocks (the padding of a batch points there) are left
