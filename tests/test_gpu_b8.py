@@ -580,6 +580,26 @@ def test_blocks_of_zero_values(tq, gain):
     check_decode(c, q[:1], run_decode(c, q[:1]), "f32")
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_continue_one_position_is_its_value(tq, fmt):
+    """The weight of a sequence's only position is exact in fp16, whatever the scale:
+    left are two roundings of a score below 64 in the exponent (2^-19 each), the
+    logarithm of a scale between 2^-16 and 1 and its power (2^-20 each) and the
+    quotient (2^-22): below 2^-16."""
+    batch = 40
+    c = Case(tq, fmt, 16, 4, 2, [1] * batch, seed=52)
+    for b in range(batch):
+        o8.store(c.f, c.cache, c.draw(1, 2).float().numpy(), c.draw(1, 2).float().numpy() * np.float32(1.1 ** (b - 20)), [0, 1], c.table[b:b + 1], [1])
+    c.lens = np.ones(batch, dtype=np.int32)
+    q = c.draw(batch, 4)
+    got = run_continue(c, q, np.arange(batch + 1), c.lens)
+    for b in range(batch):
+        k, v = c.kv(b)
+        assert np.abs(q[b].double().numpy() @ k[0].repeat(2, 0).T).max() * SCALE * 1.4427 < 64
+        ref = v[0].repeat(2, 0)
+        assert np.all(np.abs(got[b] - ref) <= np.abs(ref) * 2.0 ** -16)
+
+
 @pytest.mark.parametrize("room,stored", [(40, 0), (40, 16), (900, 64)])
 def test_blocks_that_nothing_was_stored_to(tq, room, stored):
     """A zeroed cache's fresh blocks (the padding of a batch points there) are left

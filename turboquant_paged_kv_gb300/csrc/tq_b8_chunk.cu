@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
         float by_o = 1.f;   // what the accumulators take
         if (top != -INFINITY && !(fabsf(top - sigma) <= 4.f && sigma_max != -INFINITY)) {
           sigma_max = fmaxf(sigma_max, top);
-          const float next = fmaxf(rintf(top), rintf(sigma_max) - 64.f);
+          const float next = fmaxf(top, sigma_max - 64.f);   // not rounded: the largest weight is then 8, exact in fp16
           by_o = ex2(sigma - next);
           sigma = next;
         }
