@@ -760,6 +760,96 @@ def test_offsets_past_32_bits(tq):
         assert not x[0, 77:100].any() and not x[0, -5000:].any() and int(torch.count_nonzero(x[0, 100:].view(torch.int16))) == 0
 
 
+# ---------------------------------------------------------------- chunks, row by row
+
+
+def check_rows(c, q, got, starts, lens, out_dtype="f32", rows=None, scale=SCALE):
+    """As check_continue, the bound taken from what each query sees and weighs.
+      weights: P = 8 p s_v / r, rounded to fp16 once, and once more where the row's
+        reference r moves within a step: 2 half steps, 2^-10 together
+      r is at most the largest p s_v that the row sees: no step below 2^-24 means
+        2^-28 of that per code and rounding
+      exponents: log2 s_v is off by up to 2 units of its last place (|log2 s_v| < 128:
+        2^-16), its difference to the reference by half a unit of a number below 256
+        (2^-17), the reference's moves as much: below 2^-14 relative"""
+    for b in range(len(lens)):
+        k, v = c.kv(b, int(lens[b]))
+        s = np.array([[o8.scale(c.f, c.cache, int(c.table[b, p // c.block]), h, 1) for h in range(c.n_kv)] for p in range(int(lens[b]))],
+                     dtype=np.float64)
+        q0, n = int(starts[b]), int(starts[b + 1] - starts[b])
+        for i in range(n) if rows is None else sorted({0, n - 1, *range(0, n, max(n // rows, 1))}):
+            seen = int(lens[b]) - n + i + 1
+            x = q[q0 + i].double().numpy()
+            ref, size, reach = o8.attend(x, k[:seen], v[:seen], scale)
+            floor = np.zeros_like(ref)
+            for h in range(c.n_q):
+                g = h // (c.n_q // c.n_kv)
+                z = k[:seen, g] @ x[h] * scale
+                p = np.exp(z - z.max())
+                codes = np.abs(v[:seen, g]) / s[:seen, g, None]
+                floor[h] = 2.0 ** -27 * (p / p.sum() * s[:seen, g]).max() * codes.sum(0)
+            tol = tolerance(ref, size, reach, seen, out_dtype, floor + size * (2.0 ** -11 + 2.0 ** -14), single_p=True)
+            err = np.abs(got[q0 + i] - ref)
+            assert np.all(err <= tol), (b, i, seen, float((err / tol).max()))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hist,q_len", [(0, 70), (890, 60)])
+@pytest.mark.parametrize("r", [10, 18, 24, 28, 60, 110])
+def test_continue_small_values_before_large_ones(tq, fmt, hist, q_len, r):
+    """Queries among the small values do not see the large ones behind them."""
+    n = hist + q_len
+    first = -(-(hist + 16) // 16)     # the first block of large values
+    c = Case(tq, fmt, 16, 4, 1, [n], seed=90).fill([n], lambda j: 1.0 if j < first else 2.0 ** r)
+    q = c.draw(q_len, 4)
+    got = run_continue(c, q, [0, q_len], [n])
+    assert got[:first * 16 - hist].any(-1).all()
+    check_rows(c, q, got, [0, q_len], [n], rows=None if hist == 0 else 12)
+
+
+@pytest.mark.parametrize("n,q_len,gain", [(64, 20, 30), (64, 64, 30), (700, 20, 30), (400, 150, 100)])
+def test_continue_small_values_under_the_weights_of_large_ones(tq, n, q_len, gain):
+    """As for the decode: the first block's values are 2^gain times the others', its keys score far below."""
+    c = Case(tq, "int8_blk", 16, 1, 1, [n], seed=91)
+    k, v = c.draw(n, 1).float().numpy(), c.draw(n, 1).float().numpy()
+    q = torch.ones((q_len, 1, 128), dtype=torch.bfloat16)
+    k[:16] = -40.0
+    v[:16] *= np.float32(2.0 ** gain)
+    o8.store(c.f, c.cache, k, v, [0, n], c.table, [n])
+    check_rows(c, q, run_continue(c, q, [0, q_len], [n]), [0, q_len], [n], rows=20)
+
+
+@pytest.mark.parametrize("gap", [0, 20, 60, 80, 100, 118, 122, 130, 200])
+@pytest.mark.parametrize("low,high", [(60, -60), (-60, 60), (100, -90)])
+def test_continue_scores_and_value_scales_that_rise_and_fall(tq, gap, low, high):
+    """Block by block, scores rise by gap / 2 (log2 units) and values go from 2^low over 1 to 2^high."""
+    c = Case(tq, "int8_blk", 16, 2, 1, [48], seed=92)
+    k = np.zeros((48, 1, 128), dtype=np.float32)
+    v = c.draw(48, 1).float().numpy()
+    for j, g in enumerate((low, 0, high)):
+        k[16 * j:16 * j + 16] = 0.5 * j * gap / (128 * SCALE * np.log2(np.e))
+        v[16 * j:16 * j + 16] *= np.float32(2.0 ** g)
+    o8.store(c.f, c.cache, k, v, [0, 48], c.table, [48])
+    q = torch.ones((48, 2, 128), dtype=torch.bfloat16)
+    check_rows(c, q, run_continue(c, q, [0, 48], [48]), [0, 48], [48])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hist", [0, 800])
+def test_continue_later_positions_change_nothing(tq, fmt, hist):
+    """Bit for bit, whatever the keys and values that a query does not see."""
+    q_len = 60
+    n, out = hist + q_len, []
+    for gain in (1.0, 2.0 ** 20, 2.0 ** -20):
+        c = Case(tq, fmt, 16, 4, 1, [n], seed=93)
+        k, v, q = c.draw(n, 1).float().numpy(), c.draw(n, 1).float().numpy(), c.draw(q_len, 4)
+        k[hist + 32:] *= np.float32(gain)
+        v[hist + 32:] *= np.float32(gain)
+        o8.store(c.f, c.cache, k, v, [0, n], c.table, [n])
+        out.append(run_continue(c, q, [0, q_len], [n])[:32])
+    assert np.array_equal(out[0], out[1]) and np.array_equal(out[0], out[2])
+
+
 # ---------------------------------------------------------------- together
 
 

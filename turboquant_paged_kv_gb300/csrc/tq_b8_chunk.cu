@@ -13,10 +13,14 @@
 // brings its largest magnitude to 2^14, so the scores are sums of exact
 // products. The block scales enter with the softmax: s_k multiplies a group of
 // 16 columns, log2(s_v) is added to the exponent, and the denominator takes
-// each group's sum times 2^sigma / (8 s_v). P is rounded once, to fp16 (half a
-// step is 2^-11; no step below 2^-24, which is 2^-27 sigma / s_v of the largest
-// weight). sigma follows the largest s_v of the positions at hand: it moves, and
-// the accumulators are rescaled, when that leaves 2^+-4 of it.
+// each group's sum times 2^sigma / s_v. p = 2^(score - m), and m and sigma are
+// the row's own: m at most its largest score so far, m + sigma at most its
+// largest score + log2(s_v), over the positions that it sees. So the largest P
+// of a row is 8 or more whatever the scales of the blocks are that it does not
+// see or gives no weight (one sigma for a step, from its largest s_v, took 0 for
+// rows whose own values were 2^-28 of that), and no later position changes a bit
+// of a row. P is rounded to fp16: half a step is 2^-11, and no step below 2^-24
+// errs by up to 2^-28 of the row's largest p s_v, for each code.
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread a row, no
 // shuffles), 8-11 expand codes from global memory into the two-stage fp16
@@ -24,11 +28,11 @@
 // operand, and V, read as an MN-major one), 12 issues the products: of the two
 // tiles in turn, so one tile's products run while the other's softmax does.
 // No maximum is sought in the common case: the weights are taken with the
-// maximum so far, and a row of which some P would not fit in fp16 shows in its
-// sums of 16; only then the row's new maximum is found, and what was accumulated
-// (by the softmax warps, in tensor memory) and the step's earlier P are
-// rescaled. S_t(i + 1) is issued after O_t += P_t(i) V, so a complete S_t(i + 1)
-// also says that the accumulators of step i are at rest.
+// maximum so far, and a row of which some P would not fit in fp16, or whose m has
+// fallen far behind, shows in its sums; only then the row's new m and sigma are
+// found, and what was accumulated (by the softmax warps, in tensor memory) and
+// the step's earlier P are rescaled. S_t(i + 1) is issued after O_t += P_t(i) V,
+// so a complete S_t(i + 1) also says that the accumulators of step i are at rest.
 // Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the CTA,
 // after its products in flight.
 //
@@ -56,6 +60,8 @@ constexpr int kCols = 128;             // positions a step
 constexpr int kThreads = 512;
 constexpr int kParts = 152;            // CTAs of a wave, one an SM
 constexpr float kMost = 60000.f;       // sums of 16 P up to this: every P fits in fp16
+constexpr float kMostSum = 0x1p24f;    // sums of a step's 8 p up to this: the scores are below m + 21
+constexpr float kLeast = -103.f;       // log2(s_v / 2^sigma) from below: a group's values vanish, its weights still count
 constexpr uint32_t kTileOp = 32768;    // a 128 x 128 fp16 operand: two halves of 64 columns, 128 bytes a row
 constexpr uint32_t kHalfOp = 16384;
 constexpr uint32_t kOffK = 2 * kTileOp, kOffV = 4 * kTileOp, kOffBar = 6 * kTileOp;
@@ -251,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Work s_work;
-  __shared__ float4 s_groups[8][8];   // each softmax warp's: the step's groups of 16 positions
+  __shared__ float2 s_groups[8][8];   // each softmax warp's: s_k and log2(s_v) of the step's groups of 16 positions
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 1023u) & ~1023u;
   const uint32_t bars = base + kOffBar;
@@ -459,30 +465,14 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       int blk = group_block(0);
       uint2 sc = group_scales(blk);
       int blk_next = group_block(1);
-      float m = -1e30f, l = 0.f, sigma = 0.f, sigma_max = -INFINITY;
+      float m = -1e30f, sigma = 0.f, l = 0.f;   // l: sum of 8 p
       bool ok = true;
       for (int i = 0; i < tiles; ++i) {
         const bool bad = sc.x == 0u;   // a scale that was stored is never 0
         if (bad && blk != -2 && t == 0 && warp == 0 && !a.c.good(blk)) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
         const unsigned bad_groups = __ballot_sync(0xffffffffu, bad) & 0xffu;
-        const float my_lv = bad ? 0.f : __log2f(__uint_as_float(sc.y));
-        float top = bad ? -INFINITY : my_lv;
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        if (lane < 8) s_groups[warp][lane] = bad ? make_float2(1.f, 0.f) : make_float2(__uint_as_float(sc.x), __log2f(__uint_as_float(sc.y)));
         float by_o = 1.f;   // what the accumulators take
-        if (top != -INFINITY && !(fabsf(top - sigma) <= 4.f && sigma_max != -INFINITY)) {
-          sigma_max = fmaxf(sigma_max, top);
-          const float next = fmaxf(top, sigma_max - 64.f);   // not rounded: the largest weight is then 8, exact in fp16
-          by_o = ex2(sigma - next);
-          sigma = next;
-        }
-        if (lane < 8) {
-          // s_k, log2(8 s_v / 2^sigma) and the inverse of what that stands for; below
-          // -100 the group's values vanish next to the others', its weights still count
-          const float lv = fmaxf(my_lv - sigma + 3.f, -100.f);
-          s_groups[warp][lane] = make_float4(bad ? 1.f : __uint_as_float(sc.x), lv, ex2(-lv), 0.f);
-        }
         __syncwarp();
         blk = blk_next;
         sc = group_scales(blk);
@@ -503,15 +493,14 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
             for (int j = 0; j < 32; ++j)
               if (at + 32 * c + j >= vis || (bad_groups >> (2 * c + (j >> 4)) & 1)) s[j] = -INFINITY;
           }
-          const float4 g0 = s_groups[warp][2 * c], g1 = s_groups[warp][2 * c + 1];
+          const float2 g0 = s_groups[warp][2 * c], g1 = s_groups[warp][2 * c + 1];
           // never 0, which would make NaN of a masked place; below 2^-126 the scores vanish anyway (|s| < 2^31)
           const float f0 = fmaxf(g0.x * down, 0x1p-126f), f1 = fmaxf(g1.x * down, 0x1p-126f);
           uint32_t p[16];
-          float sum0, sum1;
-          // With the maximum so far; a row of which some P would not fit in fp16 shows
-          // in its sums, takes its new maximum and goes again.
+          float next;   // `sums` with these columns
           for (int go = 0;; ++go) {
-            const float a0 = g0.y - m, a1 = g1.y - m;
+            const float d0 = fmaxf(g0.y - sigma, kLeast), d1 = fmaxf(g1.y - sigma, kLeast);
+            const float a0 = d0 + (3.f - m), a1 = d1 + (3.f - m);
             float2 x0 = make_float2(0.f, 0.f), x1 = x0;
 #pragma unroll
             for (int j = 0; j < 16; j += 2) {
@@ -526,9 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
               p[j / 2] = pack_half2(y0.x, y0.y);
               p[8 + j / 2] = pack_half2(y1.x, y1.y);
             }
-            sum0 = x0.x + x0.y;
-            sum1 = x1.x + x1.y;
-            const bool over = !(fmaxf(sum0, sum1) <= kMost && sum0 + sum1 >= 0.f);   // NaN too
+            const float sum0 = x0.x + x0.y, sum1 = x1.x + x1.y;
+            next = fmaf(sum1, ex2(-d1), fmaf(sum0, ex2(-d0), sums));
+            const bool over = !(fmaxf(sum0, sum1) <= kMost && next <= kMostSum);   // NaN too
             if (__builtin_expect(go || !__any_sync(0xffffffffu, over), 1)) break;
             float mx = -INFINITY, my = -INFINITY;
 #pragma unroll
@@ -536,11 +525,15 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
               mx = fmaxf(mx, s[j]);
               my = fmaxf(my, s[16 + j]);
             }
-            const float u = over ? fmaxf(m, fmaxf(mx * f0, my * f1)) : m;
-            const float e = ex2(m - u);
+            mx *= f0;
+            my *= f1;
+            const float u = over ? fmaxf(m, fmaxf(mx, my)) : m, down_by = m - u;
+            const float r = over ? fmaxf(sigma + down_by, fmaxf(g0.y + (mx - u), g1.y + (my - u))) : sigma;
+            const float e = ex2(down_by + (sigma - r)), e_l = ex2(down_by);
             m = u;
-            l *= e;
-            sums *= e;
+            sigma = r;
+            l *= e_l;
+            sums *= e_l;
             by_o *= e;
             wait_st();
 #pragma unroll 1
@@ -556,8 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
               tmem_st16(t_s + 16 * d, q);
             }
           }
-          sums = fmaf(sum0, g0.z, sums);
-          sums = fmaf(sum1, g1.z, sums);
+          sums = next;
           tmem_st16(t_s + 16 * c, p);
         }
         l += sums;
@@ -579,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       }
       if (ok && warp_wait(kODone0 + t, 0)) {
         fence_after();
-        const float scale = l > 0.f ? ex2(sigma - 3.f) / l : (l == 0.f ? 0.f : l);   // NaN stays
+        const float scale = l > 0.f ? ex2(sigma) / l : (l == 0.f ? 0.f : l);   // NaN stays
         const bool whole = w.slot < 0;
         const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.rec_o)) & 31) == 0;
         const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + head;
@@ -596,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
             else write32<float>(a.rec_o + static_cast<long long>(w.slot * a.part_rows + r) * kB8D + 32 * c, y, wide);
           }
         }
-        if (live && !whole) a.rec_lse[w.slot * a.part_rows + r] = l == 0.f ? -INFINITY : m + __log2f(l);
+        if (live && !whole) a.rec_lse[w.slot * a.part_rows + r] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
       }
     }
   } else if (warp < 12) {
