@@ -850,6 +850,23 @@ def test_continue_later_positions_change_nothing(tq, fmt, hist):
     assert np.array_equal(out[0], out[1]) and np.array_equal(out[0], out[2])
 
 
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("hist,q_len,max_q", [(10, 20, 5), (0, 140, 70), (900, 30, 7)])
+def test_continue_rows_that_were_not_stored(tq, block, hist, q_len, max_q):
+    """Store and attention cut a chunk at the same max_q_len: what stands in the cache
+    behind the last served query (NaN codes, scales of any size) does not count."""
+    n, kept = hist + q_len, hist + max_q
+    c = Case(tq, "e4m3_blk", block, 4, 1, [n], seed=94)
+    c.cache[:] = 0x7f
+    c.fill([kept])
+    q = c.draw(q_len, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, [0, q_len], [n], max_q=max_q, status=status)
+    assert int(status) == tq.TQ_DEV_SEQ_TOO_LONG
+    assert not got[max_q:].any()
+    check_rows(c, q, got, [0, max_q], [kept], rows=12)
+
+
 # ---------------------------------------------------------------- together
 
 

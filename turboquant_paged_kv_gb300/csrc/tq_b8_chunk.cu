@@ -220,7 +220,7 @@ struct Work {
   int slot;             // where the records of this part of a split unit go (-1: whole)
   int q0, rows;         // row of its first query in q and out; rows of A, its queries' heads
   int pos0;             // position of that query (may be negative)
-  int limit;            // positions that may be read
+  int limit;            // positions that its last query sees: what stands behind them need not have been stored
   int tile0, tiles;     // steps of 128 positions: [tile0, tile0 + tiles)
   int zero0, zeros;     // queries that nobody serves
 };
@@ -331,7 +331,6 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       w.seq = seq;
       w.h = h;
       w.slot = parts > 1 ? (unit - full) * parts + part : -1;
-      w.limit = min(raw_len, min(a.max_seq_len, a.cap));
       const int served = min(n, a.max_q_len);
       w.zero0 = qs + served;
       w.zeros = tile_q == 0 && part == 0 ? n - served : 0;   // queries past max_q_len
@@ -340,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
       w.q0 = qs + tile_q * per;
       w.rows = min(per, served - tile_q * per) * a.group;
       w.pos0 = raw_len - n + tile_q * per;
-      const int seen = min(w.pos0 + min(per, served - tile_q * per), w.limit);   // positions that the last query sees
-      const int all_tiles = seen > 0 ? (seen + kCols - 1) / kCols : 0;
+      w.limit = max(min(w.pos0 + min(per, served - tile_q * per), min(a.max_seq_len, a.cap)), 0);
+      const int all_tiles = (w.limit + kCols - 1) / kCols;
       const int each = parts > 1 ? max((all_tiles + parts - 1) / parts, 2) : all_tiles;   // steps of a part
       w.tile0 = min(part * each, all_tiles);
       w.tiles = min(each, all_tiles - w.tile0);
