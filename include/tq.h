@@ -573,6 +573,10 @@ size_t tq_b8_continue_workspace_size(const tq_config* cfg, int batch, int total_
 /* Device. Causal attention of chunks of queries whose keys and values are
  * already stored, as tq_continue: query i of a chunk of q_len sits at position
  * seq_lens[b] - q_len + i and sees positions 0 .. that one.
+ * The weights are rounded to fp16 (by 2^-11) where out is f16 or bf16, and held
+ * in two fp16 parts (2^-22), as tq_b8_decode does, where it is f32. What a query
+ * gives does not depend on what is cached behind its position. Scores: see
+ * tq_b8_decode.
  *   q, q_stride, q_dtype, out, out_dtype
  *              as for tq_b8_decode, [total_q][n_q][d]; rows from
  *              query_start[batch] to total_q are neither read nor written; a

@@ -867,6 +867,31 @@ def test_continue_rows_that_were_not_stored(tq, block, hist, q_len, max_q):
     check_rows(c, q, got, [0, max_q], [kept], rows=12)
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("group", [1, 4, 7])
+@pytest.mark.parametrize("hist", [0, 640])
+def test_continue_f32_output_has_weights_to_match(tq, fmt, group, hist):
+    """Two fp16 parts a weight, as the decode's: the bound without a rounding to fp16.
+    Short rows of small scores, where that is the largest term. The exponents: log2 of
+    the value scales (of magnitude 8 to 16, off by 2 units of the last place: 2^-19),
+    their differences and the reference's moves below that: 2^-17 together."""
+    q_lens = [2, 3, 5, 8, 12] * 4
+    lens = [x + (hist if i == 7 else 0) for i, x in enumerate(q_lens)]
+    c = Case(tq, fmt, 16, group, 1, lens, seed=95).fill(lens)
+    starts = starts_of(q_lens)
+    q = c.draw(int(starts[-1]), group, gain=0.05)
+    got = run_continue(c, q, starts, lens)
+    for b, n in enumerate(lens):
+        k, v = c.kv(b)
+        floor = c.floor(b, n, chunks=True)
+        for i in range(q_lens[b]):
+            seen = n - q_lens[b] + i + 1
+            ref, size, reach = o8.attend(q[starts[b] + i].double().numpy(), k[:seen], v[:seen], SCALE)
+            tol = tolerance(ref, size, reach, seen, "f32", floor + size * 2.0 ** -17)
+            err = np.abs(got[starts[b] + i] - ref)
+            assert np.all(err <= tol), (b, i, seen, float((err / tol).max()))
+
+
 # ---------------------------------------------------------------- together
 
 

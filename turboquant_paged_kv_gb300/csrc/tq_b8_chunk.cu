@@ -20,7 +20,13 @@
 // see or gives no weight (one sigma for a step, from its largest s_v, took 0 for
 // rows whose own values were 2^-28 of that), and no later position changes a bit
 // of a row. P is rounded to fp16: half a step is 2^-11, and no step below 2^-24
-// errs by up to 2^-28 of the row's largest p s_v, for each code.
+// errs by up to 2^-28 of the row's largest p s_v, for each code. With f32 output P
+// is held in two fp16 parts (hi + lo, 2^-22), as in the decode, and its product
+// takes twice the instructions: the two cases below with f32 output 259 -> 302 and
+// 694 -> 815 us, their errors against 64 bits 2.1e-4 -> 0.9e-5 and 1.4e-5 (what is
+// left is the tensor cores' sum over the positions). With fp16 output the one part
+// adds 2.1e-4 to the output's own rounding of 2.1e-4 (together 2.9e-4), with bf16
+// nothing to its 1.7e-3.
 //
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1 (a thread a row, no
 // shuffles), 8-11 expand codes from global memory into the two-stage fp16
@@ -164,6 +170,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[16]) { tmem_ld16(addr, r); }
+__device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { tmem_ld32(addr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16]) { tmem_st16(addr, r); }
+__device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) { tmem_st32(addr, r); }
+
 template <typename TO>
 __device__ __forceinline__ void write4(TO* dst, float4 v) {
   if constexpr (std::is_same<TO, float>::value) {
@@ -254,6 +265,7 @@ __device__ __forceinline__ void expand_rows(const uint4 x, uint32_t row_at, int 
 
 template <typename TQ, typename TO, bool INT8>
 __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs a) {
+  constexpr bool kTwo = std::is_same<TO, float>::value;   // P in two fp16 parts
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Work s_work;
@@ -495,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
           const float2 g0 = s_groups[warp][2 * c], g1 = s_groups[warp][2 * c + 1];
           // never 0, which would make NaN of a masked place; below 2^-126 the scores vanish anyway (|s| < 2^31)
           const float f0 = fmaxf(g0.x * down, 0x1p-126f), f1 = fmaxf(g1.x * down, 0x1p-126f);
-          uint32_t p[16];
+          uint32_t p[kTwo ? 32 : 16];   // the hi parts, then the lo parts
           float next;   // `sums` with these columns
           for (int go = 0;; ++go) {
             const float d0 = fmaxf(g0.y - sigma, kLeast), d1 = fmaxf(g1.y - sigma, kLeast);
@@ -511,8 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
               y1.y = ex2(y1.y);
               x0 = add2(x0, y0);
               x1 = add2(x1, y1);
-              p[j / 2] = pack_half2(y0.x, y0.y);
-              p[8 + j / 2] = pack_half2(y1.x, y1.y);
+              if constexpr (kTwo) {
+                split_half2(y0.x, y0.y, p[j / 2], p[16 + j / 2]);
+                split_half2(y1.x, y1.y, p[8 + j / 2], p[24 + j / 2]);
+              } else {
+                p[j / 2] = pack_half2(y0.x, y0.y);
+                p[8 + j / 2] = pack_half2(y1.x, y1.y);
+              }
             }
             const float sum0 = x0.x + x0.y, sum1 = x1.x + x1.y;
             next = fmaf(sum1, ex2(-d1), fmaf(sum0, ex2(-d0), sums));
@@ -537,19 +554,26 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
             wait_st();
 #pragma unroll 1
             for (int d = 0; d < c; ++d) {   // the P of this step that are there already
-              uint32_t q[16];
-              tmem_ld16(t_s + 16 * d, q);
+              uint32_t q[kTwo ? 32 : 16];
+              tmem_ld(t_s + 32 * d, q);
               wait_ld();
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                const float2 y = half2_to_float2(q[j]);
-                q[j] = pack_half2(y.x * e, y.y * e);
+                float2 y = half2_to_float2(q[j]);
+                if constexpr (kTwo) {
+                  const float2 lo = half2_to_float2(q[16 + j]);
+                  y.x += lo.x;
+                  y.y += lo.y;
+                  split_half2(y.x * e, y.y * e, q[j], q[16 + j]);
+                } else {
+                  q[j] = pack_half2(y.x * e, y.y * e);
+                }
               }
-              tmem_st16(t_s + 16 * d, q);
+              tmem_st(t_s + 32 * d, q);
             }
           }
           sums = next;
-          tmem_st16(t_s + 16 * c, p);
+          tmem_st(t_s + 32 * c, p);   // where these columns of S stood
         }
         l += sums;
         if (__builtin_expect(i > 0 && __any_sync(0xffffffffu, by_o != 1.f), 0)) {
@@ -682,7 +706,11 @@ __global__ void __launch_bounds__(kThreads, 1) b8_chunk_kernel(const B8ChunkArgs
             const uint32_t d = tmem + kColO + t * 128, p = tmem + kColS + t * 128;
             mma_ts(d, p, v_at, kIdescPV, i > 0);
 #pragma unroll
-            for (int k = 1; k < 8; ++k) mma_ts(d, p + 8 * k, v_at + (2048 >> 4) * k, kIdescPV, true);
+            for (int k = 0; k < 8; ++k) {   // 16 positions: 8 columns, 32 apart for each 32 positions
+              const uint32_t at = p + 32 * (k >> 1) + 8 * (k & 1);
+              if (k > 0) mma_ts(d, at, v_at + (2048 >> 4) * k, kIdescPV, true);
+              if constexpr (kTwo) mma_ts(d, at + 16, v_at + (2048 >> 4) * k, kIdescPV, true);
+            }
             if (!more) mma_commit(bar(kODone0 + t));
           }
           __syncwarp();
