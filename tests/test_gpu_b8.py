@@ -892,6 +892,72 @@ def test_continue_f32_output_has_weights_to_match(tq, fmt, group, hist):
             assert np.all(err <= tol), (b, i, seen, float((err / tol).max()))
 
 
+_CONTEXT_CHILD = """
+import ctypes, importlib.util, sys
+import numpy as np
+spec = importlib.util.spec_from_file_location("abi", sys.argv[1])
+abi = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(abi)
+lib, rt = abi.load(), ctypes.CDLL("libcudart.so.13")     # the runtime that the library is linked to
+batch, n_q, n_kv, n = 2, 8, 2, 300
+cfg = abi.tq_config(abi.TQ_PRESET_INT8_BLK, 128, 16, n_q, n_kv, 0, 0)
+lay = abi.tq_b8_layout()
+assert lib.tq_b8_layout_for(ctypes.byref(cfg), ctypes.byref(lay)) == 0
+rng = np.random.default_rng(1)
+f16 = lambda *shape: rng.standard_normal(shape).astype(np.float16)
+host = dict(k=f16(batch * n, n_kv, 128), v=f16(batch * n, n_kv, 128), q=f16(batch * n, n_q, 128),
+            starts=np.array([0, n, 2 * n], dtype=np.int32), lens=np.array([n, n], dtype=np.int32),
+            table=np.arange(38, dtype=np.int32).reshape(2, 19))
+ws = max(lib.tq_b8_decode_workspace_size(ctypes.byref(cfg), batch, n),
+         lib.tq_b8_continue_workspace_size(ctypes.byref(cfg), batch, batch * n, n, n))
+sizes = dict(cache=38 * lay.block_bytes, ws=ws, one=batch * n_q * 512, many=batch * n * n_q * 512)
+
+def once():
+    d = {}
+    for name, size in [*((k, x.nbytes) for k, x in host.items()), *sizes.items()]:
+        d[name] = ctypes.c_void_p()
+        assert rt.cudaMalloc(ctypes.byref(d[name]), ctypes.c_size_t(size)) == 0
+        assert rt.cudaMemset(d[name], 0, ctypes.c_size_t(size)) == 0
+    for name, x in host.items():
+        assert rt.cudaMemcpy(d[name], ctypes.c_void_p(x.ctypes.data), ctypes.c_size_t(x.nbytes), 1) == 0
+    status = [lib.tq_b8_store(ctypes.byref(cfg), d["k"], 0, d["v"], 0, 0, d["starts"], batch, 2 * n, n, d["cache"], 38, d["table"], 19,
+                              d["lens"], None, None),
+              lib.tq_b8_decode(ctypes.byref(cfg), d["q"], 0, 0, d["cache"], 38, d["table"], 19, d["lens"], batch, n, 0.0, d["one"], 2,
+                               d["ws"], ws, None, None),
+              lib.tq_b8_continue(ctypes.byref(cfg), d["q"], 0, 0, d["starts"], batch, 2 * n, n, d["cache"], 38, d["table"], 19,
+                                 d["lens"], n, 0.0, d["many"], 2, d["ws"], ws, None, None)]
+    out = []
+    for name in ("one", "many"):
+        x = np.empty(sizes[name] // 4, dtype=np.float32)
+        assert rt.cudaMemcpy(ctypes.c_void_p(x.ctypes.data), d[name], ctypes.c_size_t(x.nbytes), 2) == 0
+        out.append(x)
+    return status, out
+
+status, first = once()
+assert status == [0, 0, 0] and all(x.any() and np.isfinite(x).all() for x in first), status
+if sys.argv[2] == "reset":
+    assert rt.cudaDeviceReset() == 0
+else:
+    cu, ctx = ctypes.CDLL("libcuda.so.1"), ctypes.c_void_p()
+    assert cu.cuCtxCreate_v2(ctypes.byref(ctx), 0, 0) == 0       # and made current
+status, second = once()
+assert status == [0, 0, 0], status
+assert all(np.array_equal(x, y) for x, y in zip(first, second))
+print("same")
+"""
+
+
+@pytest.mark.parametrize("how", ["reset", "another"])
+def test_calls_in_a_context_after_the_first(tq, how):
+    """A process of its own whose CUDA context ends and begins anew, or is left for
+    another one of the same device: nothing is remembered of the first."""
+    import subprocess
+    import sys
+    from turboquant_paged_kv_gb300 import _abi
+    run = subprocess.run([sys.executable, "-c", _CONTEXT_CHILD, _abi.__file__, how], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.strip() == "same", run.stdout + run.stderr
+
+
 # ---------------------------------------------------------------- together
 
 

@@ -136,7 +136,8 @@ inline tq_status b8_stride(long long* stride, long long row) {
   return *stride < row || *stride % 8 ? TQ_ERR_INVALID_ARG : TQ_OK;
 }
 // What a device is asked for once: its SM count, and that a kernel may take `smem`
-// bytes of dynamic shared memory (`done`: a bit a device, one word a kernel).
+// bytes of dynamic shared memory (`done`: a bit a device, one word a kernel). The
+// runtime keeps the latter for the device, through a reset and for every context.
 inline cudaError_t b8_current_device(int* dev, int* sms) {
   static std::atomic<int> known[64];
   cudaError_t err = cudaGetDevice(dev);
