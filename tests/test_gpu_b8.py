@@ -958,6 +958,38 @@ def test_calls_in_a_context_after_the_first(tq, how):
     assert run.returncode == 0 and run.stdout.strip() == "same", run.stdout + run.stderr
 
 
+@pytest.mark.parametrize("group", [2, 6])
+@pytest.mark.parametrize("gain", [40, 70, 100, 120, 200])
+@pytest.mark.parametrize("even", [False, True])
+def test_decode_value_scales_as_far_apart_as_they_get(tq, group, gain, even):
+    """Some blocks' values are 2^gain times the others', their keys give them no weight
+    (or one around 2^-gain, so that both kinds count) with even query heads and all of
+    it with odd ones: each head has its own values.
+    Enough tiles for every warp to meet both kinds; all sequences share their blocks."""
+    n, batch = 1600, 64
+    c = Case(tq, "int8_blk", 16, group, 1, [n], seed=23)
+    k, v = c.draw(n, 1).float().numpy(), c.draw(n, 1).float().numpy()
+    big = np.arange(n) // 16 % 5 == 1
+    k[big] = -gain / (128 * SCALE * np.log2(np.e)) if even else -40.0
+    v[big] *= np.float32(2.0 ** (gain // 2))
+    v[~big] *= np.float32(2.0 ** (gain // 2 - gain))
+    o8.store(c.f, c.cache, k, v, [0, n], c.table, [n])
+    c.table = np.repeat(c.table, batch, 0)
+    c.lens = np.full(batch, n, dtype=np.int32)
+    q = torch.ones((batch, group, 128), dtype=torch.bfloat16)
+    q[:, 1::2] = -1.0
+    q *= torch.linspace(0.5, 1.5, batch)[:, None, None].to(torch.bfloat16)
+    got = run_decode(c, q)
+    kk, vv = c.kv(0)
+    for b in range(batch):
+        ref, size, reach = o8.attend(q[b].double().numpy(), kk, vv, SCALE)
+        z = kk[:, 0] @ q[b].double().numpy().T * SCALE
+        # the floor of `tolerance`, and no more than the weight itself, where that is less than a step
+        floor = np.minimum(2.0 ** -24, np.exp(z - z.max(0))).T @ np.abs(vv[:, 0])
+        assert np.all(np.abs(got[b] - ref) <= tolerance(ref, size, reach, n, "f32", floor)), b
+        assert np.all(np.abs(got[b]).max(-1) > 0), b
+
+
 # ---------------------------------------------------------------- together
 
 

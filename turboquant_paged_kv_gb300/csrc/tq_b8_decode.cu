@@ -20,10 +20,11 @@
 //   O^T[128, 8 heads] += V^T . P^T with P = 8 p s_v / sigma in two fp16 parts
 //     (hi + lo, 2^-22 relative, and never more than 2^-25 off: the weight of a
 //     position errs by at most 2^-28 sigma / s_v of the largest). sigma, the
-//     reference of the accumulators, is a block scale met before: it moves (and
-//     the accumulators are rescaled) when a block's s_v leaves [sigma / 16,
-//     16 sigma], so P keeps its bits whatever the blocks' scales are. P stays
-//     below 8 * 2^8 * 16 = 2^15 (2^8: see the softmax).
+//     reference of a head's accumulators, is a block scale met before: it moves
+//     (and the accumulators are rescaled) when a block's s_v leaves [sigma / 16,
+//     16 sigma], so P keeps its bits whatever the blocks' scales are (see
+//     `reference` for scales very far apart). P stays below 8 * 2^8 * 16 = 2^15
+//     (2^8: see the softmax).
 //   With at most 4 heads a pair, columns 4 .. 7 repeat the heads and carry the
 //   lo parts; else the lo parts take a second mma.
 // Softmax in log2 units, the running maximum moving only when a score passes
@@ -163,6 +164,18 @@ __device__ __forceinline__ Place find_tile(const B8SplitArgs& a, long long x, in
   return p;
 }
 
+// The log2 of a head's reference, a whole number: that of the block's value scale,
+// lv, as long as neither side is lost. `had` is the log2 of what the accumulators
+// hold, `comes` that of the block's largest weight times its scale: the
+// accumulators stay below 2^100 and P below 2^15, and P keeps its bits unless it is
+// 2^-16 of what is there. Both in units of the output, so 2^-120 is low enough.
+__device__ __forceinline__ float reference(float lv, float had, float comes) {
+  const float least = fmaxf(had - 100.f, comes - 12.f), most = fmaxf(comes + 6.f, had - 10.f);
+  return fmaxf(rintf(fminf(fmaxf(lv, least), most)), -120.f);
+}
+// 2^x, x whole, -126 <= x <= 127
+__device__ __forceinline__ float power_of_2(float x) { return __int_as_float((static_cast<int>(x) + 127) << 23); }
+
 template <typename TQ, bool INT8, bool WIDE>
 __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitArgs a) {
   extern __shared__ __align__(128) uint8_t s_ring[];
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
   uint32_t qf[16];           // the query heads as the B operand: k-step s, coordinates 32 t + 4 s .. + 3 of head g (or g & 3)
   float qs0 = 0.f, qs1 = 0.f;  // scale of heads 2 t, 2 t + 1 (mod 4 unless WIDE)
   float acc[8][4];           // O^T: coordinates 16 g + 2 j, + 1 (rows) x heads 2 t, 2 t + 1
-  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, sigma = 0.f, inv_sigma = 0.f, sigma_max = 0.f;
+  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f, sigma0 = 0.f, sigma1 = 0.f, inv0 = 0.f, inv1 = 0.f;   // sigma: log2 of the reference, a whole number; inv: 8 / 2^sigma
   bool fresh = true;
   int stage = 0;
   for (; todo > 0; --todo) {
@@ -270,7 +283,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
       for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
       m0 = m1 = -1e30f;
       l0 = l1 = 0.f;
-      sigma = inv_sigma = sigma_max = 0.f;   // no reference yet
+      sigma0 = sigma1 = inv0 = inv1 = 0.f;   // no reference yet
     }
 
     cp_wait<kStages - 2>();
@@ -305,46 +318,79 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
         if (g + 8 >= left) x10 = x11 = -INFINITY;
       }
       const float t0 = fmaxf(x00, x10), t1 = fmaxf(x01, x11);
-      float rv = s_v * inv_sigma;
+      float rv0 = s_v * inv0, rv1 = s_v * inv1, far0 = 0.f, far1 = 0.f;
+      bool far = false;
       const bool grow = t0 > m0 + kStep || t1 > m1 + kStep;
-      const bool move = !(rv <= 8.f * 16.f && rv >= 8.f * 0.0625f);
-      if (__any_sync(0xffffffffu, grow) || move) {
+      const bool move = !(fmaxf(rv0, rv1) <= 8.f * 16.f && fminf(rv0, rv1) >= 8.f * 0.0625f);
+      if (__any_sync(0xffffffffu, grow || move)) {
         float u0 = fmaxf(m0, t0), u1 = fmaxf(m1, t1);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
           u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
           u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
         }
-        float e0 = ex2(m0 - u0), e1 = ex2(m1 - u1);
+        const float by0 = m0 - u0, by1 = m1 - u1;
         m0 = u0;
         m1 = u1;
-        l0 *= e0;
-        l1 *= e1;
-        if (move) {   // never below 2^-64 of the largest reference: what the accumulators hold stays finite
-          sigma_max = fmaxf(sigma_max, s_v);
-          const float next = fmaxf(s_v, sigma_max * 0x1p-64f);
-          const float by = sigma / next;
-          sigma = next;
-          inv_sigma = 8.f / next;
-          rv = s_v * inv_sigma;
-          e0 *= by;
-          e1 *= by;
+        l0 *= ex2(by0);
+        l1 *= ex2(by1);
+        float n0 = sigma0, n1 = sigma1;
+        if (__any_sync(0xffffffffu, move)) {
+          float a0 = 0.f, a1 = 0.f, v0 = t0, v1 = t1;   // a head's largest accumulator and its largest score here
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            a0 = fmaxf(a0, fmaxf(fabsf(acc[j][0]), fabsf(acc[j][2])));
+            a1 = fmaxf(a1, fmaxf(fabsf(acc[j][1]), fabsf(acc[j][3])));
+          }
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) {
+            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, o));
+            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, o));
+            v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, o));
+            v1 = fmaxf(v1, __shfl_xor_sync(0xffffffffu, v1, o));
+          }
+          if constexpr (!WIDE) {
+            a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, 2));
+            a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, 2));
+          }
+          const float lv = __log2f(s_v);
+          n0 = reference(lv, __log2f(a0) + sigma0 + by0, v0 - u0 + lv);
+          n1 = reference(lv, __log2f(a1) + sigma1 + by1, v1 - u1 + lv);
+          inv0 = power_of_2(3.f - n0);
+          inv1 = power_of_2(3.f - n1);
+          far0 = fmaxf(rintf(lv) - n0 - 60.f, 0.f);
+          far1 = fmaxf(rintf(lv) - n1 - 60.f, 0.f);
+          far = __any_sync(0xffffffffu, far0 + far1 > 0.f);
+          rv0 = s_v * power_of_2(3.f - n0 - far0);
+          rv1 = s_v * power_of_2(3.f - n1 - far1);
         }
+        // 2^(by + sigma - n) in two factors: either alone may pass what fp32 holds
+        const float d0 = sigma0 - n0, d1 = sigma1 - n1, h0 = floorf(0.5f * d0), h1 = floorf(0.5f * d1);
+        const float f0a = ex2(0.5f * by0 + h0), f0b = ex2(0.5f * by0 + (d0 - h0));
+        const float f1a = ex2(0.5f * by1 + h1), f1b = ex2(0.5f * by1 + (d1 - h1));
+        sigma0 = n0;
+        sigma1 = n1;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          acc[j][0] *= e0;
-          acc[j][1] *= e1;
-          acc[j][2] *= e0;
-          acc[j][3] *= e1;
+          acc[j][0] = acc[j][0] * f0a * f0b;
+          acc[j][1] = acc[j][1] * f1a * f1b;
+          acc[j][2] = acc[j][2] * f0a * f0b;
+          acc[j][3] = acc[j][3] * f1a * f1b;
         }
       }
       float p00 = ex2(x00 - m0), p01 = ex2(x01 - m1), p10 = ex2(x10 - m0), p11 = ex2(x11 - m1);
       l0 += p00 + p10;
       l1 += p01 + p11;
-      p00 *= rv;
-      p01 *= rv;
-      p10 *= rv;
-      p11 *= rv;
+      if (__builtin_expect(far, 0)) {   // small weights of large values: p alone may vanish
+        p00 = ex2((x00 - m0) + far0);
+        p10 = ex2((x10 - m0) + far0);
+        p01 = ex2((x01 - m1) + far1);
+        p11 = ex2((x11 - m1) + far1);
+      }
+      p00 *= rv0;
+      p01 *= rv1;
+      p10 *= rv0;
+      p11 *= rv1;
       uint32_t h0, h1, e0, e1;
       split_half2(p00, p01, h0, e0);
       split_half2(p10, p11, h1, e1);
@@ -400,9 +446,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int head = 2 * t + k;
-        const float l = k ? l1 : l0, m = k ? m1 : m0;
+        const float l = k ? l1 : l0, m = k ? m1 : m0, sigma = k ? sigma1 : sigma0;
         if (head < a.group) {
-          const float f = l > 0.f ? 0.125f * sigma / l : (l == 0.f ? 0.f : l);   // NaN stays
+          const float f = l > 0.f ? power_of_2(sigma - 3.f) / l : (l == 0.f ? 0.f : l);   // NaN stays
           float4* o = reinterpret_cast<float4*>(a.rec_o + (rec + head) * kB8D + 16 * g);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
