@@ -23,7 +23,7 @@
 // errs by up to 2^-28 of the row's largest p s_v, for each code. With f32 output P
 // is held in two fp16 parts (hi + lo, 2^-22), as in the decode, and its product
 // takes twice the instructions: the two cases below with f32 output 259 -> 302 and
-// 694 -> 815 us, their errors against 64 bits 2.1e-4 -> 0.9e-5 and 1.4e-5 (what is
+// 695 -> 815 us, their errors against 64 bits 2.1e-4 -> 0.9e-5 and 1.4e-5 (what is
 // left is the tensor cores' sum over the positions). With fp16 output the one part
 // adds 2.1e-4 to the output's own rounding of 2.1e-4 (together 2.9e-4), with bf16
 // nothing to its 1.7e-3.
@@ -45,13 +45,15 @@
 // Bound: tensor cores by its operations; measured, the softmax's latency beside
 // them. A step of 256 rows x 128 positions is 32 products of 64 cycles (2240
 // cycles with their commits) and takes about 3600: 7500 warp instructions, and
-// the shared-memory pipe nine tenths busy (operands, codes, tensor-memory
-// traffic). 4 chunks of about 2000 queries over up to 8192 positions, 32 query
-// heads: 695 us, 1219 TFLOP/s, 0.63 of a measured bf16 GEMM; 32 chunks of 128
-// over 4096: 257 us, 1083 TFLOP/s. What moved it: products issued from uniform
-// registers (from a branch that one lane takes, each cost 75 to 200 cycles), no
-// search for the maximum, and code small enough for the instruction cache (the
-// step's softmax rolled, the prologue and the epilogue short: 823 to 695 us).
+// the shared-memory pipe four fifths busy or more (operands, codes,
+// tensor-memory traffic). 4 chunks of about 2000 queries over up to 8192
+// positions, 32 query heads: 695 us, 1219 TFLOP/s, 0.63 of a measured bf16 GEMM;
+// 32 chunks of 128 over 4096: 259 us, 1078 TFLOP/s. What moved it: products issued
+// from uniform registers (from a branch that one lane takes, each cost 75 to 200
+// cycles), no search for the maximum, and code small enough for the instruction
+// cache (the step's softmax rolled, the prologue and the epilogue short: 823 to
+// 695 us). A reference for each row costs nothing beside one for the step (691 to
+// 696 us against 703): its arithmetic runs while the scores are on their way.
 // Tried and slower: S in halves of 64 positions one half ahead, P handed over in
 // halves, an issuing warp for each tile (both tiles then fall into step), two
 // threads a row, eight expanding warps.
@@ -819,7 +821,9 @@ B8ChunkPlan b8_chunk_plan(const tq_config* cfg, int batch, int total_q, int max_
   p.units = tiles * cfg->num_kv_heads;
   // Splitting pays while the last wave is a good part of all (at most 6 waves), and
   // where the history has steps to split. Measured at 512 units of 33 steps (3.4
-  // waves): 279 us whole, 257 us with the last 56 units in 2 parts.
+  // waves): 279 us whole, 257 us with the last 56 units in 2 parts. The rule counts
+  // units and not their steps: one history of 131072 among 31 of 500, 5 queries each,
+  // takes 1.77 ms, since the units of the long one are walked by one CTA each.
   p.may_split = p.units > 0 && p.units <= 6 * kParts && max_seq_len > 3 * kCols;
   p.part_rows = longest < per ? longest * group : per * group;
   const size_t records = static_cast<size_t>(kParts) * p.part_rows;

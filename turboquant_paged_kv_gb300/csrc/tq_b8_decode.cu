@@ -31,8 +31,8 @@
 // it by 2^8 (one warp vote a tile).
 //
 // Bound: HBM, 256 bytes a (position, head). 4 x 131072 positions of 8 heads, 64
-// query heads: 163.7 us, 6.56 TB/s, 0.98 of a measured copy; 64 sequences of 512
-// to 16384: 189 us, 6.34 TB/s; 32 x 4096: 49 us, 5.5 TB/s, where a warp has 36
+// query heads: 166.5 us, 6.45 TB/s, 0.96 of a measured copy; 64 sequences of 512
+// to 16384: 192 us, 6.23 TB/s; 32 x 4096: 49.7 us, 5.4 TB/s, where a warp has 36
 // tiles only and the start (lengths, block ids, first tiles, one after another)
 // and the merge (3.4 us) show. A warp copies its own tiles (cp.async, 4 in a
 // ring): 12 warps with 4 tiles each took 49.3 us there, 10 with 5 52.1, 8 with 6
