@@ -67,7 +67,11 @@ typedef enum {
                              entry points below, its own key cache)          */
   TQ_PRESET_E4M3_BLK = 5, /* K and V: e4m3 with one fp32 scale per (block, KV head)
                              (the tq_b8_* entry points below, their own cache) */
-  TQ_PRESET_INT8_BLK = 6  /* K and V: int8 (-127 .. 127), scales as above      */
+  TQ_PRESET_INT8_BLK = 6, /* K and V: int8 (-127 .. 127), scales as above      */
+  TQ_PRESET_KV_BF16 = 7,  /* K and V as they are, bf16: the layers that stay
+                             unquantised (the tq_kv16_* entry points below,
+                             their own cache)                                */
+  TQ_PRESET_KV_F16 = 8    /* the same in fp16                                */
 } tq_preset;
 
 typedef enum { TQ_DTYPE_F16 = 0, TQ_DTYPE_BF16 = 1, TQ_DTYPE_F32 = 2 } tq_dtype;
@@ -78,7 +82,7 @@ typedef enum { TQ_DTYPE_F16 = 0, TQ_DTYPE_BF16 = 1, TQ_DTYPE_F32 = 2 } tq_dtype;
 #define TQ_DEV_SEQ_TOO_LONG       4u  /* decode: seq_len > max_seq_len or > row cap */
 #define TQ_DEV_TIMEOUT            8u  /* decode: a bounded wait on a copy expired, or the
                                          launch's shared-memory plan did not fit */
-#define TQ_DEV_NOT_FINITE        16u  /* tq_b8_store: an infinity or a NaN among the inputs */
+#define TQ_DEV_NOT_FINITE        16u  /* tq_b8_store, tq_kv16_append: an infinity or a NaN among the keys or values */
 
 /* Problem description shared by store and decode. */
 typedef struct {
@@ -595,6 +599,115 @@ tq_status tq_b8_continue(const tq_config* cfg, const void* q, long long q_stride
                          void* out, int out_dtype, void* workspace, size_t workspace_bytes,
                          unsigned int* dev_status, tq_stream_t stream);
 
+/* ---- 16-bit cache ----------------------------------------------------------
+ * Keys and values as they are, for the layers of a model that are left
+ * unquantised beside those of the other caches ([vLLM-TQ] leaves the first and
+ * the last ones so), with the position rotation of queries and keys applied on
+ * the way in.
+ *   TQ_PRESET_KV_BF16, TQ_PRESET_KV_F16   the type of keys, values and queries
+ * The tq_kv16_* entry points use cfg->head_dim (128), block_size (16, 32, 64 or
+ * 128), num_kv_heads (at most 4096), num_q_heads (n_q % n_kv == 0 and
+ * n_q / n_kv <= 8) and flags (TQ_FLAG_INDICES_READY, which tq_kv16_decode alone
+ * heeds); partition_tokens must be 0.
+ *
+ * Cache: cache[num_blocks] of block_bytes each, [n_kv][block_size / 16] tiles of
+ * tile_bytes. A tile holds 16 positions of one KV head: 16 key rows at k_off, 16
+ * value rows at v_off, each as [2 groups of 8 rows][2 halves of 64 coordinates]
+ * [8 rows][128 bytes], where the 16-byte group c of row r's half stands at group
+ * c ^ (r & 7): 1024-byte pieces in the 128-byte swizzle that the tensor cores
+ * read, so that a tile goes from memory into an operand by a plain copy.
+ * Coordinate j of row r is at (r >> 3) * 2048 + (j >> 6) * 1024 + (r & 7) * 128 +
+ * 16 * ((j >> 3 & 7) ^ (r & 7)) + 2 * (j & 7). Position p of sequence b is in
+ * block block_table[b][p / block_size], row p % block_size.
+ *
+ * The cache holds finite numbers: tq_kv16_append sees to it for what it writes,
+ * and what stands behind a sequence's end is not used, whatever it is. (An
+ * infinity or a NaN that is put there in another way, among the values of a
+ * position that a chunk sees, may reach all queries of that chunk.) */
+typedef struct {
+  int is_bf16;
+  int tile_tokens;         /* 16 */
+  int tile_bytes;          /* 8192 */
+  int k_off, v_off;        /* 0, 4096 */
+  long long block_bytes;
+} tq_kv16_layout;
+
+/* Host. The layout of cfg's 16-bit cache (num_q_heads is not used). */
+tq_status tq_kv16_layout_for(const tq_config* cfg, tq_kv16_layout* out);
+
+/* How tq_kv16_append pairs the rot_dim rotated coordinates of a head. */
+typedef enum {
+  TQ_ROPE_HALVES = 0,   /* j with j + rot_dim / 2 */
+  TQ_ROPE_PAIRS = 1     /* 2 j with 2 j + 1       */
+} tq_rope_style;
+
+/* Device. Rotates queries and keys by their positions and writes keys and values
+ * into the cache. Rows query_start[b] .. query_start[b + 1] - 1 are the last
+ * positions of sequence b: row query_start[b] + i is position
+ * p = seq_lens[b] - q_len + i. With c = cos_sin[p][j], s = cos_sin[p][rot_dim / 2 + j]
+ * the pair (x, y) number j becomes (x c - y s, y c + x s); coordinates from
+ * rot_dim on stay. Computed in fp32 and rounded once. Keys and values that are
+ * not finite then (the largest numbers may outgrow their type) are stored as the
+ * largest finite number of their sign, NaN as 0, with TQ_DEV_NOT_FINITE; queries
+ * stay what they become.
+ *   key, value    device [total_q][n_kv][d] of the cache's type, 16-byte aligned;
+ *                 rows key_stride / value_stride elements apart (0: n_kv * d; else
+ *                 >= n_kv * d and a multiple of 8)
+ *   q, q_out      device [total_q][n_q][d] of the cache's type, 16-byte aligned,
+ *                 strides as above for n_q; q_out may be q (with the same stride)
+ *                 and overlaps nothing else. Both NULL: no queries
+ *   cos_sin       device fp32 [num_positions][rot_dim], 16-byte aligned; NULL with
+ *                 rot_dim 0: no rotation, q_out is a copy
+ *   rot_dim       0 or a multiple of 16 up to d
+ *   rope_style    tq_rope_style (not looked at with rot_dim 0)
+ *   query_start   device int32 [batch + 1], non-decreasing from 0; rows from
+ *                 query_start[batch] to total_q are neither read nor written
+ *   block_table, bt_stride, seq_lens
+ *                 as for tq_b8_store: lengths WITH the chunk
+ * Not stored: rows before position 0, positions past bt_stride * block_size and,
+ * with a rotation, from num_positions on (TQ_DEV_SEQ_TOO_LONG), and those of a
+ * block id outside [0, num_blocks) (TQ_DEV_BLOCK_OUT_OF_RANGE). Queries of
+ * positions before 0 or, with a rotation, from num_positions on are not written.
+ * A block that is written belongs to one sequence of the batch alone. batch or
+ * total_q == 0 is a no-op. One launch, no workspace. */
+tq_status tq_kv16_append(const tq_config* cfg, const void* key, long long key_stride,
+                         const void* value, long long value_stride,
+                         const void* q, long long q_stride, void* q_out, long long q_out_stride,
+                         const float* cos_sin, int rot_dim, int num_positions, int rope_style,
+                         const int* query_start, int batch, int total_q,
+                         void* cache, long long num_blocks,
+                         const int* block_table, int bt_stride, const int* seq_lens,
+                         unsigned int* dev_status, tq_stream_t stream);
+
+/* Host. Bytes of workspace of tq_kv16_decode. 0 on bad input. */
+size_t tq_kv16_decode_workspace_size(const tq_config* cfg, int batch, int max_seq_len);
+
+/* Device. Attention of one query per sequence over its seq_lens[b] cached
+ * positions: arguments, empty sequences, bad block ids and scores as for
+ * tq_b8_decode. q is of the cache's type. */
+tq_status tq_kv16_decode(const tq_config* cfg, const void* q, long long q_stride,
+                         const void* cache, long long num_blocks,
+                         const int* block_table, int bt_stride,
+                         const int* seq_lens, int batch, int max_seq_len, float scale,
+                         void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                         unsigned int* dev_status, tq_stream_t stream);
+
+/* Host. Bytes of workspace of tq_kv16_continue for the same sizes. 0 on bad
+ * input. */
+size_t tq_kv16_continue_workspace_size(const tq_config* cfg, int batch, int total_q, int max_q_len,
+                                       int max_seq_len);
+
+/* Device. Causal attention of chunks of queries whose keys and values are
+ * already stored: arguments and rules as for tq_b8_continue. q is of the cache's
+ * type. What a query gives does not depend on what is cached behind its position. */
+tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stride,
+                           const int* query_start, int batch, int total_q, int max_q_len,
+                           const void* cache, long long num_blocks,
+                           const int* block_table, int bt_stride,
+                           const int* seq_lens, int max_seq_len, float scale,
+                           void* out, int out_dtype, void* workspace, size_t workspace_bytes,
+                           unsigned int* dev_status, tq_stream_t stream);
+
 /* Host. Static description of a status code. */
 const char* tq_status_string(int status);
 
@@ -603,7 +716,7 @@ int tq_version(void);
 
 #define TQ_ABI_VERSION 105   /* 1.01: tq_dequant; 1.02: 3bit_nc runs; 1.03: TurboQuant_prod (tq_prod_*);
                                  1.04: tq_continue; 1.05: tq_decode_append
-                                 (tq_b8_*: added since, nothing else changed) */
+                                 (tq_b8_*, tq_kv16_*: added since, nothing else changed) */
 
 #ifdef __cplusplus
 }

@@ -15,10 +15,11 @@ import functools
 import torch
 
 from . import _abi
-from ._abi import (PRESET_IDS, TQ_DEV_BLOCK_OUT_OF_RANGE, TQ_DEV_SEQ_TOO_LONG,  # noqa: F401
+from ._abi import (PRESET_IDS, ROPE_STYLES, TQ_DEV_BLOCK_OUT_OF_RANGE, TQ_DEV_SEQ_TOO_LONG,  # noqa: F401
                    TQ_DECODE_NOALLOC_SCRATCH_BYTES, TQ_DEV_SLOT_OUT_OF_RANGE, TQ_DEV_TIMEOUT, TQ_DEV_NOT_FINITE,
                    TQ_DTYPE_BF16, TQ_DTYPE_F16, TQ_DTYPE_F32, TQ_ERR_WORKSPACE_TOO_SMALL,
-                   TQError, tq_b8_layout, tq_codebook, tq_config, tq_layout, tq_prod_layout)
+                   TQError, tq_b8_layout, tq_codebook, tq_config, tq_kv16_layout, tq_layout, tq_prod_layout,
+                   TQ_PRESET_KV_BF16, TQ_ROPE_HALVES, TQ_ROPE_PAIRS)
 
 
 
@@ -39,6 +40,8 @@ __all__ = ["make_config", "tq_build_codebook", "tq_layout_for", "tq_store", "tq_
            "tq_prod_scores", "tq_continue_workspace_size", "tq_continue",
            "tq_b8_layout_for", "tq_b8_store", "tq_b8_dequant", "tq_b8_decode_workspace_size", "tq_b8_decode",
            "tq_b8_continue_workspace_size", "tq_b8_continue",
+           "tq_kv16_layout_for", "tq_kv16_append", "tq_kv16_decode_workspace_size", "tq_kv16_decode",
+           "tq_kv16_continue_workspace_size", "tq_kv16_continue",
            "tq_status_string",
            "tq_version", "TQError", "lib_path"]
 
@@ -284,10 +287,10 @@ def _b8_rows(name: str, t: torch.Tensor, heads: int, d: int) -> int:
 
 
 def _b8_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: torch.Tensor, seq_lens: torch.Tensor,
-               others, stream) -> tuple:
-    """What every call on the cache has in common: index tensors, one device, the
-    current one (the library launches there), and the cache's size. Returns
-    (num_blocks, row length of the table, raw stream)."""
+               others, stream, block_bytes=None) -> tuple:
+    """What every call on the cache (8 or 16 bits) has in common: index tensors, one
+    device, the current one (the library launches there), and the cache's size.
+    Returns (num_blocks, row length of the table, raw stream)."""
     if cache.dtype != torch.uint8 or not cache.is_contiguous():
         raise ValueError("cache must be a contiguous uint8 tensor")
     if block_table.dtype != torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
@@ -311,7 +314,7 @@ def _b8_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: tor
         raise ValueError("the stream must be one of the tensors' device")
     else:
         raw = stream.cuda_stream
-    have = cache.numel() // _b8_block_bytes(cfg.preset, cfg.head_dim, cfg.block_size, cfg.num_kv_heads)
+    have = cache.numel() // (block_bytes or _b8_block_bytes)(cfg.preset, cfg.head_dim, cfg.block_size, cfg.num_kv_heads)
     if num_blocks is None:
         num_blocks = have
     elif num_blocks > have:
@@ -427,3 +430,114 @@ def tq_b8_continue(cfg: tq_config, q: torch.Tensor, query_start: torch.Tensor, m
                              _b8_workspace(workspace), _b8_status(dev_status), raw)
     if st:
         raise TQError("tq_b8_continue", st)
+
+
+# ---- 16-bit cache, with the position rotation on the way in (kv_bf16, kv_fp16) --
+
+def tq_kv16_layout_for(cfg: tq_config) -> tq_kv16_layout:
+    lay = tq_kv16_layout()
+    _abi.check("tq_kv16_layout_for", _LIB.tq_kv16_layout_for(ctypes.byref(cfg), ctypes.byref(lay)))
+    return lay
+
+
+@functools.lru_cache(maxsize=256)
+def _kv16_block_bytes(preset: int, head_dim: int, block_size: int, num_kv_heads: int) -> int:
+    return tq_kv16_layout_for(make_config(preset, num_kv_heads, num_kv_heads, head_dim, block_size)).block_bytes
+
+
+def _kv16_rows(name: str, t: torch.Tensor, cfg: tq_config, heads: int) -> int:
+    """As _b8_rows, of the cache's own type."""
+    if t.dtype != (torch.bfloat16 if cfg.preset == TQ_PRESET_KV_BF16 else torch.float16):
+        raise ValueError(f"{name} must have the cache's type, got {t.dtype}")
+    return _b8_rows(name, t, heads, cfg.head_dim)
+
+
+def tq_kv16_append(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query_start: torch.Tensor, cache: torch.Tensor,
+                   block_table: torch.Tensor, seq_lens: torch.Tensor, cos_sin: torch.Tensor | None = None,
+                   style: str = "halves", q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                   num_blocks: int | None = None, dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Rotate chunks of new tokens by their positions and write them into the
+    cache: key, value [total_q, n_kv, d], rows query_start[b] .. query_start[b + 1]
+    - 1 become the last positions of sequence b, seq_lens [batch] int32 are the
+    lengths with the chunk. cos_sin [positions, rot_dim] float32 (rot_dim / 2
+    cosines, then as many sines) pairs a head's first rot_dim coordinates as
+    `style` says, "halves" or "pairs"; None: no rotation. q [total_q, n_q, d] is
+    rotated into q_out (which may be q). Rows may be a stride apart."""
+    ks = _kv16_rows("key", key, cfg, cfg.num_kv_heads)
+    vs = _kv16_rows("value", value, cfg, cfg.num_kv_heads)
+    rows = key.shape[0]
+    if value.shape[0] != rows:
+        raise ValueError("key and value must have one number of rows")
+    qs = os_ = rot = positions = 0
+    q_at = out_at = angles = None
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out must be given together")
+        qs = _kv16_rows("q", q, cfg, cfg.num_q_heads)
+        os_ = _kv16_rows("q_out", q_out, cfg, cfg.num_q_heads)
+        if q.shape[0] != rows or q_out.shape[0] != rows:
+            raise ValueError("q, q_out and key must have one number of rows")
+        q_at, out_at = q.data_ptr(), q_out.data_ptr()
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 matrix [positions, rot_dim]")
+        positions, rot = cos_sin.shape
+        if rot == 0:
+            raise ValueError("cos_sin must have columns (None: no rotation)")
+        angles = cos_sin.data_ptr()
+    how = ROPE_STYLES.get(style)
+    if how is None:
+        raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}, got {style!r}")
+    _b8_starts(query_start, seq_lens)
+    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens,
+                                (key, value, query_start, q, q_out, cos_sin, dev_status), stream, _kv16_block_bytes)
+    st = _LIB.tq_kv16_append(cfg, key.data_ptr(), ks, value.data_ptr(), vs, q_at, qs, out_at, os_, angles, rot, positions, how,
+                             query_start.data_ptr(), seq_lens.shape[0], rows, cache.data_ptr(), nb, block_table.data_ptr(), width,
+                             seq_lens.data_ptr(), _b8_status(dev_status), raw)
+    if st:
+        raise TQError("tq_kv16_append", st)
+
+
+def tq_kv16_decode_workspace_size(cfg: tq_config, batch: int, max_seq_len: int) -> int:
+    return int(_LIB.tq_kv16_decode_workspace_size(ctypes.byref(cfg), batch, max_seq_len))
+
+
+def tq_kv16_decode(cfg: tq_config, q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                   seq_lens: torch.Tensor, max_seq_len: int, out: torch.Tensor, workspace: torch.Tensor,
+                   scale: float = 0.0, num_blocks: int | None = None, dev_status: torch.Tensor | None = None,
+                   stream=None) -> None:
+    """q [B, n_q, d] of the cache's type (rows may be a stride apart); out [B, n_q, d]; seq_lens [B] int32."""
+    qs = _kv16_rows("q", q, cfg, cfg.num_q_heads)
+    out_type = _b8_out("out", out, q.shape)
+    if q.shape[0] != seq_lens.shape[0]:
+        raise ValueError("q must have one row per sequence")
+    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (q, out, workspace, dev_status), stream, _kv16_block_bytes)
+    st = _LIB.tq_kv16_decode(cfg, q.data_ptr(), qs, cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(),
+                             q.shape[0], max_seq_len, scale, out.data_ptr(), out_type, workspace.data_ptr(),
+                             _b8_workspace(workspace), _b8_status(dev_status), raw)
+    if st:
+        raise TQError("tq_kv16_decode", st)
+
+
+def tq_kv16_continue_workspace_size(cfg: tq_config, batch: int, total_q: int, max_q_len: int, max_seq_len: int) -> int:
+    return int(_LIB.tq_kv16_continue_workspace_size(ctypes.byref(cfg), batch, total_q, max_q_len, max_seq_len))
+
+
+def tq_kv16_continue(cfg: tq_config, q: torch.Tensor, query_start: torch.Tensor, max_q_len: int, cache: torch.Tensor,
+                     block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, out: torch.Tensor,
+                     workspace: torch.Tensor, scale: float = 0.0, num_blocks: int | None = None,
+                     dev_status: torch.Tensor | None = None, stream=None) -> None:
+    """Causal attention of chunks whose keys and values are stored: q [total_q,
+    n_q, d] of the cache's type (rows may be a stride apart), query_start int32
+    [batch + 1], seq_lens int32 [batch] (lengths with the chunk), out [total_q,
+    n_q, d]; rows of out from query_start[batch] on are left as they are."""
+    qs = _kv16_rows("q", q, cfg, cfg.num_q_heads)
+    out_type = _b8_out("out", out, q.shape)
+    _b8_starts(query_start, seq_lens)
+    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (q, query_start, out, workspace, dev_status), stream,
+                                _kv16_block_bytes)
+    st = _LIB.tq_kv16_continue(cfg, q.data_ptr(), qs, query_start.data_ptr(), seq_lens.shape[0], q.shape[0], max_q_len,
+                               cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(), max_seq_len, scale,
+                               out.data_ptr(), out_type, workspace.data_ptr(), _b8_workspace(workspace), _b8_status(dev_status), raw)
+    if st:
+        raise TQError("tq_kv16_continue", st)

@@ -25,9 +25,16 @@ TQ_PRESET_3BIT_NC = 3
 TQ_PRESET_PROD3 = 4
 TQ_PRESET_E4M3_BLK = 5
 TQ_PRESET_INT8_BLK = 6
+TQ_PRESET_KV_BF16 = 7
+TQ_PRESET_KV_F16 = 8
 PRESET_IDS = {"k8v4": TQ_PRESET_K8V4, "4bit_nc": TQ_PRESET_4BIT_NC,
               "k3v4_nc": TQ_PRESET_K3V4_NC, "3bit_nc": TQ_PRESET_3BIT_NC, "prod3": TQ_PRESET_PROD3,
-              "e4m3_blk": TQ_PRESET_E4M3_BLK, "int8_blk": TQ_PRESET_INT8_BLK}
+              "e4m3_blk": TQ_PRESET_E4M3_BLK, "int8_blk": TQ_PRESET_INT8_BLK,
+              "kv_bf16": TQ_PRESET_KV_BF16, "kv_fp16": TQ_PRESET_KV_F16}
+
+TQ_ROPE_HALVES = 0
+TQ_ROPE_PAIRS = 1
+ROPE_STYLES = {"halves": TQ_ROPE_HALVES, "pairs": TQ_ROPE_PAIRS}
 
 TQ_DTYPE_F16 = 0
 TQ_DTYPE_BF16 = 1
@@ -45,7 +52,8 @@ EXPORTED = ("tq_build_codebook", "tq_layout_for", "tq_store", "tq_decode_workspa
             "tq_dequant", "tq_prod_layout_for", "tq_prod_store", "tq_prod_scores_workspace_size",
             "tq_prod_scores", "tq_continue_workspace_size", "tq_continue", "tq_b8_layout_for", "tq_b8_store",
             "tq_b8_dequant", "tq_b8_decode_workspace_size", "tq_b8_decode", "tq_b8_continue_workspace_size",
-            "tq_b8_continue", "tq_status_string", "tq_version")
+            "tq_b8_continue", "tq_kv16_layout_for", "tq_kv16_append", "tq_kv16_decode_workspace_size", "tq_kv16_decode",
+            "tq_kv16_continue_workspace_size", "tq_kv16_continue", "tq_status_string", "tq_version")
 
 TQ_DECODE_NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -78,6 +86,11 @@ class tq_b8_layout(ctypes.Structure):
     _fields_ = [("code_limit", ctypes.c_int), ("is_int8", ctypes.c_int), ("tile_tokens", ctypes.c_int),
                 ("tile_bytes", ctypes.c_int), ("k_off", ctypes.c_int), ("v_off", ctypes.c_int),
                 ("scale_off", ctypes.c_int), ("block_bytes", ctypes.c_longlong)]
+
+
+class tq_kv16_layout(ctypes.Structure):
+    _fields_ = [("is_bf16", ctypes.c_int), ("tile_tokens", ctypes.c_int), ("tile_bytes", ctypes.c_int),
+                ("k_off", ctypes.c_int), ("v_off", ctypes.c_int), ("block_bytes", ctypes.c_longlong)]
 
 
 class tq_codebook(ctypes.Structure):
@@ -127,6 +140,15 @@ _SIGS = {
     "tq_b8_continue_workspace_size": (_sz, [ctypes.POINTER(tq_config), _i, _i, _i, _i]),
     "tq_b8_continue": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _i, _vp, _i, _i, _i, _vp, _ll, _vp, _i, _vp, _i, _f,
                             _vp, _i, _vp, _sz, _vp, _vp]),
+    "tq_kv16_layout_for": (_i, [ctypes.POINTER(tq_config), ctypes.POINTER(tq_kv16_layout)]),
+    "tq_kv16_append": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _i, _i, _i, _vp, _i, _i,
+                            _vp, _ll, _vp, _i, _vp, _vp, _vp]),
+    "tq_kv16_decode_workspace_size": (_sz, [ctypes.POINTER(tq_config), _i, _i]),
+    "tq_kv16_decode": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _vp, _ll, _vp, _i, _vp, _i, _i, _f, _vp, _i, _vp, _sz,
+                            _vp, _vp]),
+    "tq_kv16_continue_workspace_size": (_sz, [ctypes.POINTER(tq_config), _i, _i, _i, _i]),
+    "tq_kv16_continue": (_i, [ctypes.POINTER(tq_config), _vp, _ll, _vp, _i, _i, _i, _vp, _ll, _vp, _i, _vp, _i, _f, _vp,
+                              _i, _vp, _sz, _vp, _vp]),
     "tq_status_string": (ctypes.c_char_p, [_i]),
     "tq_version": (_i, []),
 }

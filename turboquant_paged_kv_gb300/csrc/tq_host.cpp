@@ -20,6 +20,8 @@ bool preset_info(int preset, PresetInfo* out) {
     case TQ_PRESET_PROD3:   *out = {2, 0, false, false}; return true;   // keys only: its own layout
     case TQ_PRESET_E4M3_BLK:
     case TQ_PRESET_INT8_BLK: *out = {8, 0, false, false}; return true;  // 8-bit blocks: their own layout
+    case TQ_PRESET_KV_BF16:
+    case TQ_PRESET_KV_F16: *out = {16, 0, false, false}; return true;   // not quantised: their own layout
     default: return false;
   }
 }
@@ -86,6 +88,25 @@ tq_status make_b8_layout(const tq_config* cfg, tq_b8_layout* out) {
   return TQ_OK;
 }
 
+tq_status make_kv16_layout(const tq_config* cfg, tq_kv16_layout* out) {
+  if (!cfg || !out) return TQ_ERR_INVALID_ARG;
+  if (cfg->preset != TQ_PRESET_KV_BF16 && cfg->preset != TQ_PRESET_KV_F16) return TQ_ERR_INVALID_ARG;
+  if (cfg->head_dim <= 0 || cfg->block_size <= 0 || cfg->num_kv_heads <= 0) return TQ_ERR_INVALID_ARG;
+  if ((cfg->flags & ~TQ_FLAG_INDICES_READY) || cfg->partition_tokens != 0) return TQ_ERR_INVALID_ARG;
+  if (cfg->head_dim != 128 || cfg->num_kv_heads > 4096) return TQ_ERR_UNSUPPORTED;
+  const int bs = cfg->block_size;
+  if (bs != 16 && bs != 32 && bs != 64 && bs != 128) return TQ_ERR_UNSUPPORTED;
+  tq_kv16_layout L;
+  std::memset(&L, 0, sizeof(L));
+  L.is_bf16 = cfg->preset == TQ_PRESET_KV_BF16;
+  L.tile_tokens = kTileTokens;
+  L.tile_bytes = kTileTokens * 4 * 128;
+  L.v_off = kTileTokens * 2 * 128;
+  L.block_bytes = static_cast<long long>(cfg->num_kv_heads) * (bs / kTileTokens) * L.tile_bytes;
+  *out = L;
+  return TQ_OK;
+}
+
 namespace {
 
 // P[x >= t] and sigma^2 * pdf(t) for x ~ N(0, sigma^2).
@@ -148,6 +169,8 @@ tq_status tq_build_codebook(int head_dim, int bits, tq_codebook* out) {
 tq_status tq_layout_for(const tq_config* cfg, tq_layout* out) { return tq::make_layout(cfg, out); }
 
 tq_status tq_b8_layout_for(const tq_config* cfg, tq_b8_layout* out) { return tq::make_b8_layout(cfg, out); }
+
+tq_status tq_kv16_layout_for(const tq_config* cfg, tq_kv16_layout* out) { return tq::make_kv16_layout(cfg, out); }
 
 const char* tq_status_string(int status) {
   switch (status) {

@@ -25,6 +25,9 @@ tq_status make_layout(const tq_config* cfg, tq_layout* out);
 // every tq_b8_* entry point shares.
 tq_status make_b8_layout(const tq_config* cfg, tq_b8_layout* out);
 
+// The same for the 16-bit cache and the tq_kv16_* entry points.
+tq_status make_kv16_layout(const tq_config* cfg, tq_kv16_layout* out);
+
 // Shared argument checks.
 inline bool aligned16(const void* p) { return (reinterpret_cast<unsigned long long>(p) & 15ull) == 0; }
 inline int effective_partition(const tq_config* cfg) {

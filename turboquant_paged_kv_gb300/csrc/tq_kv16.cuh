@@ -1,0 +1,46 @@
+// Shared by the kernels of the 16-bit cache: addressing and argument checks
+// (those that are not about codes and scales are the 8-bit cache's). Internal,
+// not ABI.
+//
+// Cache block: [n_kv][block_size / 16] tiles of 8192 bytes, 16 key rows then 16
+// value rows of 256 bytes, each as [2 groups of 8 rows][2 halves][8 rows][128
+// bytes] with the 16-byte group c of row r at group c ^ (r & 7).
+#ifndef TQ_KV16_CUH_
+#define TQ_KV16_CUH_
+
+#include "tq_b8.cuh"
+
+namespace tq {
+namespace {
+
+constexpr int kKvD = 128;
+constexpr int kKvRows = 16;          // positions per tile
+constexpr int kKvTileBytes = 8192;
+constexpr int kKvHalfBytes = 4096;   // the key rows, or the value rows, of a tile
+
+// Where a (block, head) lies.
+struct Kv16Cache {
+  const uint8_t* base;
+  long long num_blocks, block_bytes;
+  int n_kv, log2_bs, bt_stride;
+  __device__ __forceinline__ bool good(int blk) const { return blk >= 0 && blk < num_blocks; }
+  // tile `t` of a sequence, whose block id is blk
+  __device__ __forceinline__ const uint8_t* tile(int blk, int h, int t) const {
+    const int tpb = 1 << (log2_bs - 4);
+    return base + blk * block_bytes + (static_cast<long long>(h * tpb + (t & (tpb - 1))) << 13);
+  }
+};
+
+// Byte of the 16-byte group c8 (0 .. 15) of row r (0 .. 15) in the key or the value rows of a tile.
+__device__ __forceinline__ int kv16_at(int r, int c8) {
+  return ((r >> 3) << 11) + ((c8 >> 3) << 10) + ((r & 7) << 7) + (((c8 ^ r) & 7) << 4);
+}
+
+inline Kv16Cache kv16_cache(const tq_config* cfg, const tq_kv16_layout& L, const void* cache, long long num_blocks, int bt_stride) {
+  return {static_cast<const uint8_t*>(cache), num_blocks, L.block_bytes, cfg->num_kv_heads, b8_log2(cfg->block_size), bt_stride};
+}
+
+}  // namespace
+}  // namespace tq
+
+#endif  // TQ_KV16_CUH_
