@@ -30,7 +30,7 @@ CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 
 CU_SOURCES = ["tq_store.cu", "tq_decode.cu", "tq_decode_noalloc.cu", "tq_dequant.cu", "tq_prod.cu",
               "tq_prod_store.cu", "tq_continue.cu", "tq_b8_cache.cu", "tq_b8_decode.cu", "tq_b8_chunk.cu",
-              "tq_b8_continue.cu", "tq_kv16_append.cu", "tq_kv16_attn.cu"]
+              "tq_b8_continue.cu", "tq_kv16_append.cu", "tq_kv16_decode.cu", "tq_kv16_continue.cu"]
 CPP_SOURCES = ["tq_host.cpp"]
 
 
@@ -44,6 +44,7 @@ def _deps():
                          os.path.join(CSRC, "tq_prod.cuh"), os.path.join(CSRC, "tq_store.cuh"),
                          os.path.join(CSRC, "tq_b8.cuh"), os.path.join(CSRC, "tq_b8_chunk.cuh"),
                          os.path.join(CSRC, "tq_kv16.cuh"),
+                         os.path.join(CSRC, "tq_line.cuh"),
                          os.path.join(INCLUDE, "tq.h"),
                          os.path.abspath(__file__)]
 

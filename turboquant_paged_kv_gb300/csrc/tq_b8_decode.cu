@@ -42,6 +42,7 @@
 
 #include "tq_attn.cuh"
 #include "tq_b8.cuh"
+#include "tq_line.cuh"
 
 namespace tq {
 namespace {
@@ -76,93 +77,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint64
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory"); }
-
-// How many positions sequence i sees.
-__device__ __forceinline__ int length_of(const B8SplitArgs& a, int i, bool* too_long) {
-  const int limit = min(a.max_seq_len, a.cap), raw = ld_dep_s32(a.seq_lens + i);
-  *too_long = raw > limit;
-  return min(max(raw, 0), limit);
-}
-
-// A place in the line.
-struct Place {
-  int row, h, t, tiles, len;
-};
-__device__ __forceinline__ void next_tile(const B8SplitArgs& a, Place& p) {
-  if (++p.t < p.tiles) return;
-  p.t = 0;
-  if (++p.h < a.n_kv) return;
-  p.h = 0;
-  bool too_long;
-  do {
-    if (++p.row >= a.rows) return;
-    p.len = length_of(a, p.row, &too_long);
-    p.tiles = (p.len + kB8Rows - 1) / kB8Rows;
-  } while (p.tiles == 0);
-}
-
-// The rows of a group of 32, one a lane.
-struct Rows {
-  int len, tiles;
-  bool too_long;
-};
-__device__ __forceinline__ Rows rows_of(const B8SplitArgs& a, int i) {
-  Rows r = {0, 0, false};
-  if (i < a.rows) r.len = length_of(a, i, &r.too_long);
-  r.tiles = (r.len + kB8Rows - 1) / kB8Rows;
-  return r;
-}
-
-// Tiles of all rows, and before row `upto`, times n_kv (a warp's lanes
-// together); `first` keeps the first 32 rows.
-__device__ __forceinline__ void count_tiles(const B8SplitArgs& a, int upto, int lane, long long* total, long long* before,
-                                            bool* too_long, Rows* first) {
-  long long all = 0, bf = 0;
-  bool tl = false;
-  for (int i0 = 0; i0 < a.rows; i0 += 32) {
-    const Rows r = rows_of(a, i0 + lane);
-    if (i0 == 0) *first = r;
-    tl |= r.too_long;
-    all += __reduce_add_sync(0xffffffffu, r.tiles);
-    bf += __reduce_add_sync(0xffffffffu, i0 + lane < upto ? r.tiles : 0);
-  }
-  *total = all * a.n_kv;
-  *before = bf * a.n_kv;
-  *too_long = __any_sync(0xffffffffu, tl);
-}
-
-// x / y; most lines are short enough for 32 bits.
-__device__ __forceinline__ long long divide(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
-}
-
-// The place of tile x of the line (x < total).
-__device__ __forceinline__ Place find_tile(const B8SplitArgs& a, long long x, int lane, const Rows& first) {
-  Place p = {};
-  long long before = 0;
-  for (int i0 = 0; i0 < a.rows; i0 += 32) {
-    const Rows r = i0 == 0 ? first : rows_of(a, i0 + lane);
-    int inc = r.tiles;   // a group of 32 rows holds less than 2^32 tiles
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    const unsigned m = __ballot_sync(0xffffffffu, x < (before + static_cast<unsigned>(inc)) * a.n_kv);
-    if (m) {
-      const int src = __ffs(m) - 1;
-      const long long rest = x - (before + static_cast<unsigned>(__shfl_sync(0xffffffffu, inc - r.tiles, src))) * a.n_kv;
-      p.row = i0 + src;
-      p.tiles = __shfl_sync(0xffffffffu, r.tiles, src);
-      p.len = __shfl_sync(0xffffffffu, r.len, src);
-      p.h = static_cast<int>(divide(rest, p.tiles));
-      p.t = static_cast<int>(rest - static_cast<long long>(p.h) * p.tiles);
-      return p;
-    }
-    before += static_cast<unsigned>(__shfl_sync(0xffffffffu, inc, 31));
-  }
-  return p;
-}
 
 // The log2 of a head's reference, a whole number: that of the block's value scale,
 // lv, as long as neither side is lost. `had` is the log2 of what the accumulators
@@ -462,104 +376,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) b8_split_kernel(const B8SplitA
   }
 }
 
-template <typename TO>
-__device__ __forceinline__ void write4(TO* dst, float4 v) {
-  if constexpr (std::is_same<TO, float>::value) {
-    *reinterpret_cast<float4*>(dst) = v;
-  } else if constexpr (std::is_same<TO, __half>::value) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-}
-
-// A CTA of WARPS warps per (sequence, query head): the records of the pair are
-// those of the warps whose parts of the line meet it; warp k takes every
-// WARPS-th one, four at a time, a lane 4 coordinates.
-template <typename TO, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) b8_merge_kernel(const B8SplitArgs a) {
-  __shared__ float s_m[WARPS], s_l[WARPS];
-  __shared__ float4 s_o[WARPS][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x / a.n_q, qh = blockIdx.x - row * a.n_q;
-  const int h = qh / a.group, gg = qh - h * a.group;
-  // lengths and starts are not written by the split kernel, which let this
-  // launch go only after its own wait: they may be read before this one's
-  long long total, before;
-  bool too_long;
-  Rows first;
-  count_tiles(a, row, lane, &total, &before, &too_long, &first);
-  int len;
-  if (row < 32) {
-    len = __shfl_sync(0xffffffffu, first.len, row & 31);
-  } else {
-    len = length_of(a, row, &too_long);
-  }
-  const int tiles = (len + kB8Rows - 1) / kB8Rows;
-  const long long x0 = before + static_cast<long long>(h) * tiles;
-  TO* out = static_cast<TO*>(a.out) + (static_cast<long long>(row) * a.n_q + qh) * kB8D + 4 * lane;
-  grid_dep_wait();
-  grid_dep_launch();
-  if (tiles == 0) {
-    if (warp == 0) write4<TO>(out, make_float4(0.f, 0.f, 0.f, 0.f));
-    return;
-  }
-  // owners of the pair's first and last tile: warp w owns [total w / nw, total (w + 1) / nw)
-  const long long nw = min(static_cast<long long>(a.warps), total);
-  const long long w0 = divide((x0 + 1) * nw - 1, total), w1 = divide((x0 + tiles) * nw - 1, total);
-  const long long pair = static_cast<long long>(row) * a.n_kv + h;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (long long w = w0 + warp; w <= w1; w += 4 * WARPS) {
-    float lse[4];
-    float4 x[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const long long v = w + i * WARPS;
-      const bool ok = v <= w1;
-      const long long rec = (pair + v) * a.group + gg;
-      lse[i] = ok ? ld_dep_f32(a.rec_lse + rec) : -INFINITY;
-      x[i] = ok ? ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kB8D) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (lse[i] == -INFINITY) continue;
-      const float u = fmaxf(m, lse[i]);
-      const float e = m == -INFINITY ? 0.f : exp2f(m - u), f = exp2f(lse[i] - u);
-      m = u;
-      l = l * e + f;
-      o.x = o.x * e + x[i].x * f;
-      o.y = o.y * e + x[i].y * f;
-      o.z = o.z * e + x[i].z * f;
-      o.w = o.w * e + x[i].w * f;
-    }
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  s_o[warp][lane] = o;
-  __syncthreads();
-  if (warp) return;
-#pragma unroll
-  for (int k = 1; k < WARPS; ++k) {
-    const float mk = s_m[k];
-    if (mk == -INFINITY) continue;
-    const float u = fmaxf(m, mk);
-    const float e = m == -INFINITY ? 0.f : exp2f(m - u), f = exp2f(mk - u);
-    const float4 x = s_o[k][lane];
-    m = u;
-    l = l * e + s_l[k] * f;
-    o.x = o.x * e + x.x * f;
-    o.y = o.y * e + x.y * f;
-    o.z = o.z * e + x.z * f;
-    o.w = o.w * e + x.w * f;
-  }
-  const float r = l == 0.f ? 0.f : 1.f / l;
-  write4<TO>(out, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
-}
-
 template <typename TQ, bool INT8, bool WIDE>
 cudaError_t launch_split(const B8SplitArgs& a, int ctas, int dev, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
@@ -571,17 +387,6 @@ template <typename TQ>
 cudaError_t launch_split(const B8SplitArgs& a, bool is_int8, int ctas, int dev, cudaStream_t s) {
   if (a.group > 4) return is_int8 ? launch_split<TQ, true, true>(a, ctas, dev, s) : launch_split<TQ, false, true>(a, ctas, dev, s);
   return is_int8 ? launch_split<TQ, true, false>(a, ctas, dev, s) : launch_split<TQ, false, false>(a, ctas, dev, s);
-}
-
-template <typename TO>
-cudaError_t launch_merge(const B8SplitArgs& a, long long records_each, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.rows) * static_cast<unsigned>(a.n_q));
-  // the whole decode: 4 x 131072 (59 records) 170.3 us with 4 warps, 166.7 with 16; one sequence
-  // of 301 (19 records) 6.39 with 4, 6.15 with 8; 32 x 4096 (9 records) 50.0 with 4, 51.5 with 8,
-  // 57.3 with 16
-  if (records_each > 32) return launch_pdl(b8_merge_kernel<TO, 16>, grid, dim3(16 * 32), 0, s, a);
-  if (records_each > 16) return launch_pdl(b8_merge_kernel<TO, 8>, grid, dim3(8 * 32), 0, s, a);
-  return launch_pdl(b8_merge_kernel<TO, 4>, grid, dim3(4 * 32), 0, s, a);
 }
 
 size_t b8_split_workspace(const tq_config* cfg, long long rows) {

@@ -36,6 +36,32 @@ __device__ __forceinline__ int kv16_at(int r, int c8) {
   return ((r >> 3) << 11) + ((c8 >> 3) << 10) + ((r & 7) << 7) + (((c8 ^ r) & 7) << 4);
 }
 
+// Two numbers of the cache's type in a word.
+template <typename T>
+__device__ __forceinline__ float2 to_floats(uint32_t w) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+  else return half2_to_float2(w);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t to_pair(float x, float y) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __half2 v = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+// The pair rounded, and what that leaves of x and y.
+template <typename T>
+__device__ __forceinline__ uint32_t take_pair(float& x, float& y) {
+  const uint32_t w = to_pair<T>(x, y);
+  const float2 f = to_floats<T>(w);
+  x -= f.x;
+  y -= f.y;
+  return w;
+}
+
 inline Kv16Cache kv16_cache(const tq_config* cfg, const tq_kv16_layout& L, const void* cache, long long num_blocks, int bt_stride) {
   return {static_cast<const uint8_t*>(cache), num_blocks, L.block_bytes, cfg->num_kv_heads, b8_log2(cfg->block_size), bt_stride};
 }

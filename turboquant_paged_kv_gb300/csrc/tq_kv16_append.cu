@@ -31,22 +31,6 @@ struct AppendArgs {
 
 enum Style { kNone, kHalves, kPairs };
 
-template <typename T>
-__device__ __forceinline__ float2 to_floats(uint32_t w) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
-  else return half2_to_float2(w);
-}
-template <typename T>
-__device__ __forceinline__ uint32_t to_pair(float x, float y) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
 // Infinities to the largest number of their sign, NaN to 0; true if there were any.
 template <typename T>
 __device__ __forceinline__ bool tame(uint32_t& w) {

@@ -1,4 +1,4 @@
-// tq_kv16_decode and tq_kv16_continue: attention over the 16-bit cache.
+// tq_kv16_continue: causal attention of chunks of queries over the 16-bit cache.
 //
 // A CTA per (query row, query head): 4 warps take every fourth tile of 16
 // positions, a position at a time, 4 coordinates a lane, with the running maximum
@@ -122,37 +122,6 @@ AttnArgs arguments(const tq_config* cfg, const tq_kv16_layout& L, const void* q,
 }  // namespace tq
 
 extern "C" {
-
-size_t tq_kv16_decode_workspace_size(const tq_config* cfg, int batch, int max_seq_len) {
-  using namespace tq;
-  tq_kv16_layout L;
-  if (make_kv16_layout(cfg, &L) != TQ_OK || batch < 0 || max_seq_len < 0 || b8_heads(cfg) != TQ_OK) return 0;
-  return 16;
-}
-
-tq_status tq_kv16_decode(const tq_config* cfg, const void* q, long long q_stride, const void* cache, long long num_blocks,
-                         const int* block_table, int bt_stride, const int* seq_lens, int batch, int max_seq_len,
-                         float scale, void* out, int out_dtype, void* workspace, size_t workspace_bytes,
-                         unsigned int* dev_status, tq_stream_t stream) {
-  using namespace tq;
-  tq_kv16_layout L;
-  tq_status st = make_kv16_layout(cfg, &L);
-  if (st != TQ_OK) return st;
-  if (batch < 0 || max_seq_len < 0 || !b8_dtype(out_dtype)) return TQ_ERR_INVALID_ARG;
-  if ((st = b8_heads(cfg)) != TQ_OK) return st;
-  if (batch == 0) return TQ_OK;
-  if (!q || !out || !workspace) return TQ_ERR_INVALID_ARG;
-  if ((st = b8_check(cache, num_blocks, block_table, bt_stride, seq_lens, dev_status)) != TQ_OK) return st;
-  if (!b8_aligned(q, 16) || !b8_aligned(out, 16) || !b8_aligned(workspace, 16)) return TQ_ERR_MISALIGNED;
-  if ((st = b8_stride(&q_stride, static_cast<long long>(cfg->num_q_heads) * kKvD)) != TQ_OK) return st;
-  if (workspace_bytes < tq_kv16_decode_workspace_size(cfg, batch, max_seq_len)) return TQ_ERR_WORKSPACE_TOO_SMALL;
-  if (static_cast<long long>(batch) * cfg->num_q_heads > INT_MAX) return TQ_ERR_UNSUPPORTED;
-  AttnArgs a = arguments(cfg, L, q, q_stride, cache, num_blocks, block_table, bt_stride, seq_lens, max_seq_len, scale, out, dev_status);
-  a.batch = a.rows = batch;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const cudaError_t err = L.is_bf16 ? launch<__nv_bfloat16>(a, out_dtype, s) : launch<__half>(a, out_dtype, s);
-  return err == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
-}
 
 size_t tq_kv16_continue_workspace_size(const tq_config* cfg, int batch, int total_q, int max_q_len, int max_seq_len) {
   using namespace tq;
