@@ -45,6 +45,7 @@ def _deps():
                          os.path.join(CSRC, "tq_b8.cuh"), os.path.join(CSRC, "tq_b8_chunk.cuh"),
                          os.path.join(CSRC, "tq_kv16.cuh"),
                          os.path.join(CSRC, "tq_line.cuh"),
+                         os.path.join(CSRC, "tq_tc.cuh"),
                          os.path.join(INCLUDE, "tq.h"),
                          os.path.abspath(__file__)]
 
