@@ -9,13 +9,15 @@
 // (halves: one exchange of the packed 16-bit words).
 #include <climits>
 
+#include "tq_attn.cuh"
 #include "tq_kv16.cuh"
 
 namespace tq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kEach = 4;   // loads a lane: 8 head rows a warp
+constexpr int kEach = 4;   // loads a lane and round: 8 head rows a warp
+constexpr int kEnough = 152 * 48;   // warps from which on they take more rounds rather than being more
 
 struct AppendArgs {
   Kv16Cache c;
@@ -26,7 +28,7 @@ struct AppendArgs {
   const int *query_start, *block_table, *seq_lens;
   unsigned int* status;
   long long units;
-  int batch, total_q, n_q, heads, parts, rot, num_pos, cap;   // heads: rows of a token; parts: warps a token
+  int batch, total_q, n_q, heads, parts, rounds, rot, num_pos, cap;   // heads: rows of a token; parts: warps a token; rounds of loads each
 };
 
 enum Style { kNone, kHalves, kPairs };
@@ -42,20 +44,31 @@ __device__ __forceinline__ bool tame(uint32_t& w) {
   return true;
 }
 
-// The sequence of a row: query_start[b] <= row < query_start[b + 1], -1 for none.
-// The warp's lanes together, 32 at a time, then within the 32nd part found.
-__device__ __forceinline__ int find_sequence(const AppendArgs& a, int row, int lane) {
+// The sequence of a row: query_start[b] <= row < query_start[b + 1], with its
+// starts and its length; none: false. The warp's lanes together: 32 sequences at
+// once, or every n-th first where there are more.
+struct Sequence {
+  int b, q0, q1, len;
+};
+__device__ __forceinline__ bool find_sequence(const AppendArgs& a, int row, int lane, Sequence* s) {
   int lo = 0, n = a.batch;   // the answer is in [lo, lo + n) if there is one
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int first = lo + lane * step;
-    const bool behind = first < lo + n && ld_dep_s32(a.query_start + first) <= row;
-    const unsigned m = __ballot_sync(0xffffffffu, behind);
+  while (n > 32) {
+    const int step = (n + 31) / 32, at = lo + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, ldg_or(a.query_start + at, lane * step < n, INT_MAX) <= row);
     const int k = m ? 31 - __clz(m) : 0;
     n = min(step, n - k * step);
     lo += k * step;
   }
-  return lo;
+  const int q0 = ldg_or(a.query_start + lo + lane, lane < n, INT_MAX), q1 = ldg_or(a.query_start + lo + lane + 1, lane < n, 0);
+  const int len = ldg_or(a.seq_lens + lo + lane, lane < n, 0);
+  const unsigned m = __ballot_sync(0xffffffffu, q0 <= row);
+  if (!m) return false;
+  const int k = 31 - __clz(m);
+  s->b = lo + k;
+  s->q0 = __shfl_sync(0xffffffffu, q0, k);
+  s->q1 = __shfl_sync(0xffffffffu, q1, k);
+  s->len = __shfl_sync(0xffffffffu, len, k);
+  return row < s->q1;   // (and starts that go backwards)
 }
 
 template <typename T, int STYLE>
@@ -67,29 +80,29 @@ __global__ void __launch_bounds__(kThreads) kv16_append_kernel(const AppendArgs 
   if (unit >= a.units) return;
   const int row = static_cast<int>(unit / a.parts), part = static_cast<int>(unit - static_cast<long long>(row) * a.parts);
   // this lane's rows: heads head0, head0 + 2, .. of the token's line of queries, keys, values
-  const int head0 = part * 2 * kEach + (lane >> 4);
-  const bool used = row < ld_dep_s32(a.query_start + a.batch);   // (and the loads below need not wait for it)
+  int head0 = part * a.rounds * 2 * kEach + (lane >> 4);
   const int n_kv = a.c.n_kv;
-  uint4 x[kEach];
+  auto load = [&](uint4 (&x)[kEach], int head) {
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int u = head0 + 2 * i;
-    const T* src = static_cast<const T*>(a.q) + row * a.q_stride + u * kKvD;
-    if (u >= a.n_q) src = static_cast<const T*>(a.key) + row * a.key_stride + (u - a.n_q) * kKvD;
-    if (u >= a.n_q + n_kv) src = static_cast<const T*>(a.value) + row * a.value_stride + (u - a.n_q - n_kv) * kKvD;
-    x[i] = ld_or_zero4(src + 8 * c8, u < a.heads);
-  }
-  if (!used) return;
-  const int b = find_sequence(a, row, lane);
-  const int q0 = ld_dep_s32(a.query_start + b), q1 = ld_dep_s32(a.query_start + b + 1), len = ld_dep_s32(a.seq_lens + b);
-  if (row < q0 || row >= q1) return;   // starts that go backwards
-  const long long pos = static_cast<long long>(len) - q1 + row;
+    for (int i = 0; i < kEach; ++i) {
+      const int u = head + 2 * i;
+      const T* src = static_cast<const T*>(a.q) + row * a.q_stride + u * kKvD;
+      if (u >= a.n_q) src = static_cast<const T*>(a.key) + row * a.key_stride + (u - a.n_q) * kKvD;
+      if (u >= a.n_q + n_kv) src = static_cast<const T*>(a.value) + row * a.value_stride + (u - a.n_q - n_kv) * kKvD;
+      x[i] = ld_or_zero4(src + 8 * c8, u < a.heads);
+    }
+  };
+  uint4 x[kEach];
+  load(x, head0);
+  Sequence seq;
+  if (!find_sequence(a, row, lane, &seq)) return;
+  const long long pos = static_cast<long long>(seq.len) - seq.q1 + row;
   const bool turned = pos >= 0 && (STYLE == kNone || pos < a.num_pos);   // has its angles
   bool stored = turned && pos < a.cap;
   if (part == 0 && lane == 0 && !stored) b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
   if (!turned) return;
   int blk = -1;
-  if (stored) blk = ld_dep_s32(a.block_table + static_cast<long long>(b) * a.c.bt_stride + (pos >> a.c.log2_bs));
+  if (stored) blk = ld_dep_s32(a.block_table + static_cast<long long>(seq.b) * a.c.bt_stride + (pos >> a.c.log2_bs));
 
   float cs[8], sn[8];   // what this lane's coordinates and their partners take
   int from = lane;      // who holds the partners
@@ -122,31 +135,39 @@ __global__ void __launch_bounds__(kThreads) kv16_append_kernel(const AppendArgs 
   }
   const int r = static_cast<int>(pos) & (kKvRows - 1), t = static_cast<int>(pos >> 4);
   bool wild = false;
+  for (int round = 1;; ++round, head0 += 2 * kEach) {
+    const bool more = round < a.rounds;
+    uint4 next[kEach];
+    if (more) load(next, head0 + 2 * kEach);
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int u = head0 + 2 * i;
-    uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-    if constexpr (STYLE != kNone) {
-      uint32_t p[4];
+    for (int i = 0; i < kEach; ++i) {
+      const int u = head0 + 2 * i;
+      uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      if constexpr (STYLE != kNone) {
+        uint32_t p[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) p[k] = STYLE == kHalves ? __shfl_sync(0xffffffffu, w[k], from) : __byte_perm(w[k], 0, 0x1032);
-      if (u < a.n_q + n_kv && 8 * c8 < a.rot) {
+        for (int k = 0; k < 4; ++k) p[k] = STYLE == kHalves ? __shfl_sync(0xffffffffu, w[k], from) : __byte_perm(w[k], 0, 0x1032);
+        if (u < a.n_q + n_kv && 8 * c8 < a.rot) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 v = to_floats<T>(w[k]), o = to_floats<T>(p[k]);
-          w[k] = to_pair<T>(fmaf(v.x, cs[2 * k], o.x * sn[2 * k]), fmaf(v.y, cs[2 * k + 1], o.y * sn[2 * k + 1]));
+          for (int k = 0; k < 4; ++k) {
+            const float2 v = to_floats<T>(w[k]), o = to_floats<T>(p[k]);
+            w[k] = to_pair<T>(fmaf(v.x, cs[2 * k], o.x * sn[2 * k]), fmaf(v.y, cs[2 * k + 1], o.y * sn[2 * k + 1]));
+          }
         }
       }
-    }
-    if (u < a.n_q) {
-      *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + row * a.q_out_stride + u * kKvD + 8 * c8) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (u < a.heads && stored) {
+      if (u < a.n_q) {
+        *reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + row * a.q_out_stride + u * kKvD + 8 * c8) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else if (u < a.heads && stored) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) wild |= tame<T>(w[k]);
-      const int kv = u >= a.n_q + n_kv, h = u - a.n_q - (kv ? n_kv : 0);
-      uint8_t* dst = const_cast<uint8_t*>(a.c.tile(blk, h, t)) + kv * kKvHalfBytes + kv16_at(r, c8);
-      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int k = 0; k < 4; ++k) wild |= tame<T>(w[k]);
+        const int kv = u >= a.n_q + n_kv, h = u - a.n_q - (kv ? n_kv : 0);
+        uint8_t* dst = const_cast<uint8_t*>(a.c.tile(blk, h, t)) + kv * kKvHalfBytes + kv16_at(r, c8);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
+    if (!more) break;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) x[i] = next[i];
   }
   if (__builtin_expect(wild, 0)) b8_flag(a.status, TQ_DEV_NOT_FINITE);
 }
@@ -207,7 +228,10 @@ tq_status tq_kv16_append(const tq_config* cfg, const void* key, long long key_st
   a.total_q = total_q;
   a.n_q = q ? cfg->num_q_heads : 0;
   a.heads = a.n_q + 2 * cfg->num_kv_heads;
-  a.parts = (a.heads + 2 * kEach - 1) / (2 * kEach);
+  const int most = (a.heads + 2 * kEach - 1) / (2 * kEach);
+  const long long warps = static_cast<long long>(total_q) * most / kEnough;
+  a.rounds = warps < 1 ? 1 : (warps < most ? static_cast<int>(warps) : most);
+  a.parts = (most + a.rounds - 1) / a.rounds;
   a.rot = rot_dim;
   a.num_pos = num_positions;
   a.cap = b8_cap(cfg, bt_stride);

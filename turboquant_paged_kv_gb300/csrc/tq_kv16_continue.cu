@@ -42,7 +42,7 @@ namespace {
 
 constexpr int kRows = 256;             // of a unit: two tiles of 128
 constexpr int kCols = 128;             // positions a step
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
 constexpr int kCtas = 152;             // grid, one an SM: sizes the workspace without a device query
 constexpr float kMost = 60000.f;       // sums of P up to this: every P fits in fp16
 constexpr uint32_t kTileOp = 32768;    // a 128 x 128 operand
@@ -95,6 +95,11 @@ template <typename T>
 __device__ __forceinline__ constexpr uint32_t idesc_pv() { return idesc_qk<T>() | (1u << 16); }   // B is MN-major
 
 // Waits for the loads from tensor memory; what they brought is not used before.
+__device__ __forceinline__ void wait_ld(float (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]),
+                 "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])::"memory");
+}
 __device__ __forceinline__ void wait_ld(float (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]),
@@ -102,8 +107,18 @@ __device__ __forceinline__ void wait_ld(float (&r)[32]) {
                  "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]),
                  "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
 }
+__device__ __forceinline__ void load16(uint32_t addr, float (&r)[16]) { tmem_ld16(addr, reinterpret_cast<uint32_t*>(r)); }
 __device__ __forceinline__ void load32(uint32_t addr, float (&r)[32]) { tmem_ld32(addr, reinterpret_cast<uint32_t*>(r)); }
-__device__ __forceinline__ void store32(uint32_t addr, const float (&r)[32]) { tmem_st32(addr, reinterpret_cast<const uint32_t*>(r)); }
+
+// Waits for the other warp of the pair; true if `x` is true in any lane of either.
+__device__ __forceinline__ bool pair_any(int id, bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(r)
+               : "r"(id), "r"(static_cast<uint32_t>(x))
+               : "memory");
+  return r != 0;
+}
 
 // A part of a unit, as a CTA works on it.
 struct Work {
@@ -152,16 +167,18 @@ struct Line {
   long long total = 0;
   int b0 = -1;
   Chunk ch = {};       // lane's chunk of the 32 from b0 on
-  // the place: tile, sequence, head; the unit's steps, the step in it
-  int j = 0, b = 0, h = 0, steps = 0, off = 0;
+  // a place: tile, sequence, head; the unit's steps, the step in it
+  struct Place {
+    int j, b, h, steps, off;
+    // A cut one step from a unit's end is not worth a record: it moves there.
+    __device__ int shift() const { return off == 1 ? -1 : (off > 0 && off == steps - 1 ? 1 : 0); }
+  } at = {};
 
   __device__ Line(const ChunkArgs& args, int per_, int lane_) : a(args), per(per_), lane(lane_) {
     for (int i = 0; i < a.batch; i += 32) {
       group(i);
-      int most = 0;
       for (int k = 0; k < ch.tiles; ++k) total += steps_of(a, ch, k, per);
-      most = __reduce_max_sync(0xffffffffu, ch.tiles);
-      tiles_most = max(tiles_most, most);
+      tiles_most = max(tiles_most, __reduce_max_sync(0xffffffffu, ch.tiles));
     }
     total = warp_sum(total) * a.c.n_kv;
   }
@@ -170,57 +187,65 @@ struct Line {
     b0 = first;
     ch = chunk_of(a, first + lane, per);
   }
-  __device__ void find(long long x) {   // x < total
-    for (j = 0; j < tiles_most; ++j) {
+  // Step x of the units of tile index j_ of the 32 sequences: `s` their steps, a lane each.
+  __device__ Place locate(long long x, int j, int s) {
+    int inc = s;   // below 32 * 2^24
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, x < static_cast<long long>(inc) * a.c.n_kv)) - 1;
+    const int steps = __shfl_sync(0xffffffffu, s, src);
+    x -= static_cast<long long>(__shfl_sync(0xffffffffu, inc, src) - steps) * a.c.n_kv;
+    const int h = static_cast<int>(x / steps);
+    return {j, b0 + src, h, steps, static_cast<int>(x - static_cast<long long>(h) * steps)};
+  }
+  // Goes to step x0 of the line, where its cut moves; x1, the next cut, moves too (x0 < x1 <= total).
+  __device__ void go(long long& x0, long long& x1) {
+    long long before = 0, end = x1;
+    bool found = false, last = x1 >= total;
+    for (int j = 0; j < tiles_most && !(found && last); ++j) {
       for (int i = 0; i < a.batch; i += 32) {
         group(i);
         const int s = steps_of(a, ch, j, per);
-        long long inc = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
+        const long long behind = before + static_cast<long long>(__reduce_add_sync(0xffffffffu, s)) * a.c.n_kv;
+        if (!found && x0 < behind) {
+          found = true;
+          at = locate(x0 - before, j, s);
         }
-        inc *= a.c.n_kv;
-        const unsigned here = __ballot_sync(0xffffffffu, x < inc);
-        if (here) {
-          const int src = __ffs(here) - 1;
-          steps = __shfl_sync(0xffffffffu, s, src);
-          const long long rest = x - (__shfl_sync(0xffffffffu, inc, src) - static_cast<long long>(steps) * a.c.n_kv);
-          b = i + src;
-          h = static_cast<int>(rest / steps);
-          off = static_cast<int>(rest - static_cast<long long>(h) * steps);
-          return;
+        if (!last && x1 < behind) {
+          last = true;
+          end = x1 + locate(x1 - before, j, s).shift();
         }
-        x -= __shfl_sync(0xffffffffu, inc, 31);
+        before = behind;
       }
     }
+    x1 = end;
+    const int by = at.shift();
+    x0 += by;
+    group(at.b & ~31);
+    if (by < 0) at.off = 0;
+    if (by > 0 && x0 < x1) next();
   }
   __device__ void next() {   // the next unit, from its first step (there is one)
-    off = 0;
-    if (++h < a.c.n_kv) return;
-    h = 0;
-    ++b;
-    while (j < tiles_most) {
-      for (int i = b & ~31; i < a.batch; i += 32) {
+    at.off = 0;
+    if (++at.h < a.c.n_kv) return;
+    at.h = 0;
+    ++at.b;
+    while (at.j < tiles_most) {
+      for (int i = at.b & ~31; i < a.batch; i += 32) {
         group(i);
-        const unsigned more = __ballot_sync(0xffffffffu, i + lane >= b && ch.tiles > j);
+        const unsigned more = __ballot_sync(0xffffffffu, i + lane >= at.b && ch.tiles > at.j);
         if (more) {
-          b = i + __ffs(more) - 1;
-          steps = __shfl_sync(0xffffffffu, steps_of(a, ch, j, per), b & 31);
+          at.b = i + __ffs(more) - 1;
+          at.steps = __shfl_sync(0xffffffffu, steps_of(a, ch, at.j, per), at.b & 31);
           return;
         }
       }
-      b = 0;
-      ++j;
+      at.b = 0;
+      ++at.j;
     }
-  }
-  // A cut one step from a unit's end is not worth a record: it moves there.
-  __device__ long long snapped(long long x) {
-    if (x >= total) return total;
-    find(x);
-    if (off == 1) return x - 1;
-    return off > 0 && off == steps - 1 ? x + 1 : x;
   }
 };
 
@@ -231,15 +256,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
   __shared__ uint32_t s_tmem;
   __shared__ Work s_work[2];
   __shared__ unsigned s_bad[4];   // a step's groups of 16 positions whose block id is bad
+  __shared__ float2 s_pair[2][kRows];   // what the two threads of a row tell one another
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 1023u) & ~1023u;
   const uint32_t bars = base + kOffBar;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
   if (threadIdx.x == 32) {
-    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kWEmpty0 || i == kWEmpty1 ? 11 : (i == kPFull0 || i == kPFull1 ? 4 : (i == kQFull ? 2 : 1)));
+    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kWEmpty0 || i == kWEmpty1 ? 19 : (i == kPFull0 || i == kPFull1 ? 8 : (i == kQFull ? 2 : 1)));
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 8) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&s_tmem))) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
@@ -268,20 +294,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     return __all_sync(0xffffffffu, ok) != 0;
   };
 
-  if (warp < 8) {
-    // ---- softmax
-    const int t = warp >> 2;
+  if (warp < 16) {
+    // ---- softmax: of tile warp / 8, two threads a row, for the left and the right 64 columns
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");   // 4 x 104 + 64 = 5 x 96 registers a thread
+    const int t = warp >> 3, half = warp >> 2 & 1;
+    const int pair = 1 + (t << 2 | (warp & 3));   // the barrier of this warp and the one of the other half
     const unsigned by_group = (65536u + a.group - 1) / a.group;   // row / group for rows below 256, group <= 8
-    const int r = threadIdx.x;   // this thread's row, 0 .. 255
+    const int r = t * 128 + (warp & 3) * 32 + lane;   // this thread's row, 0 .. 255
     const int qi = static_cast<int>(r * by_group >> 16), head = r - qi * a.group;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + kColS + t * 128, t_o = tmem + lanes + kColO + t * 128;
+    const uint32_t t_s = tmem + lanes + kColS + t * 128 + half * 64, t_o = tmem + lanes + kColO + t * 128 + half * 64;
     const float f = fmaxf(a.qscale, 0x1p-126f);   // never 0, which would make NaN of a masked place
     unsigned steps = 0, served = 0;   // of this tile so far
     int before = 0;
-    bool ok = true;
+    bool ok = true;   // the same for both warps of a pair, so that neither waits for one that gave up
     for (unsigned part = 0; ok; ++part) {
-      if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
+      if (pair_any(pair, !long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
       const Work w = s_work[part & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
@@ -289,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       before = w.tiles;
       auto zero_rows = [&](int q0, int count) {   // `count` queries from q0 on, this KV head's part
         const long long all = static_cast<long long>(count) * a.group * (kKvD / 4);
-        for (long long i = threadIdx.x; i < all; i += 256) {
+        for (long long i = threadIdx.x; i < all; i += 512) {
           const long long x = i / (kKvD / 4);
           write4<TO>(static_cast<TO*>(a.out) + ((q0 + x / a.group) * a.n_q + w.h * a.group + x % a.group) * kKvD + 4 * (i % (kKvD / 4)),
                      make_float4(0.f, 0.f, 0.f, 0.f));
@@ -304,27 +332,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       const bool live = r < w.rows;
       const int vis = live ? max(min(w.pos0 + qi + 1, w.limit), 0) : 0;   // positions that this row sees
       const int vis_least = __reduce_min_sync(0xffffffffu, live ? vis : 0x7fffffff);
-      float m = -1e30f, l = 0.f;   // l: sum of P
+      float m = -1e30f, l = 0.f;   // l: sum of this thread's P
       for (int i = 0; i < w.tiles; ++i, ++steps) {
-        if (!(ok = warp_wait(kSFull0 + t, steps & 1))) break;
+        const bool there = warp_wait(kSFull0 + t, steps & 1);
         fence_after();
-        const int at = (w.tile0 + i) * kCols;
-        const unsigned bad = s_bad[(w.step0 + i) & 3];
-        const bool masked = bad || at + kCols > vis_least;
-        auto mask = [&](float (&s)[32], int c) {
+        const int at = (w.tile0 + i) * kCols + half * 64;
+        const unsigned bad = s_bad[(w.step0 + i) & 3] >> 4 * half & 15;
+        const bool masked = bad || at + 64 > vis_least;
+        auto mask = [&](float (&s)[16], int c) {
           if (__builtin_expect(masked, 0)) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (at + 32 * c + j >= vis || (bad >> (2 * c + (j >> 4)) & 1)) s[j] = -INFINITY;
+            for (int j = 0; j < 16; ++j)
+              if (at + 16 * c + j >= vis || (bad >> c & 1)) s[j] = -INFINITY;
           }
         };
-        float by_o = 1.f;   // what the accumulators take
-        uint32_t p[kTwo ? 64 : 32];   // two chunks of 32 positions, each: the hi parts, then the lo parts
-        auto weigh = [&](const float (&s)[32], int k) {   // chunk k of the two: its P, and their sum
+        uint32_t p[kTwo ? 64 : 32];   // 64 positions; in two parts: of each 32 the hi parts, then the lo parts
+        float2 x0, x1;
+        auto weigh = [&](const float (&s)[16], int c) {   // the P of 16 positions, added to the sums
           const float a0 = 3.f - m;
-          float2 x0 = make_float2(0.f, 0.f), x1 = x0;
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
+          for (int j = 0; j < 16; j += 4) {
             float2 y0 = fma2(make_float2(s[j], s[j + 1]), make_float2(f, f), make_float2(a0, a0));
             float2 y1 = fma2(make_float2(s[j + 2], s[j + 3]), make_float2(f, f), make_float2(a0, a0));
             y0.x = ex2(y0.x);
@@ -334,124 +361,116 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
             x0 = add2(x0, y0);
             x1 = add2(x1, y1);
             if constexpr (kTwo) {
-              p[32 * k + j / 2] = take_pair<T>(y0.x, y0.y);
-              p[32 * k + j / 2 + 1] = take_pair<T>(y1.x, y1.y);
-              p[32 * k + 16 + j / 2] = to_pair<T>(y0.x, y0.y);
-              p[32 * k + 16 + j / 2 + 1] = to_pair<T>(y1.x, y1.y);
+              const int k = 32 * (c >> 1) + 8 * (c & 1) + j / 2;
+              p[k] = take_pair<T>(y0.x, y0.y);
+              p[k + 1] = take_pair<T>(y1.x, y1.y);
+              p[k + 16] = to_pair<T>(y0.x, y0.y);
+              p[k + 17] = to_pair<T>(y1.x, y1.y);
             } else {
-              p[16 * k + j / 2] = to_pair<T>(y0.x, y0.y);
-              p[16 * k + j / 2 + 1] = to_pair<T>(y1.x, y1.y);
+              p[8 * c + j / 2] = to_pair<T>(y0.x, y0.y);
+              p[8 * c + j / 2 + 1] = to_pair<T>(y1.x, y1.y);
             }
           }
+        };
+        auto weigh_all = [&]() {
+          x0 = x1 = make_float2(0.f, 0.f);
+          float s[16], z[16];
+          load16(t_s, s);
+          wait_ld(s);
+          load16(t_s + 16, z);
+          mask(s, 0);
+          weigh(s, 0);
+          wait_ld(z);
+          load16(t_s + 32, s);
+          mask(z, 1);
+          weigh(z, 1);
+          wait_ld(s);
+          load16(t_s + 48, z);
+          mask(s, 2);
+          weigh(s, 2);
+          wait_ld(z);
+          mask(z, 3);
+          weigh(z, 3);
           x0 = add2(x0, x1);
           return x0.x + x0.y;
         };
-        float x[32], y[32];
-        load32(t_s, x);
-#pragma unroll 1
-        for (int c = 0; c < 4; c += 2) {   // rolled: the code stays in the instruction cache
-          wait_ld(x);
-          load32(t_s + 32 * c + 32, y);
-          mask(x, c);
-          float sum = weigh(x, 0);
-          wait_ld(y);
-          if (c == 0) load32(t_s + 64, x);
-          mask(y, c + 1);
-          sum += weigh(y, 1);
+        float sum;
+        for (int go = 0;; ++go) {   // once, but for rows that outgrow their m
+          sum = weigh_all();
+          if (go) break;
           const bool over = !(sum <= kMost);   // NaN too
-          if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
-            float s[32], top = -INFINITY;
-#pragma unroll 1
-            for (int k = 0; k < 2; ++k) {
-              load32(t_s + 32 * (c + k), s);
-              wait_ld(s);
-              mask(s, c + k);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) top = fmaxf(top, s[j]);
-            }
-            const float u = over ? fmaxf(m, top * f) : m, e = ex2(m - u);
-            m = u;
-            l *= e;
-            by_o *= e;
-            if (c) {   // the P of this step that are there already
-              wait_st();
-#pragma unroll 1
-              for (int k = 0; k < (kTwo ? 2 : 1); ++k) {
-                float o[32];
-                load32(t_s + 32 * k, o);
-                wait_ld(o);
-#pragma unroll
-                for (int j = 0; j < (kTwo ? 16 : 32); ++j) {
-                  float2 v = to_floats<T>(__float_as_uint(o[j]));
-                  if constexpr (kTwo) {
-                    const float2 lo = to_floats<T>(__float_as_uint(o[16 + j]));
-                    v.x = (v.x + lo.x) * e;
-                    v.y = (v.y + lo.y) * e;
-                    o[j] = __uint_as_float(take_pair<T>(v.x, v.y));
-                    o[16 + j] = __uint_as_float(to_pair<T>(v.x, v.y));
-                  } else {
-                    o[j] = __uint_as_float(to_pair<T>(v.x * e, v.y * e));
-                  }
-                }
-                store32(t_s + 32 * k, o);
-              }
-            }
-            load32(t_s + 32 * c, s);
-            wait_ld(s);
-            mask(s, c);
-            sum = weigh(s, 0);
-            load32(t_s + 32 * c + 32, s);
-            wait_ld(s);
-            mask(s, c + 1);
-            sum += weigh(s, 1);
+          if (__builtin_expect(!pair_any(pair, over || !there), 1)) break;
+          if (pair_any(pair, !there)) {
+            ok = false;
+            break;
           }
-          l += sum;
-          // where these columns of S stood
-          if constexpr (kTwo) {
-            tmem_st32(t_s + 32 * c, p);
-            tmem_st32(t_s + 32 * c + 32, p + 32);
-          } else {
-            tmem_st32(t_s + 32 * c, p);
-          }
-        }
-        if (__builtin_expect(i > 0 && __any_sync(0xffffffffu, by_o != 1.f), 0)) {
-          float o[32];
+          float top = -INFINITY;
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
-            load32(t_o + 32 * c, o);
-            wait_ld(o);
+            float s[16];
+            load16(t_s + 16 * c, s);
+            wait_ld(s);
+            mask(s, c);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] *= by_o;
-            store32(t_o + 32 * c, o);
+            for (int j = 0; j < 16; ++j) top = fmaxf(top, s[j]);
+          }
+          s_pair[half][r] = make_float2(top * f, over ? 1.f : 0.f);
+          pair_any(pair, false);
+          const float2 other = s_pair[half ^ 1][r];
+          const float u = over || other.y != 0.f ? fmaxf(m, fmaxf(top * f, other.x)) : m, e = ex2(m - u);
+          m = u;
+          l *= e;
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float o[16];
+              load16(t_o + 16 * c, o);
+              wait_ld(o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] *= e;
+              tmem_st16(t_o + 16 * c, reinterpret_cast<const uint32_t*>(o));
+            }
           }
         }
+        if (!ok) break;
+        l += sum;
+        // where these columns of S stood
+        tmem_st32(t_s, p);
+        if constexpr (kTwo) tmem_st32(t_s + 32, p + 32);
         wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull0 + t));
       }
-      if (!ok || !(ok = warp_wait(kODone0 + t, served++ & 1))) break;
+      if (!ok) break;
+      const bool there = warp_wait(kODone0 + t, served++ & 1);
       fence_after();
+      s_pair[half][r].x = l;
+      if (pair_any(pair, !there)) break;
+      l += s_pair[half ^ 1][r].x;
+      pair_any(pair, false);   // read before it is written again
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
       const bool whole = w.slot < 0;
       const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.rec_o)) & 31) == 0;
       const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + w.h * a.group + head;
       const long long rec = static_cast<long long>(w.slot) * a.part_rows + r;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {   // 32 bytes a store: whole sectors, though a row a thread
+      for (int c = 0; c < 2; ++c) {   // 32 bytes a store: whole sectors, though a row a thread
         float o[32];
         load32(t_o + 32 * c, o);
         wait_ld(o);
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
         if (live) {
-          if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kKvD + 32 * c, o, wide);
-          else write32<float>(a.rec_o + rec * kKvD + 32 * c, o, wide);
+          if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kKvD + half * 64 + 32 * c, o, wide);
+          else write32<float>(a.rec_o + rec * kKvD + half * 64 + 32 * c, o, wide);
         }
       }
-      if (live && !whole) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
+      if (live && !whole && half == 0) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
     }
-  } else if (warp == 8) {
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+  if (warp == 16) {
     // ---- products. The whole warp walks the steps, so that descriptors and addresses
     // stay in uniform registers; one lane, always the same, issues.
     const bool leader = elect_one();
@@ -529,16 +548,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       warp_wait(kEnd, 0);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     // ---- the work, keys and values
     Line line(a, per, lane);
     const long long cut = line.total / 2;   // two steps a CTA at least
     const long long ctas = cut < 1 ? 1 : (cut < gridDim.x ? cut : gridDim.x);
     long long x = 0, end = 0;
     if (blockIdx.x < ctas && line.total > 0) {
-      end = line.snapped(line.total * (blockIdx.x + 1) / ctas);
-      x = line.snapped(line.total * blockIdx.x / ctas);
-      if (x < end) line.find(x);
+      x = line.total * blockIdx.x / ctas;
+      end = line.total * (blockIdx.x + 1) / ctas;
+      line.go(x, end);
     }
     if (a.may_split && lane == 0) a.split_units[blockIdx.x] = make_int4(0, 0, 0, 0);
     const unsigned group16 = lane & 7;
@@ -550,31 +569,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       Work w = {};
       w.seq = -1;
       if (x < end) {
-        const int src = line.b & 31;
+        const int src = line.at.b & 31;
         Chunk ch;
         ch.q0 = __shfl_sync(0xffffffffu, line.ch.q0, src);
         ch.n = __shfl_sync(0xffffffffu, line.ch.n, src);
         ch.len = __shfl_sync(0xffffffffu, line.ch.len, src);
-        const int served = min(ch.n, a.max_q_len), first = line.j * per;
+        const int served = min(ch.n, a.max_q_len), first = line.at.j * per;
         const long long left = end - x;
-        const int steps = left < line.steps - line.off ? static_cast<int>(left) : line.steps - line.off;
-        w.seq = line.b;
-        w.h = line.h;
+        const int steps = left < line.at.steps - line.at.off ? static_cast<int>(left) : line.at.steps - line.at.off;
+        w.seq = line.at.b;
+        w.h = line.at.h;
         w.q0 = ch.q0 + first;
         w.rows = min(per, served - first) * a.group;
         w.pos0 = ch.len - ch.n + first;
-        w.limit = limit_of(a, ch, line.j, per);
-        w.tile0 = line.off;
+        w.limit = limit_of(a, ch, line.at.j, per);
+        w.tile0 = line.at.off;
         w.tiles = w.limit == 0 ? 0 : steps;
-        w.slot = line.off > 0 ? 2 * static_cast<int>(blockIdx.x) : (steps < line.steps ? 2 * static_cast<int>(blockIdx.x) + 1 : -1);
+        w.slot = line.at.off > 0 ? 2 * static_cast<int>(blockIdx.x) : (steps < line.at.steps ? 2 * static_cast<int>(blockIdx.x) + 1 : -1);
         w.zero0 = ch.q0 + served;
-        w.zeros = line.j == 0 && line.off == 0 ? ch.n - served : 0;   // queries past max_q_len
+        w.zeros = line.at.j == 0 && line.at.off == 0 ? ch.n - served : 0;   // queries past max_q_len
         w.step0 = step;
-        if (line.j == 0 && line.off == 0 && line.h == 0 && lane == 0 && (ch.n > a.max_q_len || ch.len > a.limit))
+        if (line.at.j == 0 && line.at.off == 0 && line.at.h == 0 && lane == 0 && (ch.n > a.max_q_len || ch.len > a.limit))
           b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
-        if (line.off == 0 && steps < line.steps && lane == 0) {
+        if (line.at.off == 0 && steps < line.at.steps && lane == 0) {
           // who has the unit's last step, unless the cut before that one moved behind it
-          const long long last = x + line.steps;
+          const long long last = x + line.at.steps;
           long long owner = (last * ctas - 1) / line.total;
           if (last - line.total * owner / ctas < 2) --owner;
           a.split_units[blockIdx.x] = make_int4(w.q0, w.rows, w.h * a.group, static_cast<int>(owner) - blockIdx.x + 1);
@@ -674,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       if (!(ok = long_wait(kQEmpty, (filled++ & 1) ^ 1, wait_for))) break;
       const int c = lane & 15, last = rows > 128 ? kRows : 128;
 #pragma unroll 8
-      for (int r = 2 * (warp - 10) + (lane >> 4); r < last; r += 4) {
+      for (int r = 2 * (warp - 18) + (lane >> 4); r < last; r += 4) {
         const int qi = static_cast<int>(r * by_group >> 16), head = head0 + r - qi * a.group;
         const T* src = static_cast<const T*>(a.q) + (r < rows ? (q0 + qi) * a.q_stride + static_cast<long long>(head) * kKvD + 8 * c : 0);
         const uint32_t to = base + (r >> 7) * kTileOp + (c >> 3) * kHalfQ + (r & 127) * 128 + (((c ^ r) & 7) << 4);
@@ -686,10 +705,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       if (lane == 0) mbar_arrive(bar(kQFull));
     }
   }
+  }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
 }
 
 // Merges the parts of split units: a warp a row, 8 rows of a unit a CTA.
