@@ -40,16 +40,17 @@
 namespace tq {
 namespace {
 
-constexpr int kRows = 256;             // of a unit: two tiles of 128
-constexpr int kCols = 128;             // positions a step
-constexpr int kThreads = 640;
+constexpr int kRows = 256;             // of a unit, a CTA: two tiles of 128
+constexpr int kCols = 128;             // positions a step, in two halves
+constexpr int kThreads = 512;
 constexpr int kCtas = 152;             // grid, one an SM: sizes the workspace without a device query
 constexpr float kMost = 60000.f;       // sums of P up to this: every P fits in fp16
 constexpr uint32_t kTileOp = 32768;    // a 128 x 128 operand
 constexpr uint32_t kHalfQ = 16384;     // Q: two halves of 64 columns, 128 bytes a row
 constexpr uint32_t kOffK = 2 * kTileOp, kOffV = 4 * kTileOp, kOffBar = 6 * kTileOp;
-constexpr uint32_t kSmem = kOffBar + 256 + 1024;   // and room to align to 1024
-constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns
+constexpr uint32_t kSmem = kOffBar + 512 + 1024;   // and room to align to 1024
+constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: two halves' S of each tile, O of each tile
+constexpr int kPairRows = 256;                     // rows a chunk, on average, from which on pairs of CTAs are used
 constexpr unsigned long long kStepNs = 100000;     // what a step may take, where a wait is for many
 
 struct ChunkArgs {
@@ -70,36 +71,34 @@ struct ChunkArgs {
 
 // barriers, 8 bytes each from kOffBar
 enum {
-  kWFull0, kWFull1, kWEmpty0, kWEmpty1, kQFull, kQEmpty, kKFull0, kKFull1, kVFull0, kVFull1, kKEmpty0, kKEmpty1, kVEmpty0, kVEmpty1,
-  kSFull0, kSFull1, kPFull0, kPFull1, kODone0, kODone1, kEnd, kBars
+  kWFull0, kWFull1, kWEmpty0, kWEmpty1, kQFull, kQEmpty, kODone0, kODone1, kEnd0, kEnd1, kSFull0, kPFull0 = kSFull0 + 4,
+  kKFull0 = kPFull0 + 4, kVFull0 = kKFull0 + 4, kKEmpty0 = kVFull0 + 4, kVEmpty0 = kKEmpty0 + 4, kKPeer0 = kVEmpty0 + 4, kVPeer0 = kKPeer0 + 4,
+  kBars = kVPeer0 + 4
 };
-static_assert(kBars * 8 <= 256, "barriers");
+static_assert(kBars * 8 <= 512, "barriers");
 
 // shared-memory operand descriptors, 128-byte swizzle. Q: 8-row groups 1024 bytes
-// apart; K: 2048 (its halves lie 1024 behind); V: halves 1024 apart, groups 2048.
+// apart; K: 2048 (its halves lie 1024 behind); V: halves 1024 apart, groups 2048 (a pair:
+// one half, groups 1024 apart).
 __device__ __forceinline__ uint64_t desc_q(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 __device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
   return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (1ull << 16) | (128ull << 32) | (1ull << 46) | (2ull << 61);
 }
+template <int CTAS>
 __device__ __forceinline__ uint64_t desc_v(uint32_t addr) {
-  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (64ull << 16) | (128ull << 32) | (1ull << 46) | (2ull << 61);
+  return static_cast<uint64_t>((addr & 0x3ffff) >> 4) | (64ull << 16) | ((CTAS == 2 ? 64ull : 128ull) << 32) | (1ull << 46) | (2ull << 61);
 }
-// f16 x f16 or bf16 x bf16 -> f32, M = 128, N = 128
-template <typename T>
+// f16 x f16 or bf16 x bf16 -> f32, M = 128 a CTA, N = 64 positions or 128 coordinates
+template <typename T, int CTAS>
 __device__ __forceinline__ constexpr uint32_t idesc_qk() {
-  return (1u << 4) | (std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u) | ((128u / 8) << 17) | ((128u / 16) << 24);
+  return (1u << 4) | (std::is_same<T, __nv_bfloat16>::value ? (1u << 7) | (1u << 10) : 0u) | ((64u / 8) << 17) | ((CTAS * 128u / 16) << 24);
 }
-template <typename T>
-__device__ __forceinline__ constexpr uint32_t idesc_pv() { return idesc_qk<T>() | (1u << 16); }   // B is MN-major
+template <typename T, int CTAS>
+__device__ __forceinline__ constexpr uint32_t idesc_pv() { return idesc_qk<T, CTAS>() + ((64u / 8) << 17) + (1u << 16); }   // B is MN-major
 
 // Waits for the loads from tensor memory; what they brought is not used before.
-__device__ __forceinline__ void wait_ld(float (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]),
-                 "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])::"memory");
-}
 __device__ __forceinline__ void wait_ld(float (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]), "+f"(r[8]), "+f"(r[9]),
@@ -107,18 +106,7 @@ __device__ __forceinline__ void wait_ld(float (&r)[32]) {
                  "+f"(r[19]), "+f"(r[20]), "+f"(r[21]), "+f"(r[22]), "+f"(r[23]), "+f"(r[24]), "+f"(r[25]), "+f"(r[26]), "+f"(r[27]),
                  "+f"(r[28]), "+f"(r[29]), "+f"(r[30]), "+f"(r[31])::"memory");
 }
-__device__ __forceinline__ void load16(uint32_t addr, float (&r)[16]) { tmem_ld16(addr, reinterpret_cast<uint32_t*>(r)); }
 __device__ __forceinline__ void load32(uint32_t addr, float (&r)[32]) { tmem_ld32(addr, reinterpret_cast<uint32_t*>(r)); }
-
-// Waits for the other warp of the pair; true if `x` is true in any lane of either.
-__device__ __forceinline__ bool pair_any(int id, bool x) {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n barrier.cta.red.or.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-               : "=r"(r)
-               : "r"(id), "r"(static_cast<uint32_t>(x))
-               : "memory");
-  return r != 0;
-}
 
 // A part of a unit, as a CTA works on it.
 struct Work {
@@ -128,6 +116,7 @@ struct Work {
   int pos0;            // position of that query (may be negative)
   int limit;           // positions that its last query sees: what stands behind them need not have been stored
   int tile0, tiles;    // steps: [tile0, tile0 + tiles); none: zeros are written
+  int halves;          // of them, those that anybody sees
   int zero0, zeros;    // queries that nobody serves
   unsigned step0;      // steps of the CTA before
 };
@@ -249,31 +238,44 @@ struct Line {
   }
 };
 
-template <typename T, typename TO>
+template <typename T, typename TO, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs a) {
   constexpr bool kTwo = std::is_same<TO, float>::value;   // P in two parts
+  constexpr int kStages = 2 * CTAS, kLog = CTAS;          // of keys and of values, 64 KB each in all
+  constexpr uint32_t kStage = kTileOp / CTAS;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Work s_work[2];
-  __shared__ unsigned s_bad[4];   // a step's groups of 16 positions whose block id is bad
-  __shared__ float2 s_pair[2][kRows];   // what the two threads of a row tell one another
+  __shared__ unsigned s_bad[2 * kStages];   // a step's groups of 16 positions whose block id is bad
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 1023u) & ~1023u;
   const uint32_t bars = base + kOffBar;
   auto bar = [&](int i) { return bars + 8u * static_cast<uint32_t>(i); };
+  const int rank = CTAS == 2 ? static_cast<int>(cluster_rank()) : 0;   // 0 issues the products
+  const int team = blockIdx.x / CTAS, teams = gridDim.x / CTAS;
   if (threadIdx.x == 32) {
-    for (int i = 0; i < kBars; ++i) mbar_init(bar(i), i == kWEmpty0 || i == kWEmpty1 ? 19 : (i == kPFull0 || i == kPFull1 ? 8 : (i == kQFull ? 2 : 1)));
+    for (int i = 0; i < kBars; ++i)
+      mbar_init(bar(i), i == kWEmpty0 || i == kWEmpty1 ? 15
+                        : (i >= kPFull0 && i < kPFull0 + 4) || i == kQFull ? 4 * CTAS
+                        : i == kQEmpty || (i >= kKEmpty0 && i < kVEmpty0 + 4) ? 2 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 16) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(&s_tmem))) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  if (warp == 8) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(&s_tmem));
+    if constexpr (CTAS == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(to) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(to) : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
   }
   fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();   // the other CTA's barriers are there
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-  const int per = kRows / a.group;   // queries of a unit
+  const int per = CTAS * kRows / a.group;   // queries of a unit
   grid_dep_wait();
   grid_dep_launch();
 
@@ -283,6 +285,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     return false;
   };
   auto warp_wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };   // one answer for the warp
+  auto arrive_first = [&](int b) {   // at the barrier of the CTA that issues
+    if (rank == 0) mbar_arrive(bar(b));
+    else mbar_arrive_at(bar(b), 0);
+  };
+  auto commit = [&](int b) {
+    if constexpr (CTAS == 2) mma_commit2(bar(b));
+    else mma_commit(bar(b));
+  };
   // A wait for a whole part of `steps` steps.
   auto long_wait = [&](int b, uint32_t parity, int steps) {
     const uint64_t t0 = global_ns(), most = kWaitNs + kStepNs * static_cast<uint64_t>(steps);
@@ -294,22 +304,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     return __all_sync(0xffffffffu, ok) != 0;
   };
 
-  if (warp < 16) {
-    // ---- softmax: of tile warp / 8, two threads a row, for the left and the right 64 columns
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");   // 4 x 104 + 64 = 5 x 96 registers a thread
-    const int t = warp >> 3, half = warp >> 2 & 1;
-    const int pair = 1 + (t << 2 | (warp & 3));   // the barrier of this warp and the one of the other half
-    const unsigned by_group = (65536u + a.group - 1) / a.group;   // row / group for rows below 256, group <= 8
-    const int r = t * 128 + (warp & 3) * 32 + lane;   // this thread's row, 0 .. 255
+  if (warp < 8) {
+    // ---- softmax: of tile warp / 4, a thread a row
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");   // 2 x 192 + 2 x 64 = 4 x 128 registers a thread
+    const int t = warp >> 2;
+    const unsigned by_group = (65536u + a.group - 1) / a.group;   // row / group for rows below 512, group <= 8
+    const int r = (CTAS * t + rank) * 128 + (warp & 3) * 32 + lane;   // this thread's row of the unit
     const int qi = static_cast<int>(r * by_group >> 16), head = r - qi * a.group;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t_s = tmem + lanes + kColS + t * 128 + half * 64, t_o = tmem + lanes + kColO + t * 128 + half * 64;
+    const uint32_t t_o = tmem + lanes + kColO + t * 128;
     const float f = fmaxf(a.qscale, 0x1p-126f);   // never 0, which would make NaN of a masked place
-    unsigned steps = 0, served = 0;   // of this tile so far
+    unsigned n = 0, served = 0;   // halves of this tile so far (their S comes in that order), and parts
     int before = 0;
-    bool ok = true;   // the same for both warps of a pair, so that neither waits for one that gave up
+    bool ok = true;
     for (unsigned part = 0; ok; ++part) {
-      if (pair_any(pair, !long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
+      if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
       const Work w = s_work[part & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
@@ -317,41 +326,43 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       before = w.tiles;
       auto zero_rows = [&](int q0, int count) {   // `count` queries from q0 on, this KV head's part
         const long long all = static_cast<long long>(count) * a.group * (kKvD / 4);
-        for (long long i = threadIdx.x; i < all; i += 512) {
+        for (long long i = threadIdx.x; i < all; i += 256) {
           const long long x = i / (kKvD / 4);
           write4<TO>(static_cast<TO*>(a.out) + ((q0 + x / a.group) * a.n_q + w.h * a.group + x % a.group) * kKvD + 4 * (i % (kKvD / 4)),
                      make_float4(0.f, 0.f, 0.f, 0.f));
         }
       };
-      if (w.zeros) zero_rows(w.zero0, w.zeros);
+      if (w.zeros && rank == 0) zero_rows(w.zero0, w.zeros);
       if (w.tiles == 0) {
-        zero_rows(w.q0, w.rows / a.group);
+        if (rank == 0) zero_rows(w.q0, w.rows / a.group);
         continue;
       }
-      if (t * 128 >= w.rows) continue;
+      if (t * CTAS * 128 >= w.rows) continue;
       const bool live = r < w.rows;
       const int vis = live ? max(min(w.pos0 + qi + 1, w.limit), 0) : 0;   // positions that this row sees
       const int vis_least = __reduce_min_sync(0xffffffffu, live ? vis : 0x7fffffff);
-      float m = -1e30f, l = 0.f;   // l: sum of this thread's P
-      for (int i = 0; i < w.tiles; ++i, ++steps) {
-        const bool there = warp_wait(kSFull0 + t, steps & 1);
+      auto scores_there = [&](unsigned i) { return warp_wait(kSFull0 + 2 * t + (i & 1), i >> 1 & 1); };
+      float m = -1e30f, l = 0.f;   // l: sum of P
+      for (int i = 0; i < w.halves; ++i, ++n) {
+        if (!(ok = scores_there(n))) break;
         fence_after();
-        const int at = (w.tile0 + i) * kCols + half * 64;
-        const unsigned bad = s_bad[(w.step0 + i) & 3] >> 4 * half & 15;
+        const uint32_t t_s = tmem + lanes + kColS + t * 128 + (n & 1) * 64;
+        const int at = w.tile0 * kCols + i * 64;
+        const unsigned bad = s_bad[(w.step0 + (i >> 1)) & (2 * kStages - 1)] >> 4 * (i & 1) & 15;
         const bool masked = bad || at + 64 > vis_least;
-        auto mask = [&](float (&s)[16], int c) {
+        auto mask = [&](float (&s)[32], int c) {
           if (__builtin_expect(masked, 0)) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (at + 16 * c + j >= vis || (bad >> c & 1)) s[j] = -INFINITY;
+            for (int j = 0; j < 32; ++j)
+              if (at + 32 * c + j >= vis || (bad >> (2 * c + (j >> 4)) & 1)) s[j] = -INFINITY;
           }
         };
         uint32_t p[kTwo ? 64 : 32];   // 64 positions; in two parts: of each 32 the hi parts, then the lo parts
-        float2 x0, x1;
-        auto weigh = [&](const float (&s)[16], int c) {   // the P of 16 positions, added to the sums
+        auto weigh = [&](const float (&s)[32], int c) {   // the P of 32 positions, and their sum
           const float a0 = 3.f - m;
+          float2 x0 = make_float2(0.f, 0.f), x1 = x0;
 #pragma unroll
-          for (int j = 0; j < 16; j += 4) {
+          for (int j = 0; j < 32; j += 4) {
             float2 y0 = fma2(make_float2(s[j], s[j + 1]), make_float2(f, f), make_float2(a0, a0));
             float2 y1 = fma2(make_float2(s[j + 2], s[j + 3]), make_float2(f, f), make_float2(a0, a0));
             y0.x = ex2(y0.x);
@@ -361,78 +372,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
             x0 = add2(x0, y0);
             x1 = add2(x1, y1);
             if constexpr (kTwo) {
-              const int k = 32 * (c >> 1) + 8 * (c & 1) + j / 2;
+              const int k = 32 * c + j / 2;
               p[k] = take_pair<T>(y0.x, y0.y);
               p[k + 1] = take_pair<T>(y1.x, y1.y);
               p[k + 16] = to_pair<T>(y0.x, y0.y);
               p[k + 17] = to_pair<T>(y1.x, y1.y);
             } else {
-              p[8 * c + j / 2] = to_pair<T>(y0.x, y0.y);
-              p[8 * c + j / 2 + 1] = to_pair<T>(y1.x, y1.y);
+              p[16 * c + j / 2] = to_pair<T>(y0.x, y0.y);
+              p[16 * c + j / 2 + 1] = to_pair<T>(y1.x, y1.y);
             }
           }
-        };
-        auto weigh_all = [&]() {
-          x0 = x1 = make_float2(0.f, 0.f);
-          float s[16], z[16];
-          load16(t_s, s);
-          wait_ld(s);
-          load16(t_s + 16, z);
-          mask(s, 0);
-          weigh(s, 0);
-          wait_ld(z);
-          load16(t_s + 32, s);
-          mask(z, 1);
-          weigh(z, 1);
-          wait_ld(s);
-          load16(t_s + 48, z);
-          mask(s, 2);
-          weigh(s, 2);
-          wait_ld(z);
-          mask(z, 3);
-          weigh(z, 3);
           x0 = add2(x0, x1);
           return x0.x + x0.y;
         };
         float sum;
-        for (int go = 0;; ++go) {   // once, but for rows that outgrow their m
-          sum = weigh_all();
-          if (go) break;
-          const bool over = !(sum <= kMost);   // NaN too
-          if (__builtin_expect(!pair_any(pair, over || !there), 1)) break;
-          if (pair_any(pair, !there)) {
-            ok = false;
-            break;
-          }
-          float top = -INFINITY;
+        {
+          float x[32], y[32];
+          load32(t_s, x);
+          wait_ld(x);
+          load32(t_s + 32, y);
+          mask(x, 0);
+          sum = weigh(x, 0);
+          wait_ld(y);
+          mask(y, 1);
+          sum += weigh(y, 1);
+        }
+        const bool over = !(sum <= kMost);   // NaN too
+        if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
+          float s[32], top = -INFINITY;
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            float s[16];
-            load16(t_s + 16 * c, s);
+          for (int c = 0; c < 2; ++c) {
+            load32(t_s + 32 * c, s);
             wait_ld(s);
             mask(s, c);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) top = fmaxf(top, s[j]);
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, s[j]);
           }
-          s_pair[half][r] = make_float2(top * f, over ? 1.f : 0.f);
-          pair_any(pair, false);
-          const float2 other = s_pair[half ^ 1][r];
-          const float u = over || other.y != 0.f ? fmaxf(m, fmaxf(top * f, other.x)) : m, e = ex2(m - u);
+          const float u = over ? fmaxf(m, top * f) : m, e = ex2(m - u);
           m = u;
           l *= e;
           if (i > 0) {
+            // the next half's scores are issued after the product before this one's: once they are there, the accumulators rest
+            if (!(ok = scores_there(n + 1))) break;
+            fence_after();
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-              float o[16];
-              load16(t_o + 16 * c, o);
-              wait_ld(o);
+              load32(t_o + 32 * c, s);
+              wait_ld(s);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] *= e;
-              tmem_st16(t_o + 16 * c, reinterpret_cast<const uint32_t*>(o));
+              for (int j = 0; j < 32; ++j) s[j] *= e;
+              tmem_st32(t_o + 32 * c, reinterpret_cast<const uint32_t*>(s));
             }
           }
+          load32(t_s, s);
+          wait_ld(s);
+          mask(s, 0);
+          sum = weigh(s, 0);
+          load32(t_s + 32, s);
+          wait_ld(s);
+          mask(s, 1);
+          sum += weigh(s, 1);
         }
-        if (!ok) break;
         l += sum;
         // where these columns of S stood
         tmem_st32(t_s, p);
@@ -440,126 +440,168 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         wait_st();
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull0 + t));
+        if (lane == 0) arrive_first(kPFull0 + 2 * t + (n & 1));
       }
-      if (!ok) break;
-      const bool there = warp_wait(kODone0 + t, served++ & 1);
+      if (ok && w.halves > 1) {   // the products' sign to the last half, answered so that the barriers' phases stay alike
+        ok = scores_there(n);
+        if (lane == 0) arrive_first(kPFull0 + 2 * t + (n & 1));
+        ++n;
+      }
+      if (!ok || !(ok = warp_wait(kODone0 + t, served++ & 1))) break;
       fence_after();
-      s_pair[half][r].x = l;
-      if (pair_any(pair, !there)) break;
-      l += s_pair[half ^ 1][r].x;
-      pair_any(pair, false);   // read before it is written again
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
       const bool whole = w.slot < 0;
       const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.rec_o)) & 31) == 0;
       const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + w.h * a.group + head;
       const long long rec = static_cast<long long>(w.slot) * a.part_rows + r;
 #pragma unroll 1
-      for (int c = 0; c < 2; ++c) {   // 32 bytes a store: whole sectors, though a row a thread
+      for (int c = 0; c < 4; ++c) {   // 32 bytes a store: whole sectors, though a row a thread
         float o[32];
         load32(t_o + 32 * c, o);
         wait_ld(o);
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
         if (live) {
-          if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kKvD + half * 64 + 32 * c, o, wide);
-          else write32<float>(a.rec_o + rec * kKvD + half * 64 + 32 * c, o, wide);
+          if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kKvD + 32 * c, o, wide);
+          else write32<float>(a.rec_o + rec * kKvD + 32 * c, o, wide);
         }
       }
-      if (live && !whole && half == 0) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
+      if (live && !whole) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
     }
   } else {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-  if (warp == 16) {
-    // ---- products. The whole warp walks the steps, so that descriptors and addresses
-    // stay in uniform registers; one lane, always the same, issues.
+  if (warp < 10 && rank == 0) {
+    // ---- products, of tile warp - 8. The whole warp walks the halves of steps, so that
+    // descriptors and addresses stay in uniform registers; one lane, always the same,
+    // issues. Scores are issued two halves ahead: the softmax finds the next ones there.
     const bool leader = elect_one();
-    auto qk = [&](int t, int st) {
-      const uint64_t q_at = desc_q(base + t * kTileOp), k_at = desc_k(base + kOffK + st * kTileOp);
-      const uint32_t d = tmem + kColS + t * 128;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        mma_ss(d, q_at + (((k >> 2) * kHalfQ + (k & 3) * 32) >> 4), k_at + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_qk<T>(), k > 0);
-      mma_commit(bar(kSFull0 + t));
-    };
+    const int t = warp - 8;
+    const uint64_t q_at = desc_q(base + t * kTileOp);
+    const uint32_t o = tmem + kColO + t * 128;
     unsigned step = 0, filled = 0;   // steps and loaded queries so far
-    unsigned weighed[2] = {0, 0};    // steps of each tile
+    unsigned n = 0;                  // halves of the tile so far, as the softmax counts them
     int before = 0;
     bool ok = true;
+    auto keys_there = [&](unsigned i) {
+      const int st = i & (kStages - 1);
+      return warp_wait(kKFull0 + st, i >> kLog & 1) && (CTAS == 1 || warp_wait(kKPeer0 + st, i >> kLog & 1));
+    };
+    auto values_there = [&](unsigned i) {
+      const int st = i & (kStages - 1);
+      return warp_wait(kVFull0 + st, i >> kLog & 1) && (CTAS == 1 || warp_wait(kVPeer0 + st, i >> kLog & 1));
+    };
     for (unsigned part = 0; ok; ++part) {
       if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
-      const int seq = s_work[part & 1].seq, tiles = s_work[part & 1].tiles, halves = s_work[part & 1].rows > 128 ? 2 : 1;
+      const int seq = s_work[part & 1].seq, tiles = s_work[part & 1].tiles, halves = s_work[part & 1].halves;
+      const bool mine = s_work[part & 1].rows > t * CTAS * 128;   // else this warp only says that it is done with what is loaded
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
       if (seq < 0) break;
       before = tiles;
       if (tiles == 0) continue;
-      if (!(ok = warp_wait(kQFull, filled++ & 1) && warp_wait(kKFull0 + (step & 1), step >> 1 & 1))) break;
-      fence_after();
-      if (leader) {
-        for (int t = 0; t < halves; ++t) qk(t, step & 1);
-        mma_commit(bar(kKEmpty0 + (step & 1)));
-        if (tiles == 1) mma_commit(bar(kQEmpty));
-      }
-      __syncwarp();
-      for (int i = 0; i < tiles && ok; ++i, ++step) {
-        const int st = step & 1, nst = st ^ 1;
-        const bool more = i + 1 < tiles;
-        for (int t = 0; t < halves; ++t) {
-          if (!(ok = warp_wait(kPFull0 + t, weighed[t]++ & 1))) break;
-          if (t == 0 && !(ok = warp_wait(kVFull0 + st, step >> 1 & 1))) break;
-          fence_after();
-          if (leader) {
-            const uint64_t v_at = desc_v(base + kOffV + st * kTileOp);
-            const uint32_t d = tmem + kColO + t * 128, p = tmem + kColS + t * 128;
-            mma_ts(d, p, v_at, idesc_pv<T>(), i > 0);
+      auto qk = [&](int i) {   // S of half i
+        const int st = (step + (i >> 1)) & (kStages - 1);
+        if (leader) {
+          if (mine) {
+            const uint64_t k_at = desc_k(base + kOffK + st * kStage + (i & 1) * (kStage / 2));
+            const uint32_t d = tmem + kColS + t * 128 + ((n + i) & 1) * 64;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {   // 16 positions: 8 columns
-              const uint64_t vk = v_at + (4096 >> 4) * k;
+            for (int k = 0; k < 8; ++k) {
+              const uint64_t qq = q_at + (((k >> 2) * kHalfQ + (k & 3) * 32) >> 4), kk = k_at + (((k >> 2) * 1024 + (k & 3) * 32) >> 4);
+              if constexpr (CTAS == 2) mma_ss2(d, qq, kk, idesc_qk<T, CTAS>(), k > 0);
+              else mma_ss(d, qq, kk, idesc_qk<T, CTAS>(), k > 0);
+            }
+            commit(kSFull0 + 2 * t + ((n + i) & 1));
+          }
+          if ((i & 1) || i + 1 == halves) commit(kKEmpty0 + st);
+          if (i + 1 == halves) commit(kQEmpty);
+        }
+        __syncwarp();
+      };
+      auto pv = [&](uint32_t p, uint64_t v, bool acc) {
+        if constexpr (CTAS == 2) mma_ts2(o, p, v, idesc_pv<T, CTAS>(), acc);
+        else mma_ts(o, p, v, idesc_pv<T, CTAS>(), acc);
+      };
+      if (!(ok = warp_wait(kQFull, filled++ & 1) && keys_there(step))) break;
+      fence_after();
+      qk(0);
+      if (halves > 1) qk(1);
+      for (int i = 0; i < halves; ++i) {
+        const int st = (step + (i >> 1)) & (kStages - 1);
+        const unsigned count = n + i;
+        if (!(i & 1) && !(ok = values_there(step + (i >> 1)))) break;
+        if (mine && !(ok = warp_wait(kPFull0 + 2 * t + (count & 1), count >> 1 & 1))) break;
+        fence_after();
+        if (leader) {
+          if (mine) {
+            const uint64_t v_at = desc_v<CTAS>(base + kOffV + st * kStage + (i & 1) * (kStage / 2));
+            const uint32_t p = tmem + kColS + t * 128 + (count & 1) * 64;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {   // 16 positions: 8 columns
+              const uint64_t vk = v_at + (4096 / CTAS >> 4) * k;
               if constexpr (kTwo) {
                 const uint32_t pk = p + 32 * (k >> 1) + 8 * (k & 1);
-                if (k > 0) mma_ts(d, pk, vk, idesc_pv<T>(), true);
-                mma_ts(d, pk + 16, vk, idesc_pv<T>(), true);
+                pv(pk, vk, i > 0 || k > 0);
+                pv(pk + 16, vk, true);
               } else {
-                if (k > 0) mma_ts(d, p + 64 * (k >> 2) + 8 * (k & 3), vk, idesc_pv<T>(), true);
+                pv(p + 8 * k, vk, i > 0 || k > 0);
               }
             }
-            if (!more) mma_commit(bar(kODone0 + t));
-            if (t + 1 == halves) mma_commit(bar(kVEmpty0 + st));
+            if (i + 1 == halves) commit(kODone0 + t);
+            if (i + 2 == halves) commit(kSFull0 + 2 * t + (count & 1));   // in place of scores
           }
-          __syncwarp();
-          if (more) {
-            if (t == 0 && !(ok = warp_wait(kKFull0 + nst, (step + 1) >> 1 & 1))) break;
+          if ((i & 1) || i + 1 == halves) commit(kVEmpty0 + st);
+        }
+        __syncwarp();
+        if (i + 2 < halves) {
+          if (!(i & 1)) {
+            if (!(ok = keys_there(step + (i >> 1) + 1))) break;
             fence_after();
-            if (leader) {
-              qk(t, nst);
-              if (t + 1 == halves) {
-                mma_commit(bar(kKEmpty0 + nst));
-                if (i + 2 == tiles) mma_commit(bar(kQEmpty));
-              }
-            }
-            __syncwarp();
           }
+          qk(i + 2);
         }
       }
+      step += tiles;
+      if (mine) n += halves + (halves > 1);
     }
     if (!ok) {   // gave up: the products in flight come to rest before their memory goes
-      if (leader) mma_commit(bar(kEnd));
-      warp_wait(kEnd, 0);
+      if (leader) commit(kEnd0 + t);
+      warp_wait(kEnd0 + t, 0);
     }
     __syncwarp();
-  } else if (warp == 17) {
+  } else if (warp < 10 || warp == 11) {
+    // ---- the second CTA of a pair tells the first what it has loaded (and the other warps here only pass)
+    unsigned step = 0;
+    int before = 0;
+    bool ok = true;
+    for (unsigned part = 0; ok; ++part) {
+      if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
+      const int seq = s_work[part & 1].seq, tiles = s_work[part & 1].tiles;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
+      if (seq < 0) break;
+      before = tiles;
+      for (int i = 0; i < tiles && warp == 11 && rank == 1; ++i, ++step) {
+        const int st = step & (kStages - 1);
+        if (!(ok = warp_wait(kKFull0 + st, step >> kLog & 1))) break;
+        if (lane == 0) arrive_first(kKPeer0 + st);
+        if (!(ok = warp_wait(kVFull0 + st, step >> kLog & 1))) break;
+        if (lane == 0) arrive_first(kVPeer0 + st);
+      }
+    }
+  } else if (warp == 10) {
     // ---- the work, keys and values
     Line line(a, per, lane);
-    const long long cut = line.total / 2;   // two steps a CTA at least
-    const long long ctas = cut < 1 ? 1 : (cut < gridDim.x ? cut : gridDim.x);
+    const long long cut = line.total / 2;   // two steps a team at least
+    const long long ctas = cut < 1 ? 1 : (cut < teams ? cut : teams);
     long long x = 0, end = 0;
-    if (blockIdx.x < ctas && line.total > 0) {
-      x = line.total * blockIdx.x / ctas;
-      end = line.total * (blockIdx.x + 1) / ctas;
+    if (team < ctas && line.total > 0) {
+      x = line.total * team / ctas;
+      end = line.total * (team + 1) / ctas;
       line.go(x, end);
     }
-    if (a.may_split && lane == 0) a.split_units[blockIdx.x] = make_int4(0, 0, 0, 0);
+    const bool speaks = rank == 0 && lane == 0;
+    if (a.may_split && speaks) a.split_units[team] = make_int4(0, 0, 0, 0);
     const unsigned group16 = lane & 7;
     unsigned step = 0;
     int before = 0, before2 = 0;   // steps of the parts that the slot's last reader may be at
@@ -585,18 +627,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         w.limit = limit_of(a, ch, line.at.j, per);
         w.tile0 = line.at.off;
         w.tiles = w.limit == 0 ? 0 : steps;
-        w.slot = line.at.off > 0 ? 2 * static_cast<int>(blockIdx.x) : (steps < line.at.steps ? 2 * static_cast<int>(blockIdx.x) + 1 : -1);
+        w.halves = min((w.limit + 63) / 64 - 2 * w.tile0, 2 * w.tiles);
+        w.slot = line.at.off > 0 ? 2 * team : (steps < line.at.steps ? 2 * team + 1 : -1);
         w.zero0 = ch.q0 + served;
         w.zeros = line.at.j == 0 && line.at.off == 0 ? ch.n - served : 0;   // queries past max_q_len
         w.step0 = step;
-        if (line.at.j == 0 && line.at.off == 0 && line.at.h == 0 && lane == 0 && (ch.n > a.max_q_len || ch.len > a.limit))
+        if (line.at.j == 0 && line.at.off == 0 && line.at.h == 0 && speaks && (ch.n > a.max_q_len || ch.len > a.limit))
           b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
-        if (line.at.off == 0 && steps < line.at.steps && lane == 0) {
+        if (line.at.off == 0 && steps < line.at.steps && speaks) {
           // who has the unit's last step, unless the cut before that one moved behind it
           const long long last = x + line.at.steps;
           long long owner = (last * ctas - 1) / line.total;
           if (last - line.total * owner / ctas < 2) --owner;
-          a.split_units[blockIdx.x] = make_int4(w.q0, w.rows, w.h * a.group, static_cast<int>(owner) - blockIdx.x + 1);
+          a.split_units[team] = make_int4(w.q0, w.rows, w.h * a.group, static_cast<int>(owner) - team + 1);
         }
         x += steps;
       }
@@ -614,8 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       };
       int blk = block_of(0);
       for (int i = 0; i < w.tiles; ++i, ++step) {
-        const int st = step & 1;
-        const uint32_t free_phase = (step >> 1 & 1) ^ 1;
+        const int st = step & (kStages - 1);
+        const uint32_t free_phase = (step >> kLog & 1) ^ 1;
         const int blk_next = block_of(i + 1);
         const int g16 = (w.tile0 + i) * 8 + group16;
         const bool inside = g16 * 16 < w.limit, good = inside && a.c.good(blk);
@@ -623,26 +666,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         const int rows = good ? min(w.limit - g16 * 16, kKvRows) : 0;   // of values: rows behind the end may hold anything
         const unsigned all = __ballot_sync(0xffffffffu, good) & 0xffu, bad = __ballot_sync(0xffffffffu, inside && !good) & 0xffu;
         const unsigned ragged = __ballot_sync(0xffffffffu, rows < kKvRows) & 0xffu;
-        if (bad && lane == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
+        if (bad && speaks) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
         if (!(ok = warp_wait(kKEmpty0 + st, free_phase))) break;
-        const uint32_t k_to = base + kOffK + st * kTileOp + group16 * kKvHalfBytes, v_to = base + kOffV + st * kTileOp;
+        // keys: all, or this CTA's 32 positions of each half; values: all coordinates, or this CTA's 64
+        const unsigned keys = CTAS == 2 ? all & 0x33u << 2 * rank : all;
+        const uint32_t k_to = base + kOffK + st * kStage + (CTAS == 2 ? (group16 & 1) + (group16 >> 2) * 2 : group16) * kKvHalfBytes, v_to = base + kOffV + st * kStage;
         if (lane == 0) {
-          s_bad[step & 3] = bad;
-          mbar_expect(bar(kKFull0 + st), __popc(all) * kKvHalfBytes);
+          s_bad[step & (2 * kStages - 1)] = bad;
+          mbar_expect(bar(kKFull0 + st), __popc(keys) * kKvHalfBytes);
         }
         __syncwarp();
-        if (lane < 8 && good) bulk_g2s_plain(k_to, src, kKvHalfBytes, bar(kKFull0 + st));
+        if (lane < 8 && (keys >> lane & 1)) bulk_g2s_plain(k_to, src, kKvHalfBytes, bar(kKFull0 + st));
         if (!(ok = warp_wait(kVEmpty0 + st, free_phase))) break;
-        uint32_t bytes = __popc(all) * kKvHalfBytes;
+        constexpr int kRowBytes = 256 / CTAS, kTileV = kKvHalfBytes / CTAS;   // of values, here
+        uint32_t bytes = __popc(all) * kTileV;
         if (__builtin_expect(ragged, 0)) {   // their rows that are not loaded are 0: no weight takes NaN along
           bytes = 0;
 #pragma unroll 1
           for (int g = 0; g < 8; ++g) {
             const int have = __shfl_sync(0xffffffffu, rows, g);
-            bytes += have * 256;
-            for (int k = lane; k < 256 && have < kKvRows; k += 32)
-              if ((k >> 7) * 8 + (k >> 3 & 7) >= have)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(v_to + g * kKvHalfBytes + 16 * k), "r"(0u) : "memory");
+            bytes += have * kRowBytes;
+            for (int k = lane; k < kTileV / 16 && have < kKvRows; k += 32)
+              if (k / (kTileV / 32) * 8 + (k >> 3 & 7) >= have)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(v_to + g * kTileV + 16 * k), "r"(0u) : "memory");
           }
           fence_smem_async();
           __syncwarp();
@@ -650,17 +696,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         if (lane == 0) mbar_expect(bar(kVFull0 + st), bytes);
         __syncwarp();
         if (lane < 8 && rows > 0) {
-          const uint32_t to = v_to + group16 * kKvHalfBytes;
-          const uint8_t* from = src + kKvHalfBytes;
-          if (rows == kKvRows) {
+          const uint32_t to = v_to + group16 * kTileV;
+          const uint8_t* from = src + kKvHalfBytes + (CTAS == 2 ? rank * 1024 : 0);
+          if (CTAS == 1 && rows == kKvRows) {
             bulk_g2s_plain(to, from, kKvHalfBytes, bar(kVFull0 + st));
-          } else {   // whole groups of 8 rows, then the rows of one group, half by half
+          } else if constexpr (CTAS == 1) {   // whole groups of 8 rows, then the rows of one group, half by half
             const int whole = rows >> 3 << 11, rest = (rows & 7) * 128;
             if (whole) bulk_g2s_plain(to, from, whole, bar(kVFull0 + st));
             if (rest) {
               bulk_g2s_plain(to + whole, from + whole, rest, bar(kVFull0 + st));
               bulk_g2s_plain(to + whole + 1024, from + whole + 1024, rest, bar(kVFull0 + st));
             }
+          } else {   // the two groups of 8 rows
+            bulk_g2s_plain(to, from, min(rows, 8) * 128, bar(kVFull0 + st));
+            if (rows > 8) bulk_g2s_plain(to + 1024, from + 2048, (rows - 8) * 128, bar(kVFull0 + st));
           }
         }
         __syncwarp();
@@ -670,9 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       if (x < end) line.next();
     }
     // the copies in flight end before their memory goes
-    for (unsigned k = step > 2 ? step - 2 : 0; k < step; ++k) {
-      warp_wait(kKFull0 + (k & 1), k >> 1 & 1);
-      warp_wait(kVFull0 + (k & 1), k >> 1 & 1);
+    for (unsigned k = step > kStages ? step - kStages : 0; k < step; ++k) {
+      warp_wait(kKFull0 + (k & (kStages - 1)), k >> kLog & 1);
+      warp_wait(kVFull0 + (k & (kStages - 1)), k >> kLog & 1);
     }
   } else {
     // ---- queries: half a warp a row, as they are
@@ -691,25 +740,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       before = tiles;
       if (tiles == 0) continue;
       if (!(ok = long_wait(kQEmpty, (filled++ & 1) ^ 1, wait_for))) break;
-      const int c = lane & 15, last = rows > 128 ? kRows : 128;
+      const int c = lane & 15, last = rows > CTAS * 128 ? kRows : 128;
 #pragma unroll 8
-      for (int r = 2 * (warp - 18) + (lane >> 4); r < last; r += 4) {
+      for (int here = 2 * (warp - 12) + (lane >> 4); here < last; here += 8) {
+        const int r = CTAS == 2 ? here + (here & 128) + 128 * rank : here;   // of the unit
         const int qi = static_cast<int>(r * by_group >> 16), head = head0 + r - qi * a.group;
         const T* src = static_cast<const T*>(a.q) + (r < rows ? (q0 + qi) * a.q_stride + static_cast<long long>(head) * kKvD + 8 * c : 0);
-        const uint32_t to = base + (r >> 7) * kTileOp + (c >> 3) * kHalfQ + (r & 127) * 128 + (((c ^ r) & 7) << 4);
+        const uint32_t to = base + (here >> 7) * kTileOp + (c >> 3) * kHalfQ + (here & 127) * 128 + (((c ^ here) & 7) << 4);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(src), "r"(r < rows ? 16 : 0) : "memory");
       }
       asm volatile("cp.async.wait_all;\n" ::: "memory");
       fence_smem_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kQFull));
+      if (lane == 0) arrive_first(kQFull);
     }
   }
   }
   fence_before();
   __syncthreads();
+  if constexpr (CTAS == 2) cluster_sync();   // the other CTA is done with this one's barriers and memory
   fence_after();
-  if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+  if (warp == 8) {
+    if constexpr (CTAS == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+    else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tmem));
+  }
 }
 
 // Merges the parts of split units: a warp a row, 8 rows of a unit a CTA.
@@ -756,12 +810,15 @@ __global__ void __launch_bounds__(256) kv16_chunk_merge_kernel(const ChunkArgs a
 // The grid, and the workspace that split units take.
 struct Plan {
   long long units;   // (tile of queries, KV head), at most
+  int ctas;          // that work on a unit together
   int may_split, part_rows;
   size_t workspace;
 };
 Plan plan_for(const tq_config* cfg, int batch, int total_q, int max_q_len, int max_seq_len) {
   Plan p;
-  const int group = cfg->num_q_heads / cfg->num_kv_heads, per = kRows / group;
+  const int group = cfg->num_q_heads / cfg->num_kv_heads;
+  p.ctas = batch > 0 && static_cast<long long>(total_q) * group > static_cast<long long>(kPairRows) * batch ? 2 : 1;
+  const int per = p.ctas * kRows / group;
   const int longest = max_q_len < total_q ? max_q_len : total_q;
   // tiles of queries: a full one for every `per` rows at most, and one more for every
   // chunk; as many for every sequence as the longest chunk has at most
@@ -771,25 +828,30 @@ Plan plan_for(const tq_config* cfg, int batch, int total_q, int max_q_len, int m
   p.units = tiles * cfg->num_kv_heads;
   p.may_split = p.units > 0 && max_seq_len > 3 * kCols;   // a unit of three steps has no cut that stays where it is
   p.part_rows = longest < per ? longest * group : per * group;
-  const size_t records = static_cast<size_t>(2 * kCtas) * p.part_rows;
+  const size_t records = static_cast<size_t>(2 * kCtas / p.ctas) * p.part_rows;
   p.workspace = p.may_split ? (kCtas * sizeof(int4) + records * (kKvD + 1) * sizeof(float) + 15) / 16 * 16 : 16;
   return p;
 }
 
-template <typename T, typename TO>
+template <typename T, typename TO, int CTAS>
 cudaError_t launch(const ChunkArgs& a, const Plan& p, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   int dev = 0, sms = 0;
   cudaError_t err = b8_current_device(&dev, &sms);
-  if (err == cudaSuccess) err = b8_allow_smem(kv16_chunk_kernel<T, TO>, kSmem, dev, &done);
+  if (err == cudaSuccess) err = b8_allow_smem(kv16_chunk_kernel<T, TO, CTAS>, kSmem, dev, &done);
   if (err != cudaSuccess) return err;
-  const int ctas = sms < kCtas ? sms : kCtas;
+  const int most = (sms < kCtas ? sms : kCtas) / CTAS;
   // starts that go backwards may name more units than these: they are served all the same
   const long long steps = p.units * ((static_cast<long long>(a.limit) + kCols - 1) / kCols + 1);
-  const int grid = steps / 2 + 1 < ctas ? static_cast<int>(steps / 2 + 1) : ctas;
-  err = launch_pdl(kv16_chunk_kernel<T, TO>, dim3(grid), dim3(kThreads), kSmem, s, a);
+  const int teams = steps / 2 + 1 < most ? static_cast<int>(steps / 2 + 1) : most;
+  if (CTAS == 2) err = launch_pdl_cluster(kv16_chunk_kernel<T, TO, CTAS>, dim3(2 * teams), dim3(kThreads), 2, kSmem, s, a);
+  else err = launch_pdl(kv16_chunk_kernel<T, TO, CTAS>, dim3(teams), dim3(kThreads), kSmem, s, a);
   if (err != cudaSuccess || !p.may_split) return err;
-  return launch_pdl(kv16_chunk_merge_kernel<TO>, dim3(grid * ((p.part_rows + 7) / 8)), dim3(256), 0, s, a);
+  return launch_pdl(kv16_chunk_merge_kernel<TO>, dim3(teams * ((p.part_rows + 7) / 8)), dim3(256), 0, s, a);
+}
+template <typename T, typename TO>
+cudaError_t launch(const ChunkArgs& a, const Plan& p, cudaStream_t s) {
+  return p.ctas == 2 ? launch<T, TO, 2>(a, p, s) : launch<T, TO, 1>(a, p, s);
 }
 template <typename T>
 cudaError_t launch(const ChunkArgs& a, const Plan& p, int out_dtype, cudaStream_t s) {
@@ -851,7 +913,7 @@ tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stri
   a.qscale = b8_qscale(scale);
   a.split_units = static_cast<int4*>(workspace);
   a.rec_o = reinterpret_cast<float*>(a.split_units + kCtas);
-  a.rec_lse = a.rec_o + static_cast<size_t>(2 * kCtas) * p.part_rows * kKvD;
+  a.rec_lse = a.rec_o + static_cast<size_t>(2 * kCtas / p.ctas) * p.part_rows * kKvD;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t err = L.is_bf16 ? launch<__nv_bfloat16>(a, p, out_dtype, s) : launch<__half>(a, p, out_dtype, s);
   return err == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
