@@ -47,8 +47,10 @@ constexpr int kCtas = 152;             // grid, one an SM: sizes the workspace w
 constexpr float kMost = 60000.f;       // sums of P up to this: every P fits in fp16
 constexpr uint32_t kTileOp = 32768;    // a 128 x 128 operand
 constexpr uint32_t kHalfQ = 16384;     // Q: two halves of 64 columns, 128 bytes a row
-constexpr uint32_t kOffK = 2 * kTileOp, kOffV = 4 * kTileOp, kOffBar = 6 * kTileOp;
+constexpr int kStages = 5;             // of what is loaded at once: 16 KB of keys, then 16 KB of values
+constexpr uint32_t kStage = 32768, kOffLoads = 2 * kTileOp, kOffBar = kOffLoads + kStages * kStage;
 constexpr uint32_t kSmem = kOffBar + 512 + 1024;   // and room to align to 1024
+constexpr int kBad = 16;               // loads whose bad blocks are remembered (more than are between the loads and the softmax)
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: two halves' S of each tile, O of each tile
 constexpr int kPairRows = 256;                     // rows a chunk, on average, from which on pairs of CTAs are used
 constexpr unsigned long long kStepNs = 100000;     // what a step may take, where a wait is for many
@@ -71,11 +73,22 @@ struct ChunkArgs {
 
 // barriers, 8 bytes each from kOffBar
 enum {
-  kWFull0, kWFull1, kWEmpty0, kWEmpty1, kQFull, kQEmpty, kODone0, kODone1, kEnd0, kEnd1, kSFull0, kPFull0 = kSFull0 + 4,
-  kKFull0 = kPFull0 + 4, kVFull0 = kKFull0 + 4, kKEmpty0 = kVFull0 + 4, kVEmpty0 = kKEmpty0 + 4, kKPeer0 = kVEmpty0 + 4, kVPeer0 = kKPeer0 + 4,
-  kBars = kVPeer0 + 4
+  kWFull0, kWFull1, kWEmpty0, kWEmpty1, kQFull, kQEmpty, kODone0, kODone1, kEnd0, kEnd1, kTurn0, kTurn1, kSFull0, kPFull0 = kSFull0 + 4,
+  kFull0 = kPFull0 + 4, kEmpty0 = kFull0 + kStages, kBars = kEmpty0 + kStages
 };
 static_assert(kBars * 8 <= 512, "barriers");
+
+// The stage of a load and its round through the stages.
+struct Turn {
+  int stage = 0;
+  uint32_t round = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kStages) {
+      stage = 0;
+      round ^= 1;
+    }
+  }
+};
 
 // shared-memory operand descriptors, 128-byte swizzle. Q: 8-row groups 1024 bytes
 // apart; K: 2048 (its halves lie 1024 behind); V: halves 1024 apart, groups 2048 (a pair:
@@ -108,6 +121,16 @@ __device__ __forceinline__ void wait_ld(float (&r)[32]) {
 }
 __device__ __forceinline__ void load32(uint32_t addr, float (&r)[32]) { tmem_ld32(addr, reinterpret_cast<uint32_t*>(r)); }
 
+// mbar_try without a wait.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(bar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+
 // A part of a unit, as a CTA works on it.
 struct Work {
   int seq, h;          // sequence (-1: the end), KV head
@@ -117,8 +140,9 @@ struct Work {
   int limit;           // positions that its last query sees: what stands behind them need not have been stored
   int tile0, tiles;    // steps: [tile0, tile0 + tiles); none: zeros are written
   int halves;          // of them, those that anybody sees
+  int loads;           // that bring them: CTAS halves each
   int zero0, zeros;    // queries that nobody serves
-  unsigned step0;      // steps of the CTA before
+  unsigned load0;      // loads of the CTA before
 };
 
 // A sequence's chunk: its first row, queries, length and tiles of queries.
@@ -147,26 +171,35 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 }
 
 // The line: for each tile index j, each sequence that has such a tile, each KV head,
-// its steps. (Units that read the same keys and values, tiles of one chunk, are then a
-// fixed part of the line apart, so that CTAs meet them at the same time where chunks
-// are alike.) A warp walks it, the lanes together.
+// the cost of the unit. (Units that read the same keys and values, tiles of one chunk,
+// are then a fixed part of the line apart, so that teams of CTAs meet them at the same
+// time where chunks are alike.) A step costs 4, or 3 where one row tile is at work, and
+// a unit 10 more (1.57, 1.21 and 3.8 us). A warp walks it, the lanes together.
 struct Line {
+  static constexpr int kUnit = 10;
   const ChunkArgs& a;
-  int per, lane, tiles_most = 0;
+  int per, full_rows, lane, tiles_most = 0;   // full_rows: more need both row tiles
   long long total = 0;
   int b0 = -1;
   Chunk ch = {};       // lane's chunk of the 32 from b0 on
-  // a place: tile, sequence, head; the unit's steps, the step in it
-  struct Place {
-    int j, b, h, steps, off;
-    // A cut one step from a unit's end is not worth a record: it moves there.
-    __device__ int shift() const { return off == 1 ? -1 : (off > 0 && off == steps - 1 ? 1 : 0); }
+  // a unit's tile, sequence and head, steps, what each costs, and where on the line it begins
+  struct Unit {
+    int j, b, h, steps, each;
+    long long base;
+    __device__ long long behind() const { return base + static_cast<long long>(steps) * each + kUnit; }
+    // The step where a cut at x (within the unit) comes to be. Fewer than `least` steps from an end are not worth a record:
+    // the cut moves there.
+    __device__ int step_of(long long x, int least) const {
+      const long long s = (x - base) / each;
+      return s < min(least, steps) ? 0 : s > steps - least ? steps : static_cast<int>(s);
+    }
   } at = {};
+  int least = 1;
 
-  __device__ Line(const ChunkArgs& args, int per_, int lane_) : a(args), per(per_), lane(lane_) {
+  __device__ Line(const ChunkArgs& args, int per_, int full, int lane_) : a(args), per(per_), full_rows(full), lane(lane_) {
     for (int i = 0; i < a.batch; i += 32) {
       group(i);
-      for (int k = 0; k < ch.tiles; ++k) total += steps_of(a, ch, k, per);
+      for (int k = 0; k < ch.tiles; ++k) total += cost(k);
       tiles_most = max(tiles_most, __reduce_max_sync(0xffffffffu, ch.tiles));
     }
     total = warp_sum(total) * a.c.n_kv;
@@ -176,49 +209,56 @@ struct Line {
     b0 = first;
     ch = chunk_of(a, first + lane, per);
   }
-  // Step x of the units of tile index j_ of the 32 sequences: `s` their steps, a lane each.
-  __device__ Place locate(long long x, int j, int s) {
-    int inc = s;   // below 32 * 2^24
+  __device__ int each_of(int j) const { return (min(ch.n, a.max_q_len) - j * per) * a.group > full_rows ? 4 : 3; }
+  __device__ int cost(int j) const {
+    const int s = steps_of(a, ch, j, per);
+    return s ? s * each_of(j) + kUnit : 0;
+  }
+  // The unit of tile index j that place x of the 32 sequences' is in; they begin at `base`.
+  __device__ Unit locate(long long x, int j, long long base) {
+    const int c = cost(j);
+    int inc = c;   // below 32 * (4 * 2^24 + 10)
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    const int src = __ffs(__ballot_sync(0xffffffffu, x < static_cast<long long>(inc) * a.c.n_kv)) - 1;
-    const int steps = __shfl_sync(0xffffffffu, s, src);
-    x -= static_cast<long long>(__shfl_sync(0xffffffffu, inc, src) - steps) * a.c.n_kv;
-    const int h = static_cast<int>(x / steps);
-    return {j, b0 + src, h, steps, static_cast<int>(x - static_cast<long long>(h) * steps)};
+    const int src = __ffs(__ballot_sync(0xffffffffu, x - base < static_cast<long long>(inc) * a.c.n_kv)) - 1;
+    const int here = __shfl_sync(0xffffffffu, c, src);
+    base += static_cast<long long>(__shfl_sync(0xffffffffu, inc, src) - here) * a.c.n_kv;
+    const int h = static_cast<int>((x - base) / here);
+    return {j, b0 + src, h, __shfl_sync(0xffffffffu, steps_of(a, ch, j, per), src), __shfl_sync(0xffffffffu, each_of(j), src),
+            base + static_cast<long long>(h) * here};
   }
-  // Goes to step x0 of the line, where its cut moves; x1, the next cut, moves too (x0 < x1 <= total).
-  __device__ void go(long long& x0, long long& x1) {
-    long long before = 0, end = x1;
-    bool found = false, last = x1 >= total;
-    for (int j = 0; j < tiles_most && !(found && last); ++j) {
+  // Goes to the unit of place x0, whose step `step` the cut there comes to be; last, last_step: the unit where x1 is, and
+  // the step up to which to go there (x0 < x1 <= total).
+  __device__ void go(long long x0, long long x1, int& step, long long& last, int& last_step) {
+    long long before = 0;
+    bool found = false, ended = x1 >= total;
+    last = total;
+    last_step = 0;
+    for (int j = 0; j < tiles_most && !(found && ended); ++j) {
       for (int i = 0; i < a.batch; i += 32) {
         group(i);
-        const int s = steps_of(a, ch, j, per);
-        const long long behind = before + static_cast<long long>(__reduce_add_sync(0xffffffffu, s)) * a.c.n_kv;
+        const long long behind = before + static_cast<long long>(__reduce_add_sync(0xffffffffu, cost(j))) * a.c.n_kv;
         if (!found && x0 < behind) {
           found = true;
-          at = locate(x0 - before, j, s);
+          at = locate(x0, j, before);
         }
-        if (!last && x1 < behind) {
-          last = true;
-          end = x1 + locate(x1 - before, j, s).shift();
+        if (!ended && x1 < behind) {
+          ended = true;
+          const Unit u = locate(x1, j, before);
+          last = u.base;
+          last_step = u.step_of(x1, least);
         }
         before = behind;
       }
     }
-    x1 = end;
-    const int by = at.shift();
-    x0 += by;
+    step = at.step_of(x0, least);
     group(at.b & ~31);
-    if (by < 0) at.off = 0;
-    if (by > 0 && x0 < x1) next();
   }
-  __device__ void next() {   // the next unit, from its first step (there is one)
-    at.off = 0;
+  __device__ void next() {   // the next unit (the place behind the last one is the line's end)
+    at.base = at.behind();
     if (++at.h < a.c.n_kv) return;
     at.h = 0;
     ++at.b;
@@ -229,6 +269,7 @@ struct Line {
         if (more) {
           at.b = i + __ffs(more) - 1;
           at.steps = __shfl_sync(0xffffffffu, steps_of(a, ch, at.j, per), at.b & 31);
+          at.each = __shfl_sync(0xffffffffu, each_of(at.j), at.b & 31);
           return;
         }
       }
@@ -241,12 +282,10 @@ struct Line {
 template <typename T, typename TO, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs a) {
   constexpr bool kTwo = std::is_same<TO, float>::value;   // P in two parts
-  constexpr int kStages = 2 * CTAS, kLog = CTAS;          // of keys and of values, 64 KB each in all
-  constexpr uint32_t kStage = kTileOp / CTAS;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Work s_work[2];
-  __shared__ unsigned s_bad[2 * kStages];   // a step's groups of 16 positions whose block id is bad
+  __shared__ unsigned s_bad[kBad];   // a load's groups of 16 positions whose block id is bad
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t base = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 1023u) & ~1023u;
   const uint32_t bars = base + kOffBar;
@@ -257,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     for (int i = 0; i < kBars; ++i)
       mbar_init(bar(i), i == kWEmpty0 || i == kWEmpty1 ? 15
                         : (i >= kPFull0 && i < kPFull0 + 4) || i == kQFull ? 4 * CTAS
-                        : i == kQEmpty || (i >= kKEmpty0 && i < kVEmpty0 + 4) ? 2 : 1);
+                        : i == kQEmpty || i >= kEmpty0 ? 2 : i >= kFull0 && rank == 0 ? CTAS : 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 8) {
@@ -348,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         fence_after();
         const uint32_t t_s = tmem + lanes + kColS + t * 128 + (n & 1) * 64;
         const int at = w.tile0 * kCols + i * 64;
-        const unsigned bad = s_bad[(w.step0 + (i >> 1)) & (2 * kStages - 1)] >> 4 * (i & 1) & 15;
+        const unsigned bad = s_bad[(w.load0 + i / CTAS) % kBad] >> 4 * (i % CTAS) & 15;
         const bool masked = bad || at + 64 > vis_least;
         auto mask = [&](float (&s)[32], int c) {
           if (__builtin_expect(masked, 0)) {
@@ -385,18 +424,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
           x0 = add2(x0, x1);
           return x0.x + x0.y;
         };
-        float sum;
-        {
-          float x[32], y[32];
-          load32(t_s, x);
-          wait_ld(x);
-          load32(t_s + 32, y);
-          mask(x, 0);
-          sum = weigh(x, 0);
+        float x[32], y[32];
+        load32(t_s, x);
+        wait_ld(x);
+        load32(t_s + 32, y);
+        mask(x, 0);
+        if (i == 0) {   // a maximum to begin with
           wait_ld(y);
           mask(y, 1);
-          sum += weigh(y, 1);
+          float top = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) top = fmaxf(top, fmaxf(x[j], y[j]));
+          m = fmaxf(m, top * f);
         }
+        float sum = weigh(x, 0);
+        wait_ld(y);
+        mask(y, 1);
+        sum += weigh(y, 1);
         const bool over = !(sum <= kMost);   // NaN too
         if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
           float s[32], top = -INFINITY;
@@ -454,17 +498,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.rec_o)) & 31) == 0;
       const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + w.h * a.group + head;
       const long long rec = static_cast<long long>(w.slot) * a.part_rows + r;
+      // 32 bytes a store: whole sectors, though a row a thread
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {   // 32 bytes a store: whole sectors, though a row a thread
-        float o[32];
-        load32(t_o + 32 * c, o);
+      for (int c = 0; c < 2; ++c) {
+        float o[32], x[32];
+        load32(t_o + 64 * c, o);
         wait_ld(o);
+        load32(t_o + 64 * c + 32, x);
+        auto put = [&](float (&v)[32], int col) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
-        if (live) {
-          if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kKvD + 32 * c, o, wide);
-          else write32<float>(a.rec_o + rec * kKvD + 32 * c, o, wide);
-        }
+          for (int j = 0; j < 32; ++j) v[j] = l == 0.f ? 0.f : v[j] * inv;
+          if (live) {
+            if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kKvD + col, v, wide);
+            else write32<float>(a.rec_o + rec * kKvD + col, v, wide);
+          }
+        };
+        put(o, 64 * c);
+        wait_ld(x);
+        put(x, 64 * c + 32);
       }
       if (live && !whole) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
     }
@@ -478,90 +529,89 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     const int t = warp - 8;
     const uint64_t q_at = desc_q(base + t * kTileOp);
     const uint32_t o = tmem + kColO + t * 128;
-    unsigned step = 0, filled = 0;   // steps and loaded queries so far
+    Turn scored, weighed;            // the next load whose scores are issued, whose values are
+    unsigned filled = 0;             // loaded queries so far
     unsigned n = 0;                  // halves of the tile so far, as the softmax counts them
+    unsigned turns = 0;              // where both tiles are at work, their products go in turn: what one needs next is not held up by the other's
     int before = 0;
     bool ok = true;
-    auto keys_there = [&](unsigned i) {
-      const int st = i & (kStages - 1);
-      return warp_wait(kKFull0 + st, i >> kLog & 1) && (CTAS == 1 || warp_wait(kKPeer0 + st, i >> kLog & 1));
-    };
-    auto values_there = [&](unsigned i) {
-      const int st = i & (kStages - 1);
-      return warp_wait(kVFull0 + st, i >> kLog & 1) && (CTAS == 1 || warp_wait(kVPeer0 + st, i >> kLog & 1));
-    };
     for (unsigned part = 0; ok; ++part) {
       if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
-      const int seq = s_work[part & 1].seq, tiles = s_work[part & 1].tiles, halves = s_work[part & 1].halves;
-      const bool mine = s_work[part & 1].rows > t * CTAS * 128;   // else this warp only says that it is done with what is loaded
+      const int seq = s_work[part & 1].seq, halves = s_work[part & 1].tiles ? s_work[part & 1].halves : 0;
+      const int rows = s_work[part & 1].rows;
+      const bool mine = rows > t * CTAS * 128;   // else this warp only says that it is done with what is loaded
+      const bool both = rows > CTAS * 128;
+      before = s_work[part & 1].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
       if (seq < 0) break;
-      before = tiles;
-      if (tiles == 0) continue;
-      auto qk = [&](int i) {   // S of half i
-        const int st = (step + (i >> 1)) & (kStages - 1);
-        if (leader) {
-          if (mine) {
-            const uint64_t k_at = desc_k(base + kOffK + st * kStage + (i & 1) * (kStage / 2));
-            const uint32_t d = tmem + kColS + t * 128 + ((n + i) & 1) * 64;
+      if (halves == 0) continue;
+      // S of half i, of what is loaded in `stage` (by the leader)
+      auto qk = [&](int i, int stage) {
+        const uint64_t k_at = desc_k(base + kOffLoads + stage * kStage + (CTAS == 2 ? (i & 1) * 8192 : 0));
+        const uint32_t d = tmem + kColS + t * 128 + ((n + i) & 1) * 64;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint64_t qq = q_at + (((k >> 2) * kHalfQ + (k & 3) * 32) >> 4), kk = k_at + (((k >> 2) * 1024 + (k & 3) * 32) >> 4);
-              if constexpr (CTAS == 2) mma_ss2(d, qq, kk, idesc_qk<T, CTAS>(), k > 0);
-              else mma_ss(d, qq, kk, idesc_qk<T, CTAS>(), k > 0);
-            }
-            commit(kSFull0 + 2 * t + ((n + i) & 1));
-          }
-          if ((i & 1) || i + 1 == halves) commit(kKEmpty0 + st);
-          if (i + 1 == halves) commit(kQEmpty);
+        for (int k = 0; k < 8; ++k) {
+          const uint64_t qq = q_at + (((k >> 2) * kHalfQ + (k & 3) * 32) >> 4), kk = k_at + (((k >> 2) * 1024 + (k & 3) * 32) >> 4);
+          if constexpr (CTAS == 2) mma_ss2(d, qq, kk, idesc_qk<T, CTAS>(), k > 0);
+          else mma_ss(d, qq, kk, idesc_qk<T, CTAS>(), k > 0);
         }
-        __syncwarp();
       };
       auto pv = [&](uint32_t p, uint64_t v, bool acc) {
         if constexpr (CTAS == 2) mma_ts2(o, p, v, idesc_pv<T, CTAS>(), acc);
         else mma_ts(o, p, v, idesc_pv<T, CTAS>(), acc);
       };
-      if (!(ok = warp_wait(kQFull, filled++ & 1) && keys_there(step))) break;
-      fence_after();
-      qk(0);
-      if (halves > 1) qk(1);
-      for (int i = 0; i < halves; ++i) {
-        const int st = (step + (i >> 1)) & (kStages - 1);
-        const unsigned count = n + i;
-        if (!(i & 1) && !(ok = values_there(step + (i >> 1)))) break;
-        if (mine && !(ok = warp_wait(kPFull0 + 2 * t + (count & 1), count >> 1 & 1))) break;
+      auto your_turn = [&]() {
+        if (both && lane == 0) mbar_arrive(bar(kTurn0 + (t ^ 1)));
+      };
+      // Half i - 2's weights times values, half i's scores, when both are there.
+      if (!(ok = warp_wait(kQFull, filled++ & 1))) break;
+      for (int i = 0; i < halves + 2; ++i) {
+        const bool load = i < halves && i % CTAS == 0, weights = i >= 2;
+        const unsigned count = n + i - 2;
+        const uint32_t turn = (turns & 1) ^ (t ? 0 : 1);
+        // most often all is there; else one after the other
+        bool there = true;
+        if (load) there = mbar_test(bar(kFull0 + scored.stage), scored.round);
+        if (weights && mine) there = mbar_test(bar(kPFull0 + 2 * t + (count & 1)), count >> 1 & 1) && there;
+        if (both) there = mbar_test(bar(kTurn0 + t), turn) && there;
+        if (!__all_sync(0xffffffffu, there)) {
+          if (load && !(ok = warp_wait(kFull0 + scored.stage, scored.round))) break;
+          if (weights && mine && !(ok = warp_wait(kPFull0 + 2 * t + (count & 1), count >> 1 & 1))) break;
+          if (both && !(ok = warp_wait(kTurn0 + t, turn))) break;
+        }
+        ++turns;
         fence_after();
+        const bool frees = weights && ((i - 2) % CTAS == CTAS - 1 || i == halves + 1);   // the last half of a load
         if (leader) {
           if (mine) {
-            const uint64_t v_at = desc_v<CTAS>(base + kOffV + st * kStage + (i & 1) * (kStage / 2));
-            const uint32_t p = tmem + kColS + t * 128 + (count & 1) * 64;
+            if (weights) {
+              const uint64_t v_at = desc_v<CTAS>(base + kOffLoads + 16384 + weighed.stage * kStage + (CTAS == 2 ? (i & 1) * 8192 : 0));
+              const uint32_t p = tmem + kColS + t * 128 + (count & 1) * 64;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {   // 16 positions: 8 columns
-              const uint64_t vk = v_at + (4096 / CTAS >> 4) * k;
-              if constexpr (kTwo) {
-                const uint32_t pk = p + 32 * (k >> 1) + 8 * (k & 1);
-                pv(pk, vk, i > 0 || k > 0);
-                pv(pk + 16, vk, true);
-              } else {
-                pv(p + 8 * k, vk, i > 0 || k > 0);
+              for (int k = 0; k < 4; ++k) {   // 16 positions: 8 columns
+                const uint64_t vk = v_at + (4096 / CTAS >> 4) * k;
+                if constexpr (kTwo) {
+                  const uint32_t pk = p + 32 * (k >> 1) + 8 * (k & 1);
+                  pv(pk, vk, i > 2 || k > 0);
+                  pv(pk + 16, vk, true);
+                } else {
+                  pv(p + 8 * k, vk, i > 2 || k > 0);
+                }
               }
             }
-            if (i + 1 == halves) commit(kODone0 + t);
-            if (i + 2 == halves) commit(kSFull0 + 2 * t + (count & 1));   // in place of scores
+            if (i < halves) qk(i, scored.stage);
+            if (i <= halves && (i < halves || i >= 2)) commit(kSFull0 + 2 * t + ((n + i) & 1));   // of half `halves` there are none: the product before the last one's sign
+            if (i == halves + 1) commit(kODone0 + t);
           }
-          if ((i & 1) || i + 1 == halves) commit(kVEmpty0 + st);
+          if (frees) commit(kEmpty0 + weighed.stage);
+          if (i + 1 == halves) commit(kQEmpty);
         }
         __syncwarp();
-        if (i + 2 < halves) {
-          if (!(i & 1)) {
-            if (!(ok = keys_there(step + (i >> 1) + 1))) break;
-            fence_after();
-          }
-          qk(i + 2);
-        }
+        your_turn();
+        if (i < halves && (i % CTAS == CTAS - 1 || i + 1 == halves)) scored.next();
+        if (frees) weighed.next();
       }
-      step += tiles;
       if (mine) n += halves + (halves > 1);
     }
     if (!ok) {   // gave up: the products in flight come to rest before their memory goes
@@ -571,77 +621,81 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     __syncwarp();
   } else if (warp < 10 || warp == 11) {
     // ---- the second CTA of a pair tells the first what it has loaded (and the other warps here only pass)
-    unsigned step = 0;
+    Turn loaded;
     int before = 0;
     bool ok = true;
     for (unsigned part = 0; ok; ++part) {
       if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
-      const int seq = s_work[part & 1].seq, tiles = s_work[part & 1].tiles;
+      const int seq = s_work[part & 1].seq, loads = s_work[part & 1].loads;
+      before = s_work[part & 1].tiles;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
       if (seq < 0) break;
-      before = tiles;
-      for (int i = 0; i < tiles && warp == 11 && rank == 1; ++i, ++step) {
-        const int st = step & (kStages - 1);
-        if (!(ok = warp_wait(kKFull0 + st, step >> kLog & 1))) break;
-        if (lane == 0) arrive_first(kKPeer0 + st);
-        if (!(ok = warp_wait(kVFull0 + st, step >> kLog & 1))) break;
-        if (lane == 0) arrive_first(kVPeer0 + st);
+      for (int i = 0; i < loads && warp == 11 && rank == 1; ++i, loaded.next()) {
+        if (!(ok = warp_wait(kFull0 + loaded.stage, loaded.round))) break;
+        if (lane == 0) arrive_first(kFull0 + loaded.stage);
       }
     }
   } else if (warp == 10) {
     // ---- the work, keys and values
-    Line line(a, per, lane);
-    const long long cut = line.total / 2;   // two steps a team at least
+    Line line(a, per, CTAS * 128, lane);
+    const long long cut = line.total / 5;   // one step and more a team
     const long long ctas = cut < 1 ? 1 : (cut < teams ? cut : teams);
-    long long x = 0, end = 0;
-    if (team < ctas && line.total > 0) {
-      x = line.total * team / ctas;
-      end = line.total * (team + 1) / ctas;
-      line.go(x, end);
+    line.least = !a.may_split ? INT_MAX : line.total < 16ll * teams ? 1 : 2;
+    auto cut_of = [&](long long team_) { return line.total * team_ / ctas; };
+    int from = 0, last_step = 0;   // steps of the unit at hand that are done, or others'; and those up to which to go in the last unit
+    long long last = 0;            // where that begins
+    const bool works = team < ctas && line.total > 0;
+    if (works) {
+      line.go(cut_of(team), cut_of(team + 1), from, last, last_step);
+      if (from == line.at.steps) {   // the cut moved to the next unit
+        line.next();
+        from = 0;
+      }
     }
     const bool speaks = rank == 0 && lane == 0;
     if (a.may_split && speaks) a.split_units[team] = make_int4(0, 0, 0, 0);
-    const unsigned group16 = lane & 7;
-    unsigned step = 0;
+    constexpr int kGroups = 4 * CTAS;   // of 16 positions a load
+    const int group16 = lane & (kGroups - 1);
+    Turn load;
+    unsigned loads = 0;
     int before = 0, before2 = 0;   // steps of the parts that the slot's last reader may be at
     bool ok = true;
     for (unsigned part = 0;; ++part) {
       if (!(ok = long_wait(kWEmpty0 + (part & 1), (part >> 1 & 1) ^ 1, before + before2))) break;
       Work w = {};
       w.seq = -1;
-      if (x < end) {
-        const int src = line.at.b & 31;
+      const auto& u = line.at;
+      const int to = u.base < last ? u.steps : last_step;
+      if (works && u.base <= last && from < to) {
+        const int src = u.b & 31;
         Chunk ch;
         ch.q0 = __shfl_sync(0xffffffffu, line.ch.q0, src);
         ch.n = __shfl_sync(0xffffffffu, line.ch.n, src);
         ch.len = __shfl_sync(0xffffffffu, line.ch.len, src);
-        const int served = min(ch.n, a.max_q_len), first = line.at.j * per;
-        const long long left = end - x;
-        const int steps = left < line.at.steps - line.at.off ? static_cast<int>(left) : line.at.steps - line.at.off;
-        w.seq = line.at.b;
-        w.h = line.at.h;
+        const int served = min(ch.n, a.max_q_len), first = u.j * per;
+        w.seq = u.b;
+        w.h = u.h;
         w.q0 = ch.q0 + first;
         w.rows = min(per, served - first) * a.group;
         w.pos0 = ch.len - ch.n + first;
-        w.limit = limit_of(a, ch, line.at.j, per);
-        w.tile0 = line.at.off;
-        w.tiles = w.limit == 0 ? 0 : steps;
+        w.limit = limit_of(a, ch, u.j, per);
+        w.tile0 = from;
+        w.tiles = w.limit == 0 ? 0 : to - from;
         w.halves = min((w.limit + 63) / 64 - 2 * w.tile0, 2 * w.tiles);
-        w.slot = line.at.off > 0 ? 2 * team : (steps < line.at.steps ? 2 * team + 1 : -1);
+        w.loads = w.tiles ? (w.halves + CTAS - 1) / CTAS : 0;
+        w.slot = from > 0 ? 2 * team : (to < u.steps ? 2 * team + 1 : -1);
         w.zero0 = ch.q0 + served;
-        w.zeros = line.at.j == 0 && line.at.off == 0 ? ch.n - served : 0;   // queries past max_q_len
-        w.step0 = step;
-        if (line.at.j == 0 && line.at.off == 0 && line.at.h == 0 && speaks && (ch.n > a.max_q_len || ch.len > a.limit))
+        w.zeros = u.j == 0 && from == 0 ? ch.n - served : 0;   // queries past max_q_len
+        w.load0 = loads;
+        if (u.j == 0 && from == 0 && u.h == 0 && speaks && (ch.n > a.max_q_len || ch.len > a.limit))
           b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
-        if (line.at.off == 0 && steps < line.at.steps && speaks) {
-          // who has the unit's last step, unless the cut before that one moved behind it
-          const long long last = x + line.at.steps;
-          long long owner = (last * ctas - 1) / line.total;
-          if (last - line.total * owner / ctas < 2) --owner;
+        if (from == 0 && to < u.steps && speaks) {
+          // the last team whose cut is in the unit, and stays there
+          long long owner = (u.behind() * ctas - 1) / line.total;
+          while (owner > team && u.step_of(cut_of(owner), line.least) == u.steps) --owner;
           a.split_units[team] = make_int4(w.q0, w.rows, w.h * a.group, static_cast<int>(owner) - team + 1);
         }
-        x += steps;
       }
       if (lane == 0) s_work[part & 1] = w;
       __syncwarp();
@@ -649,41 +703,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       if (w.seq < 0) break;
       before2 = before;
       before = w.tiles;
-      // the block of this lane's group of 16 positions of step i (-1: behind the end)
+      // the block of this lane's group of 16 positions of load i (-1: behind the end)
       const int* table = a.block_table + static_cast<long long>(w.seq) * a.c.bt_stride;
       auto block_of = [&](int i) {
-        const int g16 = (w.tile0 + i) * 8 + group16;
-        return ldg_or(table + (g16 >> (a.c.log2_bs - 4)), i < w.tiles && g16 * 16 < w.limit, -1);
+        const int g16 = w.tile0 * 8 + i * kGroups + group16;
+        return ldg_or(table + (g16 >> (a.c.log2_bs - 4)), i < w.loads && g16 * 16 < w.limit, -1);
       };
       int blk = block_of(0);
-      for (int i = 0; i < w.tiles; ++i, ++step) {
-        const int st = step & (kStages - 1);
-        const uint32_t free_phase = (step >> kLog & 1) ^ 1;
+      for (int i = 0; i < w.loads; ++i, ++loads, load.next()) {
         const int blk_next = block_of(i + 1);
-        const int g16 = (w.tile0 + i) * 8 + group16;
+        const int g16 = w.tile0 * 8 + i * kGroups + group16;
         const bool inside = g16 * 16 < w.limit, good = inside && a.c.good(blk);
         const uint8_t* src = a.c.tile(good ? blk : 0, w.h, g16);
         const int rows = good ? min(w.limit - g16 * 16, kKvRows) : 0;   // of values: rows behind the end may hold anything
-        const unsigned all = __ballot_sync(0xffffffffu, good) & 0xffu, bad = __ballot_sync(0xffffffffu, inside && !good) & 0xffu;
-        const unsigned ragged = __ballot_sync(0xffffffffu, rows < kKvRows) & 0xffu;
+        constexpr unsigned kAll = (1u << kGroups) - 1;
+        const unsigned all = __ballot_sync(0xffffffffu, good) & kAll, bad = __ballot_sync(0xffffffffu, inside && !good) & kAll;
+        const unsigned ragged = __ballot_sync(0xffffffffu, rows < kKvRows) & kAll;
         if (bad && speaks) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
-        if (!(ok = warp_wait(kKEmpty0 + st, free_phase))) break;
         // keys: all, or this CTA's 32 positions of each half; values: all coordinates, or this CTA's 64
-        const unsigned keys = CTAS == 2 ? all & 0x33u << 2 * rank : all;
-        const uint32_t k_to = base + kOffK + st * kStage + (CTAS == 2 ? (group16 & 1) + (group16 >> 2) * 2 : group16) * kKvHalfBytes, v_to = base + kOffV + st * kStage;
-        if (lane == 0) {
-          s_bad[step & (2 * kStages - 1)] = bad;
-          mbar_expect(bar(kKFull0 + st), __popc(keys) * kKvHalfBytes);
-        }
-        __syncwarp();
-        if (lane < 8 && (keys >> lane & 1)) bulk_g2s_plain(k_to, src, kKvHalfBytes, bar(kKFull0 + st));
-        if (!(ok = warp_wait(kVEmpty0 + st, free_phase))) break;
         constexpr int kRowBytes = 256 / CTAS, kTileV = kKvHalfBytes / CTAS;   // of values, here
-        uint32_t bytes = __popc(all) * kTileV;
+        const unsigned keys = CTAS == 2 ? all & 0x33u << 2 * rank : all;
+        const uint32_t full = bar(kFull0 + load.stage), k_to = base + kOffLoads + load.stage * kStage, v_to = k_to + 16384;
+        if (!(ok = warp_wait(kEmpty0 + load.stage, load.round ^ 1))) break;
+        uint32_t bytes = __popc(keys) * kKvHalfBytes + __popc(all) * kTileV;
         if (__builtin_expect(ragged, 0)) {   // their rows that are not loaded are 0: no weight takes NaN along
-          bytes = 0;
+          bytes = __popc(keys) * kKvHalfBytes;
 #pragma unroll 1
-          for (int g = 0; g < 8; ++g) {
+          for (int g = 0; g < kGroups; ++g) {
             const int have = __shfl_sync(0xffffffffu, rows, g);
             bytes += have * kRowBytes;
             for (int k = lane; k < kTileV / 16 && have < kKvRows; k += 32)
@@ -693,35 +739,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
           fence_smem_async();
           __syncwarp();
         }
-        if (lane == 0) mbar_expect(bar(kVFull0 + st), bytes);
+        if (lane == 0) {
+          s_bad[loads % kBad] = bad;
+          mbar_expect(full, bytes);
+        }
         __syncwarp();
-        if (lane < 8 && rows > 0) {
+        if (lane < kGroups && rows > 0) {
+          if (keys >> lane & 1) bulk_g2s_plain(k_to + (CTAS == 2 ? (group16 & 1) + (group16 >> 2) * 2 : group16) * kKvHalfBytes, src, kKvHalfBytes, full);
           const uint32_t to = v_to + group16 * kTileV;
           const uint8_t* from = src + kKvHalfBytes + (CTAS == 2 ? rank * 1024 : 0);
           if (CTAS == 1 && rows == kKvRows) {
-            bulk_g2s_plain(to, from, kKvHalfBytes, bar(kVFull0 + st));
+            bulk_g2s_plain(to, from, kKvHalfBytes, full);
           } else if constexpr (CTAS == 1) {   // whole groups of 8 rows, then the rows of one group, half by half
             const int whole = rows >> 3 << 11, rest = (rows & 7) * 128;
-            if (whole) bulk_g2s_plain(to, from, whole, bar(kVFull0 + st));
+            if (whole) bulk_g2s_plain(to, from, whole, full);
             if (rest) {
-              bulk_g2s_plain(to + whole, from + whole, rest, bar(kVFull0 + st));
-              bulk_g2s_plain(to + whole + 1024, from + whole + 1024, rest, bar(kVFull0 + st));
+              bulk_g2s_plain(to + whole, from + whole, rest, full);
+              bulk_g2s_plain(to + whole + 1024, from + whole + 1024, rest, full);
             }
           } else {   // the two groups of 8 rows
-            bulk_g2s_plain(to, from, min(rows, 8) * 128, bar(kVFull0 + st));
-            if (rows > 8) bulk_g2s_plain(to + 1024, from + 2048, (rows - 8) * 128, bar(kVFull0 + st));
+            bulk_g2s_plain(to, from, min(rows, 8) * 128, full);
+            if (rows > 8) bulk_g2s_plain(to + 1024, from + 2048, (rows - 8) * 128, full);
           }
         }
         __syncwarp();
         blk = blk_next;
       }
       if (!ok) break;
-      if (x < end) line.next();
+      line.next();
+      from = 0;
     }
-    // the copies in flight end before their memory goes
-    for (unsigned k = step > kStages ? step - kStages : 0; k < step; ++k) {
-      warp_wait(kKFull0 + (k & (kStages - 1)), k >> kLog & 1);
-      warp_wait(kVFull0 + (k & (kStages - 1)), k >> kLog & 1);
+    // the copies in flight end before their memory goes (in the first CTA of a pair, the second one's too)
+    for (int k = 0; k < kStages; ++k) {   // the last load of each stage, the oldest first
+      if (loads + k >= kStages) warp_wait(kFull0 + load.stage, load.round ^ 1);
+      load.next();
     }
   } else {
     // ---- queries: half a warp a row, as they are
@@ -766,28 +817,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
   }
 }
 
-// Merges the parts of split units: a warp a row, 8 rows of a unit a CTA.
+// Merges the parts of split units, most often two: a warp 4 rows of two parts at once,
+// 32 rows a CTA; where there are more, a warp a row, eight parts at once, 8 rows a CTA.
 template <typename TO>
 __global__ void __launch_bounds__(256) kv16_chunk_merge_kernel(const ChunkArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int per_unit = (a.part_rows + 7) / 8;
-  const int u = blockIdx.x / per_unit, r = (blockIdx.x - u * per_unit) * 8 + warp;
+  const int u = blockIdx.x / per_unit, at = blockIdx.x - u * per_unit;
   grid_dep_wait();
   grid_dep_launch();
   const uint4 unit = ld_dep_u32x4(a.split_units + u);   // first row, rows, first head, parts
-  const int parts = unit.w;
-  if (r >= static_cast<int>(unit.y) || parts == 0) return;
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int z0 = 0; z0 < parts; z0 += 8) {   // eight parts' records on their way at once
+  const int rows = unit.y, parts = unit.w;
+  if (parts == 0 || (parts == 2 && (at & 3))) return;
+  const int row0 = 8 * at + (parts == 2 ? 4 * warp : warp);
+  if (row0 >= rows) return;
+  auto record = [&](int z, int r) { return static_cast<long long>(z == 0 ? 2 * u + 1 : 2 * (u + z)) * a.part_rows + r; };
+  auto put = [&](int r, float4 o) {
+    const long long orow = (static_cast<long long>(unit.x) + r / a.group) * a.n_q + unit.z + r % a.group;
+    write4<TO>(static_cast<TO*>(a.out) + orow * kKvD + 4 * lane, o);
+  };
+  if (parts == 2) {
     float lse[8];
     float4 x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int z = z0 + k;
-      const long long rec = static_cast<long long>(z == 0 ? 2 * u + 1 : 2 * (u + z)) * a.part_rows + r;
-      lse[k] = z < parts ? ld_dep_f32(a.rec_lse + rec) : -INFINITY;
-      x[k] = z < parts ? ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kKvD) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const bool in = row0 + (k >> 1) < rows;
+      const long long rec = record(k & 1, in ? row0 + (k >> 1) : row0);
+      lse[k] = ld_dep_f32(a.rec_lse + rec);
+      x[k] = ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kKvD) + lane);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) {
+      if (row0 + (k >> 1) >= rows) break;
+      // nothing seen: a log2-sum of -infinity, zeros in the record
+      const float top = fmaxf(lse[k], lse[k + 1]);
+      const float e = lse[k] == -INFINITY ? 0.f : exp2f(lse[k] - top), f = lse[k + 1] == -INFINITY ? 0.f : exp2f(lse[k + 1] - top);
+      const float s = e + f == 0.f ? 0.f : 1.f / (e + f);
+      put(row0 + (k >> 1), make_float4((x[k].x * e + x[k + 1].x * f) * s, (x[k].y * e + x[k + 1].y * f) * s,
+                                       (x[k].z * e + x[k + 1].z * f) * s, (x[k].w * e + x[k + 1].w * f) * s));
+    }
+    return;
+  }
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int z0 = 0; z0 < parts; z0 += 8) {
+    float lse[8];
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const long long rec = record(z0 + k, row0);
+      lse[k] = z0 + k < parts ? ld_dep_f32(a.rec_lse + rec) : -INFINITY;
+      x[k] = z0 + k < parts ? ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kKvD) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -803,8 +883,7 @@ __global__ void __launch_bounds__(256) kv16_chunk_merge_kernel(const ChunkArgs a
     }
   }
   const float s = l == 0.f ? 0.f : 1.f / l;
-  const long long orow = (static_cast<long long>(unit.x) + r / a.group) * a.n_q + unit.z + r % a.group;
-  write4<TO>(static_cast<TO*>(a.out) + orow * kKvD + 4 * lane, make_float4(o.x * s, o.y * s, o.z * s, o.w * s));
+  put(row0, make_float4(o.x * s, o.y * s, o.z * s, o.w * s));
 }
 
 // The grid, and the workspace that split units take.
@@ -826,7 +905,7 @@ Plan plan_for(const tq_config* cfg, int batch, int total_q, int max_q_len, int m
   long long tiles = static_cast<long long>(total_q) / per + (batch < total_q ? batch : total_q);
   if (tiles > most) tiles = most;
   p.units = tiles * cfg->num_kv_heads;
-  p.may_split = p.units > 0 && max_seq_len > 3 * kCols;   // a unit of three steps has no cut that stays where it is
+  p.may_split = p.units > 0 && max_seq_len > 3 * kCols;   // three steps are done before a second kernel is
   p.part_rows = longest < per ? longest * group : per * group;
   const size_t records = static_cast<size_t>(2 * kCtas / p.ctas) * p.part_rows;
   p.workspace = p.may_split ? (kCtas * sizeof(int4) + records * (kKvD + 1) * sizeof(float) + 15) / 16 * 16 : 16;
@@ -843,7 +922,7 @@ cudaError_t launch(const ChunkArgs& a, const Plan& p, cudaStream_t s) {
   const int most = (sms < kCtas ? sms : kCtas) / CTAS;
   // starts that go backwards may name more units than these: they are served all the same
   const long long steps = p.units * ((static_cast<long long>(a.limit) + kCols - 1) / kCols + 1);
-  const int teams = steps / 2 + 1 < most ? static_cast<int>(steps / 2 + 1) : most;
+  const int teams = steps < most ? static_cast<int>(steps) : most;
   if (CTAS == 2) err = launch_pdl_cluster(kv16_chunk_kernel<T, TO, CTAS>, dim3(2 * teams), dim3(kThreads), 2, kSmem, s, a);
   else err = launch_pdl(kv16_chunk_kernel<T, TO, CTAS>, dim3(teams), dim3(kThreads), kSmem, s, a);
   if (err != cudaSuccess || !p.may_split) return err;
