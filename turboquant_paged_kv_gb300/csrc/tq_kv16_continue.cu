@@ -47,9 +47,11 @@ constexpr int kCtas = 152;             // grid, one an SM: sizes the workspace w
 constexpr float kMost = 60000.f;       // sums of P up to this: every P fits in fp16
 constexpr uint32_t kTileOp = 32768;    // a 128 x 128 operand
 constexpr uint32_t kHalfQ = 16384;     // Q: two halves of 64 columns, 128 bytes a row
-constexpr int kStages = 5;             // of what is loaded at once: 16 KB of keys, then 16 KB of values
-constexpr uint32_t kStage = 32768, kOffLoads = 2 * kTileOp, kOffBar = kOffLoads + kStages * kStage;
+constexpr uint32_t kStage = 32768;     // what is loaded at once: 16 KB of keys, then 16 KB of values
+// behind Q and the stages: room for the output's rows, or one more stage where the loads bound
+constexpr uint32_t kOffLoads = 2 * kTileOp, kOffOut = kOffLoads + 4 * kStage, kOffBar = kOffOut + kStage;
 constexpr uint32_t kSmem = kOffBar + 512 + 1024;   // and room to align to 1024
+
 constexpr int kBad = 16;               // loads whose bad blocks are remembered (more than are between the loads and the softmax)
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: two halves' S of each tile, O of each tile
 constexpr int kPairRows = 256;                     // rows a chunk, on average, from which on pairs of CTAs are used
@@ -74,11 +76,12 @@ struct ChunkArgs {
 // barriers, 8 bytes each from kOffBar
 enum {
   kWFull0, kWFull1, kWEmpty0, kWEmpty1, kQFull, kQEmpty, kODone0, kODone1, kEnd0, kEnd1, kTurn0, kTurn1, kSFull0, kPFull0 = kSFull0 + 4,
-  kFull0 = kPFull0 + 4, kEmpty0 = kFull0 + kStages, kBars = kEmpty0 + kStages
+  kFull0 = kPFull0 + 4, kEmpty0 = kFull0 + 5, kBars = kEmpty0 + 5
 };
 static_assert(kBars * 8 <= 512, "barriers");
 
 // The stage of a load and its round through the stages.
+template <int kStages>
 struct Turn {
   int stage = 0;
   uint32_t round = 0;
@@ -282,6 +285,7 @@ struct Line {
 template <typename T, typename TO, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs a) {
   constexpr bool kTwo = std::is_same<TO, float>::value;   // P in two parts
+  constexpr int kStages = CTAS == 2 ? 4 : 5;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Work s_work[2];
@@ -495,27 +499,68 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       fence_after();
       const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
       const bool whole = w.slot < 0;
-      const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.rec_o)) & 31) == 0;
-      const long long orow = static_cast<long long>(w.q0 + qi) * a.n_q + w.h * a.group + head;
       const long long rec = static_cast<long long>(w.slot) * a.part_rows + r;
-      // 32 bytes a store: whole sectors, though a row a thread
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        float o[32], x[32];
-        load32(t_o + 64 * c, o);
+      auto row_of = [&](int q, int hd) { return (static_cast<long long>(w.q0 + q) * a.n_q + w.h * a.group + hd) * kKvD; };
+      auto read = [&](float (&o)[32], int col) {
+        load32(t_o + col, o);
         wait_ld(o);
-        load32(t_o + 64 * c + 32, x);
-        auto put = [&](float (&v)[32], int col) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = l == 0.f ? 0.f : v[j] * inv;
-          if (live) {
-            if (whole) write32<TO>(static_cast<TO*>(a.out) + orow * kKvD + col, v, wide);
-            else write32<float>(a.rec_o + rec * kKvD + col, v, wide);
+        for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
+      };
+      if constexpr (CTAS == 2) {
+        // by way of shared memory, 128 bytes a row: a store then covers whole lines of 4 rows (a row a thread, it took a
+        // line for every lane: 1.9 us a unit instead of 0.9)
+        const uint32_t room = base + kOffOut + warp * 4096;
+        auto pass = [&](auto* out, int col, auto&& at) {   // 128 bytes from column `col` on; at: where a row of the unit begins
+          using E = typename std::remove_pointer<decltype(out)>::type;
+          constexpr int kEach = 16 / sizeof(E);
+          float o[32];
+#pragma unroll
+          for (int c = 0; c < 4 / static_cast<int>(sizeof(E)); ++c) {
+            read(o, col + 32 * c);
+#pragma unroll
+            for (int k = 0; k < 2 * static_cast<int>(sizeof(E)); ++k) {
+              uint32_t v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(E) == 4) v[j] = __float_as_uint(o[4 * k + j]);
+                else v[j] = to_pair<E>(o[8 * k + 2 * j], o[8 * k + 2 * j + 1]);
+              }
+              const int unit = 2 * static_cast<int>(sizeof(E)) * c + k;
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(room + lane * 128 + ((unit ^ (lane & 7)) << 4)), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+            }
           }
+          __syncwarp();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int mine = 4 * k + (lane >> 3), unit = lane & 7, row = r - lane + mine;
+            const uint4 v = lds128(room + mine * 128 + ((unit ^ (mine & 7)) << 4));
+            if (row < w.rows) *reinterpret_cast<uint4*>(out + at(row) + col + kEach * unit) = v;
+          }
+          __syncwarp();
         };
-        put(o, 64 * c);
-        wait_ld(x);
-        put(x, 64 * c + 32);
+        if (whole) {
+#pragma unroll 1
+          for (int col = 0; col < kKvD; col += 128 / static_cast<int>(sizeof(TO)))
+            pass(static_cast<TO*>(a.out), col, [&](int row) {
+              const int q = static_cast<int>(row * by_group >> 16);
+              return row_of(q, row - q * a.group);
+            });
+        } else {
+#pragma unroll 1
+          for (int col = 0; col < kKvD; col += 32) pass(a.rec_o, col, [&](int row) { return (rec - r + row) * kKvD; });
+        }
+      } else {
+        const bool wide = ((whole ? reinterpret_cast<uintptr_t>(a.out) : reinterpret_cast<uintptr_t>(a.rec_o)) & 31) == 0;
+#pragma unroll 1
+        for (int col = 0; col < kKvD; col += 32) {   // 32 bytes a store: whole sectors, though a row a thread
+          float o[32];
+          read(o, col);
+          if (live) {
+            if (whole) write32<TO>(static_cast<TO*>(a.out) + row_of(qi, head) + col, o, wide);
+            else write32<float>(a.rec_o + rec * kKvD + col, o, wide);
+          }
+        }
       }
       if (live && !whole) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
     }
@@ -529,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     const int t = warp - 8;
     const uint64_t q_at = desc_q(base + t * kTileOp);
     const uint32_t o = tmem + kColO + t * 128;
-    Turn scored, weighed;            // the next load whose scores are issued, whose values are
+    Turn<kStages> scored, weighed;            // the next load whose scores are issued, whose values are
     unsigned filled = 0;             // loaded queries so far
     unsigned n = 0;                  // halves of the tile so far, as the softmax counts them
     unsigned turns = 0;              // where both tiles are at work, their products go in turn: what one needs next is not held up by the other's
@@ -621,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     __syncwarp();
   } else if (warp < 10 || warp == 11) {
     // ---- the second CTA of a pair tells the first what it has loaded (and the other warps here only pass)
-    Turn loaded;
+    Turn<kStages> loaded;
     int before = 0;
     bool ok = true;
     for (unsigned part = 0; ok; ++part) {
@@ -657,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     if (a.may_split && speaks) a.split_units[team] = make_int4(0, 0, 0, 0);
     constexpr int kGroups = 4 * CTAS;   // of 16 positions a load
     const int group16 = lane & (kGroups - 1);
-    Turn load;
+    Turn<kStages> load;
     unsigned loads = 0;
     int before = 0, before2 = 0;   // steps of the parts that the slot's last reader may be at
     bool ok = true;
