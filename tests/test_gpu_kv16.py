@@ -450,7 +450,7 @@ def test_decode_device_errors(tq):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_not_a_number_query_stays_in_its_row(tq, dtype):
+def test_not_a_number_query_stays_in_its_row(tq, mode, dtype):
     lens = [40, 40]
     c = Case(tq, dtype, 16, 4, 1, lens, seed=15).fill(lens)
     q = c.draw(2, 4)
@@ -545,18 +545,42 @@ def test_refusals_with_tensors_on_the_gpu(tq):
 # ---------------------------------------------------------------- chunks
 
 
+MODE = "rows"
+
+
+@pytest.fixture(params=["rows", "single", "pair"])
+def mode(request):
+    """Which of its kernels a chunk runs on goes by the sizes of the call: few queries are rows of their own; of more, a
+    CTA takes 256 rows, or a pair of CTAs 512 where chunks have more than 256 on average. The same chunks come to the
+    latter two with rows behind the last sequence, and sequences without queries."""
+    global MODE
+    MODE = request.param
+    yield MODE
+    MODE = "rows"
+
+
 def run_continue(c, q, starts, lens, out_dtype="f32", status=None, max_q=None, max_len=None, scale=0.0):
     cache, table, _ = c.gpu()
-    lens_d = torch.from_numpy(np.asarray(lens, dtype=np.int32)).cuda()
+    rows, batch, group = q.shape[0], len(lens), c.n_q // c.n_kv
+    starts, lens = np.asarray(starts, dtype=np.int32), np.asarray(lens, dtype=np.int32)
     msl = max(int(max(lens)), 1) if max_len is None else max_len
     mq = int(np.diff(starts).max(initial=0)) if max_q is None else max_q
+    if MODE != "rows":
+        more = max(305 - rows, 0 if MODE == "single" else 256 * batch // group + 1 - rows, 0)
+        empty = max(-(-(rows + more) * group // 256) - batch, 0) if MODE == "single" else 0
+        q = torch.cat([q.cpu(), torch.zeros((more, *q.shape[1:]), dtype=q.dtype)])
+        starts, lens = np.append(starts, [starts[-1]] * empty), np.append(lens, [0] * empty)
+        table = torch.cat([table, table[:1].repeat(empty, 1)])
+        assert (q.shape[0] * group > 256 * len(lens)) == (MODE == "pair") and q.shape[0] * c.n_kv > 304
+    dev = lambda x: torch.from_numpy(np.asarray(x, dtype=np.int32)).cuda()      # noqa: E731
     out = torch.full(q.shape, 123.0, dtype=DT[out_dtype], device="cuda")
     n = c.tq.tq_kv16_continue_workspace_size(c.cfg, len(lens), q.shape[0], mq, msl)
     ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
-    c.tq.tq_kv16_continue(c.cfg, q.cuda() if not q.is_cuda else q, torch.from_numpy(np.asarray(starts, dtype=np.int32)).cuda(), mq, cache, table,
-                          lens_d, msl, out, ws, scale=scale, dev_status=status)
+    c.tq.tq_kv16_continue(c.cfg, q.cuda() if not q.is_cuda else q, dev(starts), mq, cache, table, dev(lens), msl, out, ws, scale=scale,
+                          dev_status=status)
     torch.cuda.synchronize()
-    return out.float().cpu().numpy().astype(np.float64)
+    assert torch.all(out[rows:] == 123.0)
+    return out[:rows].float().cpu().numpy().astype(np.float64)
 
 
 def check_continue(c, q, got, starts, lens, out_dtype, rows=None, scale=SCALE):
@@ -576,7 +600,7 @@ def check_continue(c, q, got, starts, lens, out_dtype, rows=None, scale=SCALE):
 @pytest.mark.parametrize("block,n_kv,group,dtype,out", [
     (16, 2, 4, "bf16", "bf16"), (32, 1, 8, "fp16", "fp16"), (64, 2, 1, "bf16", "f32"), (128, 1, 3, "fp16", "f32"),
     (16, 1, 5, "bf16", "fp16"), (64, 1, 6, "fp16", "bf16"), (32, 1, 7, "bf16", "f32"), (128, 2, 2, "bf16", "f32")])
-def test_continue(tq, block, n_kv, group, dtype, out):
+def test_continue(tq, mode, block, n_kv, group, dtype, out):
     q_lens, hist = [1, 7, 0, 33, 130, 2], [0, 19, 50, 100, 5, 255]
     lens = [a + b for a, b in zip(q_lens, hist)]
     c = Case(tq, dtype, block, n_kv * group, n_kv, lens, seed=group + 30).fill(lens)
@@ -590,7 +614,7 @@ def test_continue(tq, block, n_kv, group, dtype, out):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("q_len,hist,group,n_kv", [(300, 0, 4, 1), (257, 700, 1, 2), (128, 1024, 8, 1), (40, 1500, 4, 1), (1, 3000, 3, 1)])
-def test_continue_long(tq, dtype, q_len, hist, group, n_kv):
+def test_continue_long(tq, mode, dtype, q_len, hist, group, n_kv):
     c = Case(tq, dtype, 64, n_kv * group, n_kv, [q_len + hist], seed=q_len).fill([q_len + hist])
     q = c.draw(q_len, n_kv * group)
     got = run_continue(c, q, [0, q_len], [q_len + hist])
@@ -598,7 +622,7 @@ def test_continue_long(tq, dtype, q_len, hist, group, n_kv):
 
 
 @pytest.mark.parametrize("dtype,batch", [("bf16", 90), ("fp16", 77), ("bf16", 500)])
-def test_continue_many_chunks(tq, dtype, batch):
+def test_continue_many_chunks(tq, mode, dtype, batch):
     """More (chunk, head) units than SMs, lengths from one position on, empty chunks
     between; all sequences share their blocks."""
     c = Case(tq, dtype, 32, 8, 2, [700], seed=batch).fill([700])
@@ -617,7 +641,7 @@ def test_continue_many_chunks(tq, dtype, batch):
 
 
 @pytest.mark.parametrize("n_kv", [1, 2])
-def test_continue_lengths_far_apart(tq, n_kv):
+def test_continue_lengths_far_apart(tq, mode, n_kv):
     """One long history among short ones, chunks of one query and of many."""
     hist, q_lens = [9000, 3, 0, 700, 0, 17], [5, 200, 1, 64, 0, 1]
     lens = [a + b for a, b in zip(hist, q_lens)]
@@ -629,7 +653,7 @@ def test_continue_lengths_far_apart(tq, n_kv):
 
 
 @pytest.mark.parametrize("q_len", [5, 150])
-def test_continue_rows_without_positions_and_padding(tq, q_len):
+def test_continue_rows_without_positions_and_padding(tq, mode, q_len):
     """Queries before position 0, past max_q_len and behind the last sequence."""
     c = Case(tq, "fp16", 16, 4, 1, [q_len, 200], seed=40).fill([q_len - 3, 200])
     starts = np.array([0, q_len, q_len + 4], dtype=np.int32)
@@ -645,7 +669,7 @@ def test_continue_rows_without_positions_and_padding(tq, q_len):
     assert not got[q_len - 1].any() and got[q_len - 2].any() and np.all(got[starts[-1]:] == 123.0)
 
 
-def test_continue_starts_that_go_backwards(tq):
+def test_continue_starts_that_go_backwards(tq, mode):
     """Not allowed, but nothing outside the rows is touched."""
     batch, n, rows = 401, 600, 32
     c = Case(tq, "bf16", 32, 32, 4, [n], seed=47).fill([n])
@@ -657,7 +681,7 @@ def test_continue_starts_that_go_backwards(tq):
 
 
 @pytest.mark.parametrize("q_len,length,cut", [(140, 200, 150), (5, 900, 897), (20, 900, 500)])
-def test_continue_cuts_long_sequences(tq, q_len, length, cut):
+def test_continue_cuts_long_sequences(tq, mode, q_len, length, cut):
     """Queries keep their places; none sees a position from max_seq_len on."""
     c = Case(tq, "bf16", 32, 4, 1, [length], seed=49).fill([length])
     q = c.draw(q_len, 4)
@@ -671,7 +695,7 @@ def test_continue_cuts_long_sequences(tq, q_len, length, cut):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-def test_one_position_is_its_value(tq, dtype):
+def test_one_position_is_its_value(tq, mode, dtype):
     """The weight of a sequence's only position is 1 within ex2's 2^-22, a rounding of a score
     below 64 in the exponent (2^-18) and a rounding of P = 8 p, a number near 8, to the parts
     of the type (2^-16): within 2^-15."""
@@ -706,7 +730,7 @@ def test_output_on_16_bytes(tq, hist, dtype, out):
 
 
 @pytest.mark.parametrize("q_len", [4, 140])
-def test_continue_device_errors(tq, q_len):
+def test_continue_device_errors(tq, mode, q_len):
     c = Case(tq, "bf16", 16, 4, 1, [200], seed=41).fill([200])
     c.table[0, 3], c.table[0, 9] = -1, 2 ** 31 - 1
     q = c.draw(q_len, 4)
@@ -721,7 +745,7 @@ def test_continue_device_errors(tq, q_len):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("q_len,hist", [(37, 30), (150, 0), (6, 900)])
 @pytest.mark.parametrize("gain_k,gain_q,scale", [(0.0, 0.0, 0.0), (1e-7, 0.0, 0.0), (0.0, 1e-7, 0.0), (1e-7, 1e-7, 1e-20)])
-def test_scores_that_vanish(tq, dtype, q_len, hist, gain_k, gain_q, scale):
+def test_scores_that_vanish(tq, mode, dtype, q_len, hist, gain_k, gain_q, scale):
     """Scores of nothing or next to it: plain means of the values seen."""
     n = q_len + hist
     c = Case(tq, dtype, 16, 4, 1, [n], seed=46)
@@ -736,7 +760,7 @@ def test_scores_that_vanish(tq, dtype, q_len, hist, gain_k, gain_q, scale):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("gap", [3, 12, 20, 60, 120, 200])
 @pytest.mark.parametrize("step", [1, 16, 100, 130])
-def test_continue_scores_that_rise_and_fall(tq, dtype, gap, step):
+def test_continue_scores_that_rise_and_fall(tq, mode, dtype, gap, step):
     """Every `step` positions scores rise by `gap` (log2 units), and fall with the other heads' queries; values as
     large as fp16 has them in the end."""
     n = 8 * step + 5
@@ -754,7 +778,7 @@ def test_continue_scores_that_rise_and_fall(tq, dtype, gap, step):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("hist", [0, 800])
-def test_continue_later_positions_change_nothing(tq, dtype, hist):
+def test_continue_later_positions_change_nothing(tq, mode, dtype, hist):
     """Bit for bit, whatever the keys and values that a query does not see."""
     q_len = 60
     n, out = hist + q_len, []
@@ -774,7 +798,7 @@ def test_continue_later_positions_change_nothing(tq, dtype, hist):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("block", [16, 64])
 @pytest.mark.parametrize("hist,q_len,max_q", [(10, 20, 5), (0, 140, 70), (900, 30, 7)])
-def test_rows_that_were_not_stored(tq, dtype, block, hist, q_len, max_q):
+def test_rows_that_were_not_stored(tq, mode, dtype, block, hist, q_len, max_q):
     """What stands in the cache behind the last served query (infinities and NaN) does not count."""
     n, kept = hist + q_len, hist + max_q
     c = Case(tq, dtype, block, 4, 1, [n], seed=94)

@@ -19,7 +19,7 @@ from ._abi import (PRESET_IDS, ROPE_STYLES, TQ_DEV_BLOCK_OUT_OF_RANGE, TQ_DEV_SE
                    TQ_DECODE_NOALLOC_SCRATCH_BYTES, TQ_DEV_SLOT_OUT_OF_RANGE, TQ_DEV_TIMEOUT, TQ_DEV_NOT_FINITE,
                    TQ_DTYPE_BF16, TQ_DTYPE_F16, TQ_DTYPE_F32, TQ_ERR_WORKSPACE_TOO_SMALL,
                    TQError, tq_b8_layout, tq_codebook, tq_config, tq_kv16_layout, tq_layout, tq_prod_layout,
-                   TQ_PRESET_KV_BF16, TQ_ROPE_HALVES, TQ_ROPE_PAIRS)
+                   TQ_PRESET_KV_BF16, TQ_PRESET_KV_F16, TQ_ROPE_HALVES, TQ_ROPE_PAIRS)
 
 
 
@@ -445,11 +445,46 @@ def _kv16_block_bytes(preset: int, head_dim: int, block_size: int, num_kv_heads:
     return tq_kv16_layout_for(make_config(preset, num_kv_heads, num_kv_heads, head_dim, block_size)).block_bytes
 
 
-def _kv16_rows(name: str, t: torch.Tensor, cfg: tq_config, heads: int) -> int:
-    """As _b8_rows, of the cache's own type."""
-    if t.dtype != (torch.bfloat16 if cfg.preset == TQ_PRESET_KV_BF16 else torch.float16):
+_KV16_TYPES = {TQ_PRESET_KV_BF16: torch.bfloat16, TQ_PRESET_KV_F16: torch.float16}
+
+
+def _kv16_rows(name: str, t: torch.Tensor, kind: torch.dtype, heads: int, d: int) -> int:
+    """As _b8_rows, of the cache's own type (which it looks at first: the usual call is over at once)."""
+    if t.dtype is kind and t.dim() == 3:
+        _, have, last = t.shape
+        s0, s1, s2 = t.stride()
+        if have == heads and last == d and s2 == 1 and s1 == d and s0 >= heads * d and s0 % 8 == 0:
+            return s0
+    if t.dtype is not kind:
         raise ValueError(f"{name} must have the cache's type, got {t.dtype}")
-    return _b8_rows(name, t, heads, cfg.head_dim)
+    return _b8_rows(name, t, heads, d)
+
+
+def _kv16_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 others: tuple, stream) -> tuple:
+    """As _b8_common for the 16-bit cache: what a usual call has is checked at once, anything else goes there."""
+    if (cache.dtype is torch.uint8 and block_table.dtype is torch.int32 and seq_lens.dtype is torch.int32 and num_blocks is None
+            and stream is None and cache.is_contiguous() and block_table.is_contiguous() and block_table.dim() == 2
+            and seq_lens.is_contiguous() and seq_lens.dim() == 1):
+        rows, width = block_table.shape
+        dev = cache.get_device()
+        if (rows >= seq_lens.shape[0] and dev >= 0 and block_table.get_device() == dev and seq_lens.get_device() == dev
+                and all([t is None or t.get_device() == dev for t in others]) and dev == torch.cuda.current_device()):
+            return (cache.numel() // _kv16_block_bytes(cfg.preset, cfg.head_dim, cfg.block_size, cfg.num_kv_heads), width,
+                    torch._C._cuda_getCurrentRawStream(dev))
+    return _b8_common(cfg, cache, num_blocks, block_table, seq_lens, others, stream, _kv16_block_bytes)
+
+
+@functools.lru_cache(maxsize=None)
+def _kv16_fn(name: str):
+    return getattr(_LIB, name)
+
+
+def _kv16_type(cfg: tq_config) -> torch.dtype:
+    kind = _KV16_TYPES.get(cfg.preset)
+    if kind is None:
+        raise ValueError("the config must be of kv_bf16 or kv_fp16")
+    return kind
 
 
 def tq_kv16_append(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query_start: torch.Tensor, cache: torch.Tensor,
@@ -463,8 +498,9 @@ def tq_kv16_append(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query
     cosines, then as many sines) pairs a head's first rot_dim coordinates as
     `style` says, "halves" or "pairs"; None: no rotation. q [total_q, n_q, d] is
     rotated into q_out (which may be q). Rows may be a stride apart."""
-    ks = _kv16_rows("key", key, cfg, cfg.num_kv_heads)
-    vs = _kv16_rows("value", value, cfg, cfg.num_kv_heads)
+    kind, heads, d = _kv16_type(cfg), cfg.num_kv_heads, cfg.head_dim
+    ks = _kv16_rows("key", key, kind, heads, d)
+    vs = _kv16_rows("value", value, kind, heads, d)
     rows = key.shape[0]
     if value.shape[0] != rows:
         raise ValueError("key and value must have one number of rows")
@@ -473,8 +509,8 @@ def tq_kv16_append(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query
     if q is not None or q_out is not None:
         if q is None or q_out is None:
             raise ValueError("q and q_out must be given together")
-        qs = _kv16_rows("q", q, cfg, cfg.num_q_heads)
-        os_ = _kv16_rows("q_out", q_out, cfg, cfg.num_q_heads)
+        qs = _kv16_rows("q", q, kind, cfg.num_q_heads, d)
+        os_ = _kv16_rows("q_out", q_out, kind, cfg.num_q_heads, d)
         if q.shape[0] != rows or q_out.shape[0] != rows:
             raise ValueError("q, q_out and key must have one number of rows")
         q_at, out_at = q.data_ptr(), q_out.data_ptr()
@@ -489,9 +525,9 @@ def tq_kv16_append(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query
     if how is None:
         raise ValueError(f"style must be one of {sorted(ROPE_STYLES)}, got {style!r}")
     _b8_starts(query_start, seq_lens)
-    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens,
-                                (key, value, query_start, q, q_out, cos_sin, dev_status), stream, _kv16_block_bytes)
-    st = _LIB.tq_kv16_append(cfg, key.data_ptr(), ks, value.data_ptr(), vs, q_at, qs, out_at, os_, angles, rot, positions, how,
+    nb, width, raw = _kv16_common(cfg, cache, num_blocks, block_table, seq_lens,
+                                  (key, value, query_start, q, q_out, cos_sin, dev_status), stream)
+    st = _kv16_fn("tq_kv16_append")(cfg, key.data_ptr(), ks, value.data_ptr(), vs, q_at, qs, out_at, os_, angles, rot, positions, how,
                              query_start.data_ptr(), seq_lens.shape[0], rows, cache.data_ptr(), nb, block_table.data_ptr(), width,
                              seq_lens.data_ptr(), _b8_status(dev_status), raw)
     if st:
@@ -507,12 +543,12 @@ def tq_kv16_decode(cfg: tq_config, q: torch.Tensor, cache: torch.Tensor, block_t
                    scale: float = 0.0, num_blocks: int | None = None, dev_status: torch.Tensor | None = None,
                    stream=None) -> None:
     """q [B, n_q, d] of the cache's type (rows may be a stride apart); out [B, n_q, d]; seq_lens [B] int32."""
-    qs = _kv16_rows("q", q, cfg, cfg.num_q_heads)
+    qs = _kv16_rows("q", q, _kv16_type(cfg), cfg.num_q_heads, cfg.head_dim)
     out_type = _b8_out("out", out, q.shape)
     if q.shape[0] != seq_lens.shape[0]:
         raise ValueError("q must have one row per sequence")
-    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (q, out, workspace, dev_status), stream, _kv16_block_bytes)
-    st = _LIB.tq_kv16_decode(cfg, q.data_ptr(), qs, cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(),
+    nb, width, raw = _kv16_common(cfg, cache, num_blocks, block_table, seq_lens, (q, out, workspace, dev_status), stream)
+    st = _kv16_fn("tq_kv16_decode")(cfg, q.data_ptr(), qs, cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(),
                              q.shape[0], max_seq_len, scale, out.data_ptr(), out_type, workspace.data_ptr(),
                              _b8_workspace(workspace), _b8_status(dev_status), raw)
     if st:
@@ -531,12 +567,11 @@ def tq_kv16_continue(cfg: tq_config, q: torch.Tensor, query_start: torch.Tensor,
     n_q, d] of the cache's type (rows may be a stride apart), query_start int32
     [batch + 1], seq_lens int32 [batch] (lengths with the chunk), out [total_q,
     n_q, d]; rows of out from query_start[batch] on are left as they are."""
-    qs = _kv16_rows("q", q, cfg, cfg.num_q_heads)
+    qs = _kv16_rows("q", q, _kv16_type(cfg), cfg.num_q_heads, cfg.head_dim)
     out_type = _b8_out("out", out, q.shape)
     _b8_starts(query_start, seq_lens)
-    nb, width, raw = _b8_common(cfg, cache, num_blocks, block_table, seq_lens, (q, query_start, out, workspace, dev_status), stream,
-                                _kv16_block_bytes)
-    st = _LIB.tq_kv16_continue(cfg, q.data_ptr(), qs, query_start.data_ptr(), seq_lens.shape[0], q.shape[0], max_q_len,
+    nb, width, raw = _kv16_common(cfg, cache, num_blocks, block_table, seq_lens, (q, query_start, out, workspace, dev_status), stream)
+    st = _kv16_fn("tq_kv16_continue")(cfg, q.data_ptr(), qs, query_start.data_ptr(), seq_lens.shape[0], q.shape[0], max_q_len,
                                cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(), max_seq_len, scale,
                                out.data_ptr(), out_type, workspace.data_ptr(), _b8_workspace(workspace), _b8_status(dev_status), raw)
     if st:

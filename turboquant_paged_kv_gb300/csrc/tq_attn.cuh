@@ -179,6 +179,19 @@ __device__ __forceinline__ void split_half2(float x0, float x1, uint32_t& hi, ui
   lo = pack_half2(x0 - hf.x, x1 - hf.y);
 }
 
+// Four numbers rounded to TO.
+template <typename TO>
+__device__ __forceinline__ void write4(TO* dst, float4 v) {
+  if constexpr (std::is_same<TO, float>::value) {
+    *reinterpret_cast<float4*>(dst) = v;
+  } else if constexpr (std::is_same<TO, __half>::value) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
+  } else {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void u2_to_f4(uint2 raw, float out[4]) {
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {

@@ -67,6 +67,29 @@ inline Kv16Cache kv16_cache(const tq_config* cfg, const tq_kv16_layout& L, const
 }
 
 }  // namespace
+
+// Rows of queries, each over positions of its own (tq_kv16_decode.cu).
+struct Kv16RowsArgs {
+  Kv16Cache c;
+  const void* q;
+  long long q_stride;
+  const int *block_table, *seq_lens;
+  const int* query_start;   // rows of chunks; null: a row a sequence
+  unsigned int* status;
+  void* out;
+  float *rec_o, *rec_lse;   // [records][group][d], [records][group] (log2 units)
+  int rows, n_kv, n_q, group, max_seq_len, cap;
+  int batch, max_q_len;     // with query_start
+  int warps;                // of the whole split grid
+  int early_indices;
+  float qscale;             // softmax scale * log2(e)
+};
+// Whether so many rows over so many positions are served by one launch of clusters, a
+// cluster a (row, KV head), rather than by what costs `most` (rounds of clusters x tiles a
+// warp and 3); if so, `ctas` is their size.
+bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int* ctas);
+cudaError_t kv16_short_launch(const Kv16RowsArgs& a, bool is_bf16, int out_dtype, int ctas, int dev, cudaStream_t s);
+
 }  // namespace tq
 
 #endif  // TQ_KV16_CUH_

@@ -55,6 +55,10 @@ constexpr uint32_t kSmem = kOffBar + 512 + 1024;   // and room to align to 1024
 constexpr int kBad = 16;               // loads whose bad blocks are remembered (more than are between the loads and the softmax)
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: two halves' S of each tile, O of each tile
 constexpr int kPairRows = 256;                     // rows a chunk, on average, from which on pairs of CTAs are used
+// Up to which cost (tq_kv16.cuh) queries are rows of their own: 1 x 64 over 2000 of 2 heads (16 tiles a warp) 12.4 us for
+// 19.3, 3 x 7 over 400 of 8 (4, two rounds) 10.1 for 12.9, 4 x 5 over 1000 (8, two rounds) 14.9 for 15.0, 1 x 16 over 4000
+// (31) 20.9 for 17.9, 8 x 5 over 500 (4, three rounds) 16.3 for 15.1
+constexpr int kShortMost = 22;
 constexpr unsigned long long kStepNs = 100000;     // what a step may take, where a wait is for many
 
 struct ChunkArgs {
@@ -1017,6 +1021,31 @@ tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stri
   if (workspace_bytes < p.workspace) return TQ_ERR_WORKSPACE_TOO_SMALL;
   if (static_cast<long long>(total_q) * cfg->num_q_heads > INT_MAX) return TQ_ERR_UNSUPPORTED;
   const int cap = b8_cap(cfg, bt_stride);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  // A few queries: each a row of its own over the cache, in one launch (one that this kernel's start and merge outlast).
+  int dev = 0, sms = 0, each = 0;
+  if (b8_current_device(&dev, &sms) != cudaSuccess) return TQ_ERR_CUDA;
+  if (kv16_short(total_q, cfg->num_kv_heads, max_seq_len < cap ? max_seq_len : cap, sms < kCtas ? sms : kCtas, kShortMost, &each)) {
+    Kv16RowsArgs r = {};
+    r.c = kv16_cache(cfg, L, cache, num_blocks, bt_stride);
+    r.q = q;
+    r.q_stride = q_stride;
+    r.block_table = block_table;
+    r.seq_lens = seq_lens;
+    r.query_start = query_start;
+    r.status = dev_status;
+    r.out = out;
+    r.rows = total_q;
+    r.n_kv = cfg->num_kv_heads;
+    r.n_q = cfg->num_q_heads;
+    r.group = cfg->num_q_heads / cfg->num_kv_heads;
+    r.max_seq_len = max_seq_len;
+    r.cap = cap;
+    r.batch = batch;
+    r.max_q_len = max_q_len;
+    r.qscale = b8_qscale(scale);
+    return kv16_short_launch(r, L.is_bf16, out_dtype, each, dev, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  }
   ChunkArgs a = {};
   a.c = kv16_cache(cfg, L, cache, num_blocks, bt_stride);
   a.q = q;
@@ -1038,7 +1067,6 @@ tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stri
   a.split_units = static_cast<int4*>(workspace);
   a.rec_o = reinterpret_cast<float*>(a.split_units + kCtas);
   a.rec_lse = a.rec_o + static_cast<size_t>(2 * kCtas / p.ctas) * p.part_rows * kKvD;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const cudaError_t err = L.is_bf16 ? launch<__nv_bfloat16>(a, p, out_dtype, s) : launch<__half>(a, p, out_dtype, s);
   return err == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

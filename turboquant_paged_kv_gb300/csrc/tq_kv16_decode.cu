@@ -24,28 +24,22 @@
 #include "tq_attn.cuh"
 #include "tq_kv16.cuh"
 #include "tq_line.cuh"
+#include "tq_tc.cuh"
 
 namespace tq {
 namespace {
-
-struct Kv16SplitArgs {
-  Kv16Cache c;
-  const void* q;
-  long long q_stride;
-  const int *block_table, *seq_lens;
-  unsigned int* status;
-  void* out;
-  float *rec_o, *rec_lse;   // [records][group][d], [records][group] (log2 units)
-  int rows, n_kv, n_q, group, max_seq_len, cap, warps;   // rows: sequences; warps: of the whole split grid
-  int early_indices;
-  float qscale;             // softmax scale * log2(e)
-};
 
 constexpr int kWarps = 9;          // a CTA
 constexpr int kStages = 3;         // tiles in a warp's ring
 constexpr int kMaxCtas = 256;      // grid cap: sizes the workspace without a device query
 constexpr int kMaxWarps = 4096;    // partial records beside one per pair
 constexpr int kSmem = kWarps * kStages * (kKvTileBytes + 8) + 128;   // and room to align to 128
+constexpr int kShortWarps = 8;     // a CTA of kv16_short_kernel
+constexpr int kShortSmem = kShortWarps * kStages * (kKvTileBytes + 8) + 128;
+// Up to which rounds x (tiles a warp + 3) the short kernel is used in place of the split and the merge, 2 rounds at most:
+// 16 x 1024 of 8 heads (8 tiles) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9, 32 x 1200 (10, two rounds) 29.1 for
+// 31.6, 20 x 1000 (8, two rounds) 20.4 for 20.1, 64 x 100 (1, four rounds) 15.7 for 14.9
+constexpr int kShortMost = 35;
 constexpr float kStep = 8.f;       // the running maximum moves in steps of at least this, log2 units
 static_assert(kMaxCtas * kWarps <= kMaxWarps, "workspace");
 
@@ -73,8 +67,141 @@ __device__ __forceinline__ void ldmatrix_trans(uint32_t at, uint32_t r[4]) {
                : "memory");
 }
 
+__device__ __forceinline__ float ld_cluster(uint32_t at, uint32_t rank) {   // what CTA `rank` of the cluster has at this address
+  float v;
+  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %1, %2;\n ld.shared::cluster.f32 %0, [a];\n}\n" : "=f"(v) : "r"(at), "r"(rank) : "memory");
+  return v;
+}
+
+// What a warp holds of a (sequence, KV head) pair: the query heads, their output so
+// far and the softmax's running maximum and sum.
 template <typename T, bool WIDE, int PARTS>
-__global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16SplitArgs a) {
+struct Heads {
+  uint32_t qf[16];   // the B operand: coordinates 16 s + 2 t (+ 8) of head g (or g & 3)
+  float acc[8][4];   // O^T: coordinates 16 j + g, + 8 (rows) x heads 2 t, 2 t + 1; 8 times the sum of p v
+  float m0, m1, l0, l1;
+
+  __device__ __forceinline__ void begin(const T* q, int group, int lane) {
+    const int g = lane >> 2, t = lane & 3, head = WIDE ? g : g & 3;
+    const T* src = q + head * kKvD + 2 * t;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) qf[i] = static_cast<uint32_t>(ldg_or(reinterpret_cast<const int*>(src + 8 * i), head < group, 0));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
+    m0 = m1 = -1e30f;
+    l0 = l1 = 0.f;
+  }
+
+  // The tile at kt in shared memory, of which the first `left` positions count.
+  __device__ __forceinline__ void tile(uint32_t kt, int left, float qscale, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    // where this lane's rows of the operands are: K, rows lane & 15 and the k-step's group
+    // lane / 16; V, rows (lane & 7) + 8 (lane / 16) and the coordinates' group lane / 8 & 1.
+    // Step j's groups (2 j, 2 j + 1) lie at ^ 32 j, the second four steps' 1024 behind.
+    const uint32_t r8 = lane & 7;
+    const uint32_t k_at = ((lane >> 3 & 1) << 11) + (r8 << 7) + (((lane >> 4) ^ r8) << 4);
+    const uint32_t v_at = kKvHalfBytes + ((lane >> 4) << 11) + (r8 << 7) + (((lane >> 3 & 1) ^ r8) << 4);
+    // S = K . Q^T
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      uint32_t x[4], y[4];
+      const uint32_t at = (kt + k_at) ^ (s << 5);
+      ldmatrix(at, x);
+      ldmatrix(at + 1024, y);
+      mma<T>(sa, x, qf[2 * s], qf[2 * s + 1]);
+      mma<T>(sb, y, qf[8 + 2 * s], qf[9 + 2 * s]);
+    }
+    float x00 = (sa[0] + sb[0]) * qscale, x01 = (sa[1] + sb[1]) * qscale;
+    float x10 = (sa[2] + sb[2]) * qscale, x11 = (sa[3] + sb[3]) * qscale;
+    if (left < kKvRows) {
+      if (g >= left) x00 = x01 = -INFINITY;
+      if (g + 8 >= left) x10 = x11 = -INFINITY;
+    }
+    const float t0 = fmaxf(x00, x10), t1 = fmaxf(x01, x11);
+    if (__any_sync(0xffffffffu, t0 > m0 + kStep || t1 > m1 + kStep)) {
+      float u0 = fmaxf(m0, t0), u1 = fmaxf(m1, t1);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
+        u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
+      }
+      const float f0 = ex2(m0 - u0), f1 = ex2(m1 - u1);
+      m0 = u0;
+      m1 = u1;
+      l0 *= f0;
+      l1 *= f1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc[j][0] *= f0;
+        acc[j][1] *= f1;
+        acc[j][2] *= f0;
+        acc[j][3] *= f1;
+      }
+    }
+    float p00 = ex2(x00 - m0), p01 = ex2(x01 - m1), p10 = ex2(x10 - m0), p11 = ex2(x11 - m1);
+    l0 += p00 + p10;
+    l1 += p01 + p11;
+    p00 *= 8.f;
+    p01 *= 8.f;
+    p10 *= 8.f;
+    p11 *= 8.f;
+    uint32_t h0 = take_pair<T>(p00, p01), h1 = take_pair<T>(p10, p11);
+    const uint32_t e0 = take_pair<T>(p00, p01), e1 = take_pair<T>(p10, p11);
+    uint32_t b0, b1, c0 = 0, c1 = 0, d0 = 0, d1 = 0;   // parts hi (and lo in columns 4 .. 7), then the other parts
+    if constexpr (WIDE) {
+      b0 = movmatrix_trans(h0);
+      b1 = movmatrix_trans(h1);
+      c0 = movmatrix_trans(e0);
+      c1 = movmatrix_trans(e1);
+    } else {
+      b0 = movmatrix_trans(t < 2 ? h0 : e0);
+      b1 = movmatrix_trans(t < 2 ? h1 : e1);
+    }
+    if constexpr (PARTS == 3) {
+      h0 = to_pair<T>(p00, p01);
+      h1 = to_pair<T>(p10, p11);
+      d0 = movmatrix_trans(WIDE || t < 2 ? h0 : 0u);
+      d1 = movmatrix_trans(WIDE || t < 2 ? h1 : 0u);
+    }
+    // O^T += V^T . P^T
+    uint32_t live01 = 0xffffffffu, live23 = 0xffffffffu;   // rows behind the end may hold anything, infinities too
+    if (left < kKvRows) {
+      live01 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
+      live23 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      uint32_t v[4];
+      ldmatrix_trans(((kt + v_at) ^ ((j & 3) << 5)) + (j >> 2) * 1024, v);
+      v[0] &= live01;
+      v[1] &= live01;
+      v[2] &= live23;
+      v[3] &= live23;
+      mma<T>(acc[j], v, b0, b1);
+      if constexpr (WIDE) mma<T>(acc[j], v, c0, c1);
+      if constexpr (PARTS == 3) mma<T>(acc[j], v, d0, d1);
+    }
+  }
+
+  // The whole pair's sums in every lane that has the head (l0, l1 of heads 2 t, 2 t + 1).
+  __device__ __forceinline__ void end() {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    if constexpr (!WIDE) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[j][k] += __shfl_xor_sync(0xffffffffu, acc[j][k], 2);
+    }
+  }
+};
+
+template <typename T, bool WIDE, int PARTS>
+__global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16RowsArgs a) {
   extern __shared__ uint8_t s_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
@@ -137,28 +264,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16Sp
 #pragma unroll
   for (int i = 0; i < kStages; ++i) put_one();
 
-  // where this lane's rows of the operands are: K, rows lane & 15 and the k-step's group
-  // lane / 16; V, rows (lane & 7) + 8 (lane / 16) and the coordinates' group lane / 8 & 1.
-  // Step j's groups (2 j, 2 j + 1) lie at ^ 32 j, the second four steps' 1024 behind.
-  const uint32_t r8 = lane & 7;
-  const uint32_t k_at = ((lane >> 3 & 1) << 11) + (r8 << 7) + (((lane >> 4) ^ r8) << 4);
-  const uint32_t v_at = kKvHalfBytes + ((lane >> 4) << 11) + (r8 << 7) + (((lane >> 3 & 1) ^ r8) << 4);
-  uint32_t qf[16];           // the query heads as the B operand: coordinates 16 s + 2 t (+ 8) of head g (or g & 3)
-  float acc[8][4];           // O^T: coordinates 16 j + g, + 8 (rows) x heads 2 t, 2 t + 1
-  float m0 = 0.f, m1 = 0.f, l0 = 0.f, l1 = 0.f;
+  Heads<T, WIDE, PARTS> heads;
   bool fresh = true;
   int stage = 0;
   for (; todo > 0; --todo) {
     if (fresh) {   // a new (row, head) pair: its query heads
       fresh = false;
-      const int head = WIDE ? g : g & 3;
-      const T* src = static_cast<const T*>(a.q) + get.row * a.q_stride + (get.h * a.group + head) * kKvD + 2 * t;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) qf[i] = static_cast<uint32_t>(ldg_or(reinterpret_cast<const int*>(src + 8 * i), head < a.group, 0));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) acc[j][0] = acc[j][1] = acc[j][2] = acc[j][3] = 0.f;
-      m0 = m1 = -1e30f;
-      l0 = l1 = 0.f;
+      heads.begin(static_cast<const T*>(a.q) + get.row * a.q_stride + get.h * a.group * kKvD, a.group, lane);
     }
 
     if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phases >> stage & 1))) {
@@ -171,88 +283,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16Sp
     const uint32_t kt = ring + stage * kKvTileBytes;
 
     if (!(bad >> stage & 1)) {
-      // S = K . Q^T
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        uint32_t x[4], y[4];
-        const uint32_t at = (kt + k_at) ^ (s << 5);
-        ldmatrix(at, x);
-        ldmatrix(at + 1024, y);
-        mma<T>(sa, x, qf[2 * s], qf[2 * s + 1]);
-        mma<T>(sb, y, qf[8 + 2 * s], qf[9 + 2 * s]);
-      }
-      float x00 = (sa[0] + sb[0]) * a.qscale, x01 = (sa[1] + sb[1]) * a.qscale;
-      float x10 = (sa[2] + sb[2]) * a.qscale, x11 = (sa[3] + sb[3]) * a.qscale;
-      const int left = get.len - kKvRows * get.t;   // positions from this tile on
-      if (left < kKvRows) {
-        if (g >= left) x00 = x01 = -INFINITY;
-        if (g + 8 >= left) x10 = x11 = -INFINITY;
-      }
-      const float t0 = fmaxf(x00, x10), t1 = fmaxf(x01, x11);
-      if (__any_sync(0xffffffffu, t0 > m0 + kStep || t1 > m1 + kStep)) {
-        float u0 = fmaxf(m0, t0), u1 = fmaxf(m1, t1);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) {
-          u0 = fmaxf(u0, __shfl_xor_sync(0xffffffffu, u0, o));
-          u1 = fmaxf(u1, __shfl_xor_sync(0xffffffffu, u1, o));
-        }
-        const float f0 = ex2(m0 - u0), f1 = ex2(m1 - u1);
-        m0 = u0;
-        m1 = u1;
-        l0 *= f0;
-        l1 *= f1;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          acc[j][0] *= f0;
-          acc[j][1] *= f1;
-          acc[j][2] *= f0;
-          acc[j][3] *= f1;
-        }
-      }
-      float p00 = ex2(x00 - m0), p01 = ex2(x01 - m1), p10 = ex2(x10 - m0), p11 = ex2(x11 - m1);
-      l0 += p00 + p10;
-      l1 += p01 + p11;
-      p00 *= 8.f;
-      p01 *= 8.f;
-      p10 *= 8.f;
-      p11 *= 8.f;
-      uint32_t h0 = take_pair<T>(p00, p01), h1 = take_pair<T>(p10, p11);
-      const uint32_t e0 = take_pair<T>(p00, p01), e1 = take_pair<T>(p10, p11);
-      uint32_t b0, b1, c0 = 0, c1 = 0, d0 = 0, d1 = 0;   // parts hi (and lo in columns 4 .. 7), then the other parts
-      if constexpr (WIDE) {
-        b0 = movmatrix_trans(h0);
-        b1 = movmatrix_trans(h1);
-        c0 = movmatrix_trans(e0);
-        c1 = movmatrix_trans(e1);
-      } else {
-        b0 = movmatrix_trans(t < 2 ? h0 : e0);
-        b1 = movmatrix_trans(t < 2 ? h1 : e1);
-      }
-      if constexpr (PARTS == 3) {
-        h0 = to_pair<T>(p00, p01);
-        h1 = to_pair<T>(p10, p11);
-        d0 = movmatrix_trans(WIDE || t < 2 ? h0 : 0u);
-        d1 = movmatrix_trans(WIDE || t < 2 ? h1 : 0u);
-      }
-      // O^T += V^T . P^T
-      uint32_t live01 = 0xffffffffu, live23 = 0xffffffffu;   // rows behind the end may hold anything, infinities too
-      if (left < kKvRows) {
-        live01 = (2 * t < left ? 0xffffu : 0u) | (2 * t + 1 < left ? 0xffff0000u : 0u);
-        live23 = (2 * t + 8 < left ? 0xffffu : 0u) | (2 * t + 9 < left ? 0xffff0000u : 0u);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint32_t v[4];
-        ldmatrix_trans(((kt + v_at) ^ ((j & 3) << 5)) + (j >> 2) * 1024, v);
-        v[0] &= live01;
-        v[1] &= live01;
-        v[2] &= live23;
-        v[3] &= live23;
-        mma<T>(acc[j], v, b0, b1);
-        if constexpr (WIDE) mma<T>(acc[j], v, c0, c1);
-        if constexpr (PARTS == 3) mma<T>(acc[j], v, d0, d1);
-      }
+      heads.tile(kt, get.len - kKvRows * get.t, a.qscale, lane);
     }
     __syncwarp();   // the stage is read: its next tile
     put_one();
@@ -260,29 +291,19 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16Sp
 
     // the end of the pair, or of this warp's part of it
     if (get.t + 1 == get.tiles || todo == 1) {
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-      }
-      if constexpr (!WIDE) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[j][k] += __shfl_xor_sync(0xffffffffu, acc[j][k], 2);
-      }
+      heads.end();
       const long long rec = (static_cast<long long>(get.row) * a.n_kv + get.h + wid) * a.group;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int head = 2 * t + k;
-        const float l = k ? l1 : l0, m = k ? m1 : m0;
+        const float l = k ? heads.l1 : heads.l0, m = k ? heads.m1 : heads.m0;
         if (head < a.group) {
           const float f = l > 0.f ? 0.125f / l : (l == 0.f ? 0.f : l);   // NaN stays
           float* o = a.rec_o + (rec + head) * kKvD + g;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            o[16 * j] = acc[j][k] * f;
-            o[16 * j + 8] = acc[j][k + 2] * f;
+            o[16 * j] = heads.acc[j][k] * f;
+            o[16 * j + 8] = heads.acc[j][k + 2] * f;
           }
           if (g == 0) a.rec_lse[rec + head] = l == 0.f ? -INFINITY : m + __log2f(l);
         }
@@ -293,16 +314,197 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16Sp
   }
 }
 
+// What row `row` of chunks sees, as tq_kv16_continue has it: positions of sequence `seq`.
+__device__ __forceinline__ int row_of_chunk(const Kv16RowsArgs& a, int row, int lane, int* seq, bool* too_long, bool* ours) {
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const bool in = b0 + lane < a.batch;
+    const int q0 = max(ldg_or(a.query_start + b0 + lane, in, INT_MAX), 0), q1 = ldg_or(a.query_start + b0 + lane + 1, in, 0);
+    const int len = max(ldg_or(a.seq_lens + b0 + lane, in, 0), 0);
+    const unsigned m = __ballot_sync(0xffffffffu, q0 <= row && row < q1);
+    if (m) {
+      const int k = __ffs(m) - 1, limit = min(a.max_seq_len, a.cap);
+      const int first = __shfl_sync(0xffffffffu, q0, k), last = __shfl_sync(0xffffffffu, q1, k), all = __shfl_sync(0xffffffffu, len, k);
+      const bool served = row - first < a.max_q_len;
+      *seq = b0 + k;
+      *too_long = !served || all > limit;
+      *ours = true;
+      // the chunk ends at the end of the rows, should its start say otherwise
+      return served ? max(min(all - min(last, a.rows) + row + 1, limit), 0) : 0;
+    }
+  }
+  *ours = *too_long = false;
+  return 0;
+}
+
+// Short work in one launch: a cluster of up to 8 CTAs per (sequence, KV head) pair, its
+// tiles dealt to their warps in turn; what the warps hold is merged in shared memory,
+// then what the CTAs hold, each CTA a part of the output.
+template <typename T, typename TO, bool WIDE>
+__global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const Kv16RowsArgs a) {
+  constexpr int kParts = std::is_same<T, __nv_bfloat16>::value && std::is_same<TO, float>::value ? 3 : 2;
+  extern __shared__ uint8_t s_raw[];
+  __shared__ float s_m[kShortWarps][kB8MaxGroup], s_l[kShortWarps][kB8MaxGroup];
+  __shared__ float s_o[kB8MaxGroup * kKvD], s_om[kB8MaxGroup], s_ol[kB8MaxGroup];   // the CTA's
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const uint32_t smem = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 127u) & ~127u;
+  const uint32_t ring = smem + warp * kStages * kKvTileBytes;
+  const uint32_t bars = smem + kShortWarps * kStages * kKvTileBytes + warp * kStages * 8;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  __syncwarp();
+  const int ctas = a.warps, rank = blockIdx.x % ctas, pair = blockIdx.x / ctas;   // CTAs of a pair
+  const int row = pair / a.n_kv, h = pair - row * a.n_kv;
+  const int first = rank * kShortWarps + warp, step = ctas * kShortWarps;   // of the pair's tiles
+  if (!a.early_indices) grid_dep_wait();
+  bool too_long, ours = true;   // ours: the row is somebody's
+  int len, seq = row;
+  if (a.query_start) {
+    len = row_of_chunk(a, row, lane, &seq, &too_long, &ours);
+  } else {
+    len = length_of(a, row, &too_long);
+  }
+  const int tiles = (len + kKvRows - 1) / kKvRows;
+  const int todo = tiles > first ? (tiles - first + step - 1) / step : 0;
+  // a block id a lane: this warp's tile number `lane` (no more than 32: see the launch)
+  const int ids = ldg_or(a.block_table + static_cast<long long>(seq) * a.c.bt_stride + ((first + lane * step) >> (a.c.log2_bs - 4)), lane < todo, -1);
+  if (a.early_indices) grid_dep_wait();
+  grid_dep_launch();
+  if (too_long && h == 0 && rank == 0 && threadIdx.x == 0) b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
+  const uint64_t policy = evict_first_policy();
+  const unsigned bad = __ballot_sync(0xffffffffu, lane < todo && !a.c.good(ids));   // tiles that are left out
+  if (bad && lane == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
+  auto put = [&](int i) {   // tile i of this warp's to stage i % kStages
+    const int blk = __shfl_sync(0xffffffffu, ids, i);
+    const uint32_t bar = bars + 8 * (i % kStages);
+    if (lane == 0 && !(bad >> i & 1)) {
+      mbar_expect(bar, kKvTileBytes);
+      bulk_g2s(ring + (i % kStages) * kKvTileBytes, a.c.tile(blk, h, first + i * step), kKvTileBytes, bar, policy);
+    }
+  };
+  for (int i = 0; i < kStages && i < todo; ++i) put(i);
+  Heads<T, WIDE, kParts> heads;
+  heads.begin(static_cast<const T*>(a.q) + row * a.q_stride + h * a.group * kKvD, a.group, lane);
+  unsigned phases = 0;   // a barrier's parity
+  bool ok = true;
+  for (int i = 0; i < todo; ++i) {
+    const int stage = i % kStages;
+    if (!(bad >> i & 1) && ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phases >> stage & 1)) != 0;
+      if (!ok) {   // gave up: the other copies in flight end, or have their time, and no more are asked for
+        b8_flag(a.status, TQ_DEV_TIMEOUT);
+        for (int k = 0; k < kStages; ++k) mbar_wait(bars + 8 * k, phases >> k & 1);
+        break;
+      }
+      phases ^= 1u << stage;
+      heads.tile(ring + stage * kKvTileBytes, len - kKvRows * (first + i * step), a.qscale, lane);
+    }
+    __syncwarp();
+    if (i + kStages < todo) put(i + kStages);
+  }
+  heads.end();
+  // the warp's heads to its own ring, [head][d], and their sums
+  float* mine = reinterpret_cast<float*>(s_raw + (ring - static_cast<uint32_t>(__cvta_generic_to_shared(s_raw))));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int head = 2 * t + k;
+    if (head < a.group && ok) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mine[head * kKvD + 16 * j + g] = heads.acc[j][k] * 0.125f;
+        mine[head * kKvD + 16 * j + g + 8] = heads.acc[j][k + 2] * 0.125f;
+      }
+    }
+    if (head < a.group && g == 0) {
+      s_m[warp][head] = k ? heads.m1 : heads.m0;
+      s_l[warp][head] = ok ? (k ? heads.l1 : heads.l0) : 0.f;
+    }
+  }
+  __syncthreads();
+  const int all = a.group * kKvD;
+  const float* rings = reinterpret_cast<const float*>(s_raw + (smem - static_cast<uint32_t>(__cvta_generic_to_shared(s_raw))));
+  TO* out = static_cast<TO*>(a.out) + (static_cast<long long>(row) * a.n_q + h * a.group) * kKvD;
+  if (!ours && ctas == 1) return;
+  for (int e = threadIdx.x; e < all; e += kShortWarps * 32) {
+    const int head = e >> 7;
+    float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kShortWarps; ++w) m = fmaxf(m, s_m[w][head]);
+#pragma unroll
+    for (int w = 0; w < kShortWarps; ++w) {
+      const float lw = s_l[w][head];
+      if (lw == 0.f) continue;   // nothing seen, and nothing in the ring
+      const float f = exp2f(s_m[w][head] - m);
+      l += lw * f;
+      o += rings[w * (kStages * kKvTileBytes / 4) + e] * f;
+    }
+    if (ctas == 1) {
+      out[e] = static_cast<TO>(l == 0.f ? 0.f : o / l);
+    } else {
+      s_o[e] = o;
+      if ((e & (kKvD - 1)) == 0) {
+        s_om[head] = m;
+        s_ol[head] = l;
+      }
+    }
+  }
+  if (ctas == 1) return;
+  cluster_sync();
+  const uint32_t at_o = static_cast<uint32_t>(__cvta_generic_to_shared(s_o)), at_m = static_cast<uint32_t>(__cvta_generic_to_shared(s_om)),
+                 at_l = static_cast<uint32_t>(__cvta_generic_to_shared(s_ol));
+  for (int e = rank * (kShortWarps * 32) + threadIdx.x; e < all; e += ctas * kShortWarps * 32) {
+    const int head = e >> 7;
+    float mk[8], lk[8], ok_[8], m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t from = k < ctas ? k : 0;
+      mk[k] = ld_cluster(at_m + 4 * head, from);
+      lk[k] = k < ctas ? ld_cluster(at_l + 4 * head, from) : 0.f;
+      ok_[k] = ld_cluster(at_o + 4 * e, from);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = fmaxf(m, mk[k]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (lk[k] == 0.f) continue;
+      const float f = exp2f(mk[k] - m);
+      l += lk[k] * f;
+      o += ok_[k] * f;
+    }
+    if (ours) out[e] = static_cast<TO>(l == 0.f ? 0.f : o / l);
+  }
+  cluster_sync();   // nobody goes while its sums are read
+}
+
 template <typename T, bool WIDE, int PARTS>
-cudaError_t launch_split(const Kv16SplitArgs& a, int ctas, int dev, cudaStream_t s) {
+cudaError_t launch_split(const Kv16RowsArgs& a, int ctas, int dev, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t err = b8_allow_smem(kv16_split_kernel<T, WIDE, PARTS>, kSmem, dev, &done);
   if (err != cudaSuccess) return err;
   return launch_pdl(kv16_split_kernel<T, WIDE, PARTS>, dim3(ctas), dim3(kWarps * 32), kSmem, s, a);
 }
 template <typename T, int PARTS>
-cudaError_t launch_split(const Kv16SplitArgs& a, int ctas, int dev, cudaStream_t s) {
+cudaError_t launch_split(const Kv16RowsArgs& a, int ctas, int dev, cudaStream_t s) {
   return a.group > 4 ? launch_split<T, true, PARTS>(a, ctas, dev, s) : launch_split<T, false, PARTS>(a, ctas, dev, s);
+}
+
+template <typename T, typename TO, bool WIDE>
+cudaError_t launch_short(Kv16RowsArgs a, int ctas, int dev, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t err = b8_allow_smem(kv16_short_kernel<T, TO, WIDE>, kShortSmem, dev, &done);
+  if (err != cudaSuccess) return err;
+  a.warps = ctas;
+  const dim3 grid(static_cast<unsigned>(a.rows) * a.n_kv * ctas);
+  return launch_pdl_cluster(kv16_short_kernel<T, TO, WIDE>, grid, dim3(kShortWarps * 32), ctas, kShortSmem, s, a);
+}
+template <typename T>
+cudaError_t launch_short(const Kv16RowsArgs& a, int out_dtype, int ctas, int dev, cudaStream_t s) {
+  if (out_dtype == TQ_DTYPE_F32) return a.group > 4 ? launch_short<T, float, true>(a, ctas, dev, s) : launch_short<T, float, false>(a, ctas, dev, s);
+  if (out_dtype == TQ_DTYPE_F16) return a.group > 4 ? launch_short<T, __half, true>(a, ctas, dev, s) : launch_short<T, __half, false>(a, ctas, dev, s);
+  return a.group > 4 ? launch_short<T, __nv_bfloat16, true>(a, ctas, dev, s) : launch_short<T, __nv_bfloat16, false>(a, ctas, dev, s);
 }
 
 size_t split_workspace(const tq_config* cfg, long long rows) {
@@ -311,11 +513,16 @@ size_t split_workspace(const tq_config* cfg, long long rows) {
   return (records * group * (kKvD + 1) * sizeof(float) + 15) / 16 * 16;
 }
 
-cudaError_t split_launch(Kv16SplitArgs a, bool is_bf16, int out_dtype, void* workspace, cudaStream_t s) {
+cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* workspace, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t err = b8_current_device(&dev, &sms);
   if (err != cudaSuccess) return err;
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
+  const long long tiles = (static_cast<long long>(a.max_seq_len) + kKvRows - 1) / kKvRows;
+  const long long pairs = static_cast<long long>(a.rows) * a.n_kv;
+  int each;
+  if (kv16_short(a.rows, a.n_kv, a.max_seq_len < a.cap ? a.max_seq_len : a.cap, ctas, kShortMost, &each))
+    return kv16_short_launch(a, is_bf16, out_dtype, each, dev, s);
   a.warps = ctas * kWarps;
   const size_t records = static_cast<size_t>(a.rows) * a.n_kv + kMaxWarps;
   a.rec_o = static_cast<float*>(workspace);
@@ -325,8 +532,7 @@ cudaError_t split_launch(Kv16SplitArgs a, bool is_bf16, int out_dtype, void* wor
   else err = launch_split<__nv_bfloat16, 2>(a, ctas, dev, s);
   if (err != cudaSuccess) return err;
   // records of a pair, if the lengths are alike: all of them in one round of loads
-  const long long tiles = (static_cast<long long>(a.max_seq_len) + kKvRows - 1) / kKvRows;
-  long long records_each = a.warps / (static_cast<long long>(a.rows) * a.n_kv) + 2;
+  long long records_each = a.warps / pairs + 2;
   if (records_each > tiles) records_each = tiles;
   if (out_dtype == TQ_DTYPE_F32) return launch_merge<float>(a, records_each, s);
   if (out_dtype == TQ_DTYPE_F16) return launch_merge<__half>(a, records_each, s);
@@ -334,6 +540,20 @@ cudaError_t split_launch(Kv16SplitArgs a, bool is_bf16, int out_dtype, void* wor
 }
 
 }  // namespace
+
+bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int* ctas) {
+  const long long pairs = rows * n_kv, tiles = (static_cast<long long>(max_len) + kKvRows - 1) / kKvRows;
+  int each = 8;   // as many as have an SM each, and a tile a warp
+  while (each > 1 && (pairs * each > sms || tiles <= static_cast<long long>(each / 2) * kShortWarps)) each /= 2;
+  *ctas = each;
+  const long long rounds = (pairs * each + sms - 1) / sms, of_warp = (tiles + each * kShortWarps - 1) / (each * kShortWarps);
+  return rounds <= 2 && of_warp <= 32 && rounds * (of_warp + 3) <= most;   // (32 tiles: a lane of the kernel each)
+}
+
+cudaError_t kv16_short_launch(const Kv16RowsArgs& a, bool is_bf16, int out_dtype, int ctas, int dev, cudaStream_t s) {
+  return is_bf16 ? launch_short<__nv_bfloat16>(a, out_dtype, ctas, dev, s) : launch_short<__half>(a, out_dtype, ctas, dev, s);
+}
+
 }  // namespace tq
 
 extern "C" {
@@ -362,7 +582,7 @@ tq_status tq_kv16_decode(const tq_config* cfg, const void* q, long long q_stride
   if ((st = b8_stride(&q_stride, static_cast<long long>(cfg->num_q_heads) * kKvD)) != TQ_OK) return st;
   if (workspace_bytes < split_workspace(cfg, batch)) return TQ_ERR_WORKSPACE_TOO_SMALL;
   if (static_cast<long long>(batch) * cfg->num_q_heads > INT_MAX) return TQ_ERR_UNSUPPORTED;
-  Kv16SplitArgs a = {};
+  Kv16RowsArgs a = {};
   a.c = kv16_cache(cfg, L, cache, num_blocks, bt_stride);
   a.q = q;
   a.q_stride = q_stride;

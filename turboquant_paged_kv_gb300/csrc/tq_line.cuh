@@ -109,18 +109,6 @@ __device__ __forceinline__ Place find_tile(const Args& a, long long x, int lane,
   return p;
 }
 
-template <typename TO>
-__device__ __forceinline__ void write4(TO* dst, float4 v) {
-  if constexpr (std::is_same<TO, float>::value) {
-    *reinterpret_cast<float4*>(dst) = v;
-  } else if constexpr (std::is_same<TO, __half>::value) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-}
-
 // A CTA of WARPS warps per (sequence, query head): the records of the pair are
 // those of the warps whose parts of the line meet it; warp k takes every
 // WARPS-th one, four at a time, a lane 4 coordinates.

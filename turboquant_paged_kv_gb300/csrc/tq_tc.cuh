@@ -126,18 +126,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, uint32_t (&r)[32]) { tmem
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[16]) { tmem_st16(addr, r); }
 __device__ __forceinline__ void tmem_st(uint32_t addr, const uint32_t (&r)[32]) { tmem_st32(addr, r); }
 
-template <typename TO>
-__device__ __forceinline__ void write4(TO* dst, float4 v) {
-  if constexpr (std::is_same<TO, float>::value) {
-    *reinterpret_cast<float4*>(dst) = v;
-  } else if constexpr (std::is_same<TO, __half>::value) {
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_half2(v.x, v.y), pack_half2(v.z, v.w));
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  }
-}
-
 // 32 bytes, at once where the address allows it (one answer for the grid).
 __device__ __forceinline__ void store32(void* dst, const uint32_t* v, bool wide) {
   if (!wide) {
