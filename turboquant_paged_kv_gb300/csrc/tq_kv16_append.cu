@@ -15,7 +15,7 @@
 namespace tq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kEach = 4;   // loads a lane and round: 8 head rows a warp
 constexpr int kEnough = 152 * 48;   // warps from which on they take more rounds rather than being more
 

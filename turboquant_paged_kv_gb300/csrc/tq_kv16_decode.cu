@@ -29,13 +29,14 @@
 namespace tq {
 namespace {
 
-constexpr int kWarps = 9;          // a CTA
-constexpr int kStages = 3;         // tiles in a warp's ring
+constexpr int kWarps = 13;         // a CTA
+constexpr int kStages = 2;         // tiles in a warp's ring
 constexpr int kMaxCtas = 256;      // grid cap: sizes the workspace without a device query
 constexpr int kMaxWarps = 4096;    // partial records beside one per pair
 constexpr int kSmem = kWarps * kStages * (kKvTileBytes + 8) + 128;   // and room to align to 128
 constexpr int kShortWarps = 8;     // a CTA of kv16_short_kernel
-constexpr int kShortSmem = kShortWarps * kStages * (kKvTileBytes + 8) + 128;
+constexpr int kShortStages = 3;
+constexpr int kShortSmem = kShortWarps * kShortStages * (kKvTileBytes + 8) + 128;
 // Up to which rounds x (tiles a warp + 3) the short kernel is used in place of the split and the merge, 2 rounds at most:
 // 16 x 1024 of 8 heads (8 tiles) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9, 32 x 1200 (10, two rounds) 29.1 for
 // 31.6, 20 x 1000 (8, two rounds) 20.4 for 20.1, 64 x 100 (1, four rounds) 15.7 for 14.9
@@ -348,11 +349,11 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t smem = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 127u) & ~127u;
-  const uint32_t ring = smem + warp * kStages * kKvTileBytes;
-  const uint32_t bars = smem + kShortWarps * kStages * kKvTileBytes + warp * kStages * 8;
+  const uint32_t ring = smem + warp * kShortStages * kKvTileBytes;
+  const uint32_t bars = smem + kShortWarps * kShortStages * kKvTileBytes + warp * kShortStages * 8;
   if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) mbar_init(bars + 8 * i, 1);
+    for (int i = 0; i < kShortStages; ++i) mbar_init(bars + 8 * i, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   __syncwarp();
@@ -377,33 +378,33 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
   const uint64_t policy = evict_first_policy();
   const unsigned bad = __ballot_sync(0xffffffffu, lane < todo && !a.c.good(ids));   // tiles that are left out
   if (bad && lane == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
-  auto put = [&](int i) {   // tile i of this warp's to stage i % kStages
+  auto put = [&](int i) {   // tile i of this warp's to stage i % kShortStages
     const int blk = __shfl_sync(0xffffffffu, ids, i);
-    const uint32_t bar = bars + 8 * (i % kStages);
+    const uint32_t bar = bars + 8 * (i % kShortStages);
     if (lane == 0 && !(bad >> i & 1)) {
       mbar_expect(bar, kKvTileBytes);
-      bulk_g2s(ring + (i % kStages) * kKvTileBytes, a.c.tile(blk, h, first + i * step), kKvTileBytes, bar, policy);
+      bulk_g2s(ring + (i % kShortStages) * kKvTileBytes, a.c.tile(blk, h, first + i * step), kKvTileBytes, bar, policy);
     }
   };
-  for (int i = 0; i < kStages && i < todo; ++i) put(i);
+  for (int i = 0; i < kShortStages && i < todo; ++i) put(i);
   Heads<T, WIDE, kParts> heads;
   heads.begin(static_cast<const T*>(a.q) + row * a.q_stride + h * a.group * kKvD, a.group, lane);
   unsigned phases = 0;   // a barrier's parity
   bool ok = true;
   for (int i = 0; i < todo; ++i) {
-    const int stage = i % kStages;
+    const int stage = i % kShortStages;
     if (!(bad >> i & 1) && ok) {
       ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * stage, phases >> stage & 1)) != 0;
       if (!ok) {   // gave up: the other copies in flight end, or have their time, and no more are asked for
         b8_flag(a.status, TQ_DEV_TIMEOUT);
-        for (int k = 0; k < kStages; ++k) mbar_wait(bars + 8 * k, phases >> k & 1);
+        for (int k = 0; k < kShortStages; ++k) mbar_wait(bars + 8 * k, phases >> k & 1);
         break;
       }
       phases ^= 1u << stage;
       heads.tile(ring + stage * kKvTileBytes, len - kKvRows * (first + i * step), a.qscale, lane);
     }
     __syncwarp();
-    if (i + kStages < todo) put(i + kStages);
+    if (i + kShortStages < todo) put(i + kShortStages);
   }
   heads.end();
   // the warp's heads to its own ring, [head][d], and their sums
@@ -439,7 +440,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
       if (lw == 0.f) continue;   // nothing seen, and nothing in the ring
       const float f = exp2f(s_m[w][head] - m);
       l += lw * f;
-      o += rings[w * (kStages * kKvTileBytes / 4) + e] * f;
+      o += rings[w * (kShortStages * kKvTileBytes / 4) + e] * f;
     }
     if (ctas == 1) {
       out[e] = static_cast<TO>(l == 0.f ? 0.f : o / l);
