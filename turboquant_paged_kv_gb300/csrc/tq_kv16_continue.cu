@@ -839,13 +839,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       const int wait_for = before;
       before = tiles;
       if (tiles == 0) continue;
-      if (!(ok = long_wait(kQEmpty, (filled++ & 1) ^ 1, wait_for))) break;
       const int c = lane & 15, last = rows > CTAS * 128 ? kRows : 128;
+      auto unit_row = [&](int here) { return CTAS == 2 ? here + (here & 128) + 128 * rank : here; };
+      auto row_at = [&](int r) {
+        const int qi = static_cast<int>(r * by_group >> 16);
+        return static_cast<const T*>(a.q) + (q0 + qi) * a.q_stride + static_cast<long long>(head0 + r - qi * a.group) * kKvD;
+      };
+      for (int k = threadIdx.x & 127; k < 2 * last; k += 128) {   // to L2, while the queries before are still in use
+        const int r = unit_row(k >> 1);
+        if (r < rows) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(row_at(r) + 64 * (k & 1)));
+      }
+      if (!(ok = long_wait(kQEmpty, (filled++ & 1) ^ 1, wait_for))) break;
 #pragma unroll 8
       for (int here = 2 * (warp - 12) + (lane >> 4); here < last; here += 8) {
-        const int r = CTAS == 2 ? here + (here & 128) + 128 * rank : here;   // of the unit
-        const int qi = static_cast<int>(r * by_group >> 16), head = head0 + r - qi * a.group;
-        const T* src = static_cast<const T*>(a.q) + (r < rows ? (q0 + qi) * a.q_stride + static_cast<long long>(head) * kKvD + 8 * c : 0);
+        const int r = unit_row(here);
+        const T* src = r < rows ? row_at(r) + 8 * c : static_cast<const T*>(a.q);
         const uint32_t to = base + (here >> 7) * kTileOp + (c >> 3) * kHalfQ + (here & 127) * 128 + (((c ^ here) & 7) << 4);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to), "l"(src), "r"(r < rows ? 16 : 0) : "memory");
       }
