@@ -3,35 +3,58 @@
 //
 //   out_i = sum_p softmax_p(scale q_i . k_p) v_p, p <= position of i
 //
-// A unit of work is 256 rows (the query heads of one KV head of 256 / group
-// consecutive queries, in two tiles of 128 rows) against all positions that they
-// see, 128 at a time:
+// Work. A unit is 512 rows (the query heads of one KV head of 512 / group consecutive
+// queries) of a pair of CTAs, or 256 of one, in two tiles of 128 rows a CTA, against
+// all positions that they see, in steps of 128. The steps of all units form one line,
+// cut by their cost into as many parts as there are teams of CTAs on the GPU, whatever
+// the lengths are; a unit that a cut goes through leaves records, which a second
+// kernel merges. A team walks its part of the line with one pipeline: the loads of a
+// unit's first steps and its queries come while the last of the unit before are
+// worked on. Few queries are not worth that: they run as rows of their own on the
+// decode's short kernel.
+//
+// Math, per tile t and half a step (64 positions):
 //   S_t = Q_t K^T      tcgen05.mma, A and B from shared memory
 //   P_t = 8 p          a row a thread, S read from tensor memory
 //   O_t += P_t V       A = P_t from tensor memory (it takes S_t's place), B = V
-// The steps of all units form one line, cut evenly over a grid of one CTA per SM,
-// whatever the lengths are; a unit that a cut goes through leaves records, which a
-// second kernel merges. A CTA walks its part of the line with one pipeline: the
-// loads of a unit's first steps and its queries come while the last steps of the
-// unit before are worked on.
+// S is double: the scores are issued two halves ahead, behind the product that frees
+// their place, so the softmax finds the next ones there.
+// p = 2^(score - m): no maximum is sought but in a part's first half. The weights are
+// taken with the maximum so far, and a row of which some P would not fit in fp16 shows
+// in its sum; only then the row's new m is found and what was accumulated (by the
+// softmax warps, in tensor memory) rescaled. m is the row's own, at most its largest
+// score so far, so the largest P of a row is 8 or more, and no position behind the
+// row's own changes a bit of it. P is rounded to the cache's type (bf16: by 2^-8, fp16:
+// by 2^-11 and no finer than 2^-25), as a 16-bit output is: against 64 bits, 2.3e-3
+// instead of the output's own 1.7e-3 in bf16, 2.9e-4 instead of 2.1e-4 in fp16. With
+// f32 output it is held in two parts (bf16 2^-16, fp16 2^-22), for twice the products
+// of P V.
 //
-// p = 2^(score - m): no maximum is sought in the common case. The weights are taken
-// with the maximum so far, and a row of which some P would not fit in fp16 shows in
-// its sums; only then the row's new m is found, and what was accumulated (by the
-// softmax warps, in tensor memory) and the step's earlier P are rescaled. m is the
-// row's own, at most its largest score so far, so the largest P of a row is 8 or
-// more, and no position behind the row's own changes a bit of it. P is rounded to
-// the cache's type (bf16: by 2^-8, fp16: by 2^-11 and no finer than 2^-25), which is
-// what a 16-bit output is rounded to as well; with f32 output it is held in two
-// parts (bf16 2^-16, fp16 2^-22).
+// A pair of CTAs shares one tile of keys and values (cta_group::2: each loads half of
+// the keys' positions and half of the values' coordinates). A CTA alone needs all of
+// shared memory's rate for it: of a step's 2048 cycles of products, 1024 go to reading
+// Q and K, 512 to V, 512 to loading both.
 //
-// Warps: 0-3 and 4-7 the softmax of tile 0 and 1, 8 issues the products (of the two
-// tiles in turn, so that one tile's products run while the other's softmax does), 9
-// finds the work and loads keys and values, 10 and 11 load queries. Keys and values
-// come by bulk copies, 4096 bytes a tile of 16 positions: they lie in the cache as
-// the tensor cores read them (128-byte swizzle; K a K-major operand, V an MN-major
-// one). Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the
-// CTA, after its products and copies in flight.
+// Warps: 0-3 and 4-7 the softmax of tile 0 and 1; 8 and 9 issue the products of tile 0
+// and 1 (of both CTAs of a pair, in its first), in turn, so that the two tiles stay half
+// a round apart; 10 finds the work and loads keys and values; 11, in the second CTA of
+// a pair, tells the first what has come; 12-15 load queries. Keys and values come by
+// bulk copies: they lie in the cache as the tensor cores read them (128-byte swizzle; K
+// a K-major operand, V an MN-major one). Every wait is bounded; one that runs out sets
+// TQ_DEV_TIMEOUT and ends the CTA, after its products and copies in flight.
+//
+// Bound: tensor cores by its operations. 4 chunks of 2001-2048 queries over 0-6144, 32
+// query heads, fp16: 533 us, 1590 TFLOP/s, 0.84 of a measured bf16 GEMM (603 us, 1407,
+// over seconds, where the power limit takes the clock to 1.7 GHz); 32 chunks of 128 over
+// 4096, bf16: 199 us, 1403 (212 us); 12 of 1-500 over 0-16384, 64 heads: 405 us, 1325.
+// A step of two tiles takes about 2800 cycles, 2304 of them products (64 a product,
+// 40 instead of 32 where only 64 positions stand against Q). Steps that led here, on the
+// second case: one CTA, a warp that issues for both tiles, S single 237 us; two threads a
+// row 236; pairs of CTAs 249, with S double 237; an issuing warp a tile 214; in turn, with
+// one barrier a load, 211; a line cut by cost, two-part merges 209; rows by way of shared
+// memory 202; queries asked for early 199. Tried and left out: S of the next half loaded
+// into registers before P is handed over (222 for 214), the turn given before the last
+// products are issued (202 for 199), 5 stages for a pair (223 for 222 over seconds).
 #include <climits>
 
 #include "tq_kv16.cuh"
@@ -48,13 +71,15 @@ constexpr float kMost = 60000.f;       // sums of P up to this: every P fits in 
 constexpr uint32_t kTileOp = 32768;    // a 128 x 128 operand
 constexpr uint32_t kHalfQ = 16384;     // Q: two halves of 64 columns, 128 bytes a row
 constexpr uint32_t kStage = 32768;     // what is loaded at once: 16 KB of keys, then 16 KB of values
-// behind Q and the stages: room for the output's rows, or one more stage where the loads bound
+// behind Q and the stages: room for a pair's output, or one more stage for one CTA, whose few rows wait for loads (32 x 5
+// queries over 4096: 102 us with 5 stages, 120 with 4)
 constexpr uint32_t kOffLoads = 2 * kTileOp, kOffOut = kOffLoads + 4 * kStage, kOffBar = kOffOut + kStage;
 constexpr uint32_t kSmem = kOffBar + 512 + 1024;   // and room to align to 1024
-
 constexpr int kBad = 16;               // loads whose bad blocks are remembered (more than are between the loads and the softmax)
 constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: two halves' S of each tile, O of each tile
-constexpr int kPairRows = 256;                     // rows a chunk, on average, from which on pairs of CTAs are used
+// Rows a chunk, on average, above which pairs of CTAs are used: 16 x 96 queries of 32 heads over 8192 (384 rows) 193 us for
+// 217, 16 x 64 (256) 150 for 135, where a pair's units are half empty
+constexpr int kPairRows = 256;
 // Up to which cost (tq_kv16.cuh) queries are rows of their own: 1 x 64 over 2000 of 2 heads (16 tiles a warp) 12.4 us for
 // 19.3, 3 x 7 over 400 of 8 (4, two rounds) 10.1 for 12.9, 4 x 5 over 1000 (8, two rounds) 14.9 for 15.0, 1 x 16 over 4000
 // (31) 20.9 for 17.9, 8 x 5 over 500 (4, three rounds) 16.3 for 15.1
@@ -68,7 +93,7 @@ struct ChunkArgs {
   const int *block_table, *seq_lens, *query_start;
   unsigned int* status;
   void* out;
-  // CTA i's unit that others go on with: first row, rows, first head, parts (0: none);
+  // team i's unit that others go on with: first row, rows, first head, parts (0: none);
   // record 2 i is what it adds to a unit that others began, 2 i + 1 the first part of
   // one that others go on with: [part_rows][d] and [part_rows] (log2 units)
   int4* split_units;
@@ -181,7 +206,7 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 // the cost of the unit. (Units that read the same keys and values, tiles of one chunk,
 // are then a fixed part of the line apart, so that teams of CTAs meet them at the same
 // time where chunks are alike.) A step costs 4, or 3 where one row tile is at work, and
-// a unit 10 more (1.57, 1.21 and 3.8 us). A warp walks it, the lanes together.
+// a unit 10 more (1.45, 1.14 and 3 to 4 us). A warp walks it, the lanes together.
 struct Line {
   static constexpr int kUnit = 10;
   const ChunkArgs& a;
@@ -217,21 +242,21 @@ struct Line {
     ch = chunk_of(a, first + lane, per);
   }
   __device__ int each_of(int j) const { return (min(ch.n, a.max_q_len) - j * per) * a.group > full_rows ? 4 : 3; }
-  __device__ int cost(int j) const {
+  __device__ unsigned cost(int j) const {
     const int s = steps_of(a, ch, j, per);
-    return s ? s * each_of(j) + kUnit : 0;
+    return s ? static_cast<unsigned>(s) * each_of(j) + kUnit : 0u;
   }
   // The unit of tile index j that place x of the 32 sequences' is in; they begin at `base`.
   __device__ Unit locate(long long x, int j, long long base) {
-    const int c = cost(j);
-    int inc = c;   // below 32 * (4 * 2^24 + 10)
+    const unsigned c = cost(j);
+    unsigned inc = c;   // at most 32 * (4 * 2^24 + 10)
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
     const int src = __ffs(__ballot_sync(0xffffffffu, x - base < static_cast<long long>(inc) * a.c.n_kv)) - 1;
-    const int here = __shfl_sync(0xffffffffu, c, src);
+    const unsigned here = __shfl_sync(0xffffffffu, c, src);
     base += static_cast<long long>(__shfl_sync(0xffffffffu, inc, src) - here) * a.c.n_kv;
     const int h = static_cast<int>((x - base) / here);
     return {j, b0 + src, h, __shfl_sync(0xffffffffu, steps_of(a, ch, j, per), src), __shfl_sync(0xffffffffu, each_of(j), src),
@@ -351,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     return __all_sync(0xffffffffu, ok) != 0;
   };
 
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
   if (warp < 8) {
     // ---- softmax: of tile warp / 4, a thread a row
     asm volatile("setmaxnreg.inc.sync.aligned.u32 192;\n");   // 2 x 192 + 2 x 64 = 4 x 128 registers a thread
@@ -568,9 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       }
       if (live && !whole) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
     }
-  } else {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-  if (warp < 10 && rank == 0) {
+  } else if (warp < 10 && rank == 0) {
     // ---- products, of tile warp - 8. The whole warp walks the halves of steps, so that
     // descriptors and addresses stay in uniform registers; one lane, always the same,
     // issues. Scores are issued two halves ahead: the softmax finds the next ones there.
@@ -818,9 +842,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       line.next();
       from = 0;
     }
-    // the copies in flight end before their memory goes (in the first CTA of a pair, the second one's too)
+    // the copies in flight end before their memory goes (in the first CTA of a pair, the second one's too), and so do the
+    // products that read them and what these signal to either CTA
     for (int k = 0; k < kStages; ++k) {   // the last load of each stage, the oldest first
-      if (loads + k >= kStages) warp_wait(kFull0 + load.stage, load.round ^ 1);
+      if (loads + k >= kStages) {
+        warp_wait(kFull0 + load.stage, load.round ^ 1);
+        if (ok) warp_wait(kEmpty0 + load.stage, load.round ^ 1);
+      }
       load.next();
     }
   } else {
@@ -862,7 +890,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       __syncwarp();
       if (lane == 0) arrive_first(kQFull);
     }
-  }
   }
   fence_before();
   __syncthreads();
