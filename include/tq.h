@@ -661,7 +661,7 @@ typedef enum {
  *   rot_dim       0 or a multiple of 16 up to d
  *   rope_style    tq_rope_style (not looked at with rot_dim 0)
  *   query_start   device int32 [batch + 1], non-decreasing from 0; rows from
- *                 query_start[batch] to total_q are neither read nor written
+ *                 query_start[batch] to total_q are not used, and q_out's stay
  *   block_table, bt_stride, seq_lens
  *                 as for tq_b8_store: lengths WITH the chunk
  * Not stored: rows before position 0, positions past bt_stride * block_size and,
@@ -699,7 +699,10 @@ size_t tq_kv16_continue_workspace_size(const tq_config* cfg, int batch, int tota
 
 /* Device. Causal attention of chunks of queries whose keys and values are
  * already stored: arguments and rules as for tq_b8_continue. q is of the cache's
- * type. What a query gives does not depend on what is cached behind its position. */
+ * type. The weights are rounded to it (by half a step, as out is) where out is f16
+ * or bf16, and held in two parts of it (bf16: 2^-16, f16: 2^-22) where it is f32.
+ * Scores of magnitudes from 1e9 on, which fp32 holds no units of, do not come out
+ * right. What a query gives does not depend on what is cached behind its position. */
 tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stride,
                            const int* query_start, int batch, int total_q, int max_q_len,
                            const void* cache, long long num_blocks,

@@ -365,16 +365,35 @@ def check_row(c, q, k, v, got, out_dtype, scale, chunk, where):
     assert np.all(err <= tol), (*where, float((err / tol).max()))
 
 
-def run_decode(c, q, lens=None, out_dtype="f32", status=None, max_len=None, scale=0.0):
+def shifted(shape, dtype, value, shift):
+    """A tensor of `value` that begins `shift` bytes behind a 32-byte boundary."""
+    n, off = int(np.prod(shape)), shift // torch.empty(0, dtype=dtype).element_size()
+    room = torch.full((n + 16,), value, dtype=dtype, device="cuda")
+    assert room.data_ptr() % 32 == 0
+    return room[off:off + n].view(shape)
+
+
+# More (sequence, head) pairs than this are not one launch's work on any of the sizes here
+FEW = 2 * 152
+
+
+def run_decode(c, q, lens=None, out_dtype="f32", status=None, max_len=None, scale=0.0, line=False, shift=0):
+    """`line`: with empty sequences behind the others until the line's split and merge take the call."""
     cache, table, _ = c.gpu()
+    rows = q.shape[0]
     lens = c.lens if lens is None else np.asarray(lens, dtype=np.int32)
     msl = max(int(lens.max(initial=0)), 1) if max_len is None else max_len
-    out = torch.full(q.shape, float("nan"), dtype=DT[out_dtype], device="cuda")
-    ws = torch.full((c.tq.tq_kv16_decode_workspace_size(c.cfg, q.shape[0], msl),), 255, dtype=torch.uint8, device="cuda")
-    c.tq.tq_kv16_decode(c.cfg, q.cuda() if not q.is_cuda else q, cache, table, torch.from_numpy(lens).cuda(), msl, out, ws, scale=scale,
-                        dev_status=status)
+    q = q.cuda()
+    if line:
+        more = max(FEW // c.n_kv + 1 - rows, 0)
+        q = torch.cat([q, q[:1].repeat(more, 1, 1)])
+        lens, table = np.append(lens, np.zeros(more, dtype=np.int32)), torch.cat([table, table[:1].repeat(more, 1)])
+    out = shifted(q.shape, DT[out_dtype], float("nan"), shift)
+    ws = shifted((c.tq.tq_kv16_decode_workspace_size(c.cfg, q.shape[0], msl),), torch.uint8, 255, shift)
+    c.tq.tq_kv16_decode(c.cfg, q, cache, table, torch.from_numpy(lens).cuda(), msl, out, ws, scale=scale, dev_status=status)
     torch.cuda.synchronize()
-    return out.float().cpu().numpy().astype(np.float64)
+    assert not out[rows:].any()
+    return out[:rows].float().cpu().numpy().astype(np.float64)
 
 
 def check_decode(c, q, got, out_dtype, lens=None, scale=SCALE):
@@ -387,12 +406,13 @@ def check_decode(c, q, got, out_dtype, lens=None, scale=SCALE):
 @pytest.mark.parametrize("block,n_kv,group,dtype,out", [
     (16, 8, 4, "bf16", "bf16"), (32, 2, 1, "fp16", "fp16"), (64, 1, 8, "bf16", "f32"), (128, 2, 3, "fp16", "f32"),
     (16, 1, 5, "bf16", "f32"), (64, 3, 2, "fp16", "bf16"), (16, 2, 7, "bf16", "fp16"), (32, 1, 6, "fp16", "f32"), (16, 2, 4, "fp16", "f32")])
-def test_decode(tq, block, n_kv, group, dtype, out):
+@pytest.mark.parametrize("line", [False, True])
+def test_decode(tq, block, n_kv, group, dtype, out, line):
     lens = [0, 1, 15, 16, 17, 63, 64, 65, 200, 333]
     c = Case(tq, dtype, block, n_kv * group, n_kv, [max(x, 1) for x in lens], seed=group).fill(lens)
     q = c.draw(len(lens), n_kv * group, outlier=True)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    got = run_decode(c, q, out_dtype=out, status=status)
+    got = run_decode(c, q, out_dtype=out, status=status, line=line)
     assert int(status) == 0
     assert not got[0].any()                      # nothing cached: zeros
     check_decode(c, q, got, out)
@@ -400,10 +420,11 @@ def test_decode(tq, block, n_kv, group, dtype, out):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("lens", [[1], [0], [0, 0, 0], [2100], [700, 0, 0, 1, 900], [9000, 3]])
-def test_decode_few_and_empty_sequences(tq, dtype, lens):
+@pytest.mark.parametrize("line", [False, True])
+def test_decode_few_and_empty_sequences(tq, dtype, lens, line):
     c = Case(tq, dtype, 16, 4, 1, [max(x, 1) for x in lens], seed=3).fill(lens)
     q = c.draw(len(lens), 4)
-    check_decode(c, q, run_decode(c, q), "f32")
+    check_decode(c, q, run_decode(c, q, line=line), "f32")
 
 
 def test_decode_many_sequences(tq):
@@ -415,17 +436,18 @@ def test_decode_many_sequences(tq):
     check_decode(c, q, run_decode(c, q), "f32")
 
 
-def test_decode_scale_argument_and_strided_queries(tq):
-    lens = [50, 20]
+@pytest.mark.parametrize("lens", [[50, 20], [50, 20, 0, 33] * 40])      # one launch, or the split and the merge
+def test_decode_scale_argument_and_strided_queries(tq, lens):
     c = Case(tq, "fp16", 32, 8, 2, lens, seed=12).fill(lens)
-    fused = c.draw(2, 12).cuda()
+    fused = c.draw(len(lens), 12).cuda()
     got = run_decode(c, fused[:, :8], scale=0.31)
     check_decode(c, fused[:, :8].cpu(), got, "f32", scale=float(np.float32(0.31)))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("gain", [1e-3, 30.0])
-def test_decode_scores_that_rise(tq, dtype, gain):
+@pytest.mark.parametrize("line", [False, True])
+def test_decode_scores_that_rise(tq, dtype, gain, line):
     """Keys that grow along the sequence: the running maximum moves again and again, by little or by much."""
     n = 700
     c = Case(tq, dtype, 16, 5, 1, [n], seed=24)
@@ -433,17 +455,18 @@ def test_decode_scores_that_rise(tq, dtype, gain):
     c.put(0, k.to(DT[dtype]), c.draw(n, 1))
     c.lens = np.array([n], dtype=np.int32)
     q = (torch.ones((1, 5, 128)) * torch.tensor([1.0, -1.0, 0.3, 2.0, 0.0])[None, :, None]).to(DT[dtype])
-    check_decode(c, q, run_decode(c, q), "f32")
+    check_decode(c, q, run_decode(c, q, line=line), "f32")
     got = run_continue(c, q.repeat(40, 1, 1), [0, 40], [n])
     check_continue(c, q.repeat(40, 1, 1), got, [0, 40], [n], "f32")
 
 
-def test_decode_device_errors(tq):
+@pytest.mark.parametrize("line", [False, True])
+def test_decode_device_errors(tq, line):
     c = Case(tq, "bf16", 16, 4, 2, [100, 40], seed=14).fill([100, 40])
     c.table[0, 2], c.table[1, :] = -1, 2 ** 31 - 1
     q = c.draw(2, 4)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    got = run_decode(c, q, status=status, max_len=90)
+    got = run_decode(c, q, status=status, max_len=90, line=line)
     assert int(status) == tq.TQ_DEV_BLOCK_OUT_OF_RANGE | tq.TQ_DEV_SEQ_TOO_LONG
     check_decode(c, q, got, "f32", lens=[90, 40])      # positions of bad blocks are left out; nothing left: zeros
     assert not got[1].any()
@@ -455,8 +478,9 @@ def test_not_a_number_query_stays_in_its_row(tq, mode, dtype):
     c = Case(tq, dtype, 16, 4, 1, lens, seed=15).fill(lens)
     q = c.draw(2, 4)
     q[0, 1, 3] = float("nan")
-    got = run_decode(c, q)
-    assert np.isnan(got[0, 1]).all() and np.isfinite(got[0, [0, 2, 3]]).all() and np.isfinite(got[1]).all()
+    for line in (False, True):
+        got = run_decode(c, q, line=line)
+        assert np.isnan(got[0, 1]).all() and np.isfinite(got[0, [0, 2, 3]]).all() and np.isfinite(got[1]).all()
     q = c.draw(20, 4)
     q[3, 2, 3], q[5, 0, 7] = float("nan"), float("inf")
     for lens, starts in (([40, 40], [0, 10, 20]), ([40, 40], [0, 1, 20])):
@@ -467,18 +491,20 @@ def test_not_a_number_query_stays_in_its_row(tq, mode, dtype):
         assert np.isfinite(got[fine]).all()
 
 
-def test_decode_on_streams_and_in_graphs(tq):
+@pytest.mark.parametrize("pad", [0, 80])      # one launch, or the split and the merge
+def test_decode_on_streams_and_in_graphs(tq, pad):
     """Two calls on two streams with a workspace each, and a captured call
     replayed after the lengths and the query changed, with the indices known
     early too; the same call twice gives the same bits."""
-    lens = [300, 45, 0, 128]
+    lens, rows = [300, 45, 0, 128], 4 + pad
     c = Case(tq, "bf16", 32, 16, 4, [400] * 4, seed=16).fill([400] * 4)
     cache, table, _ = c.gpu()
-    lens_d = torch.tensor(lens, dtype=torch.int32, device="cuda")
-    q = [c.draw(4, 16).cuda() for _ in range(2)]
-    n = tq.tq_kv16_decode_workspace_size(c.cfg, 4, 400)
+    table = torch.cat([table, table[:1].repeat(pad, 1)])
+    lens_d = torch.tensor(lens + [0] * pad, dtype=torch.int32, device="cuda")
+    q = [c.draw(rows, 16).cuda() for _ in range(2)]
+    n = tq.tq_kv16_decode_workspace_size(c.cfg, rows, 400)
     ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
-    out = [torch.empty((4, 16, 128), dtype=torch.float32, device="cuda") for _ in range(2)]
+    out = [torch.empty((rows, 16, 128), dtype=torch.float32, device="cuda") for _ in range(2)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
     for i in range(2):
@@ -486,7 +512,7 @@ def test_decode_on_streams_and_in_graphs(tq):
             tq.tq_kv16_decode(c.cfg, q[i], cache, table, lens_d, 400, out[i], ws[i])
     torch.cuda.synchronize()
     for i in range(2):
-        check_decode(c, q[i].cpu(), out[i].cpu().numpy().astype(np.float64), "f32", lens=lens)
+        check_decode(c, q[i][:4].cpu(), out[i].cpu().numpy().astype(np.float64), "f32", lens=lens)
     first = out[0].clone()
     tq.tq_kv16_decode(c.cfg, q[0], cache, table, lens_d, 400, out[0], ws[0])
     assert torch.equal(first, out[0])
@@ -498,15 +524,15 @@ def test_decode_on_streams_and_in_graphs(tq):
             tq.tq_kv16_decode(cfg, q[0], cache, table, lens_d, 400, out[0], ws[0])
         graphs.append(graph)
     for new in ([400, 1, 33, 0], [17, 399, 64, 250]):
-        lens_d.copy_(torch.tensor(new, dtype=torch.int32))
-        fresh = c.draw(4, 16)
+        lens_d[:4].copy_(torch.tensor(new, dtype=torch.int32))
+        fresh = c.draw(rows, 16)
         q[0].copy_(fresh)
         for graph in graphs:
             out[0].fill_(float("nan"))
             torch.cuda.synchronize()
             graph.replay()
             torch.cuda.synchronize()
-            check_decode(c, fresh, out[0].cpu().numpy().astype(np.float64), "f32", lens=new)
+            check_decode(c, fresh[:4], out[0].cpu().numpy().astype(np.float64), "f32", lens=new)
 
 
 def test_refusals_with_tensors_on_the_gpu(tq):
@@ -559,23 +585,22 @@ def mode(request):
     MODE = "rows"
 
 
-def run_continue(c, q, starts, lens, out_dtype="f32", status=None, max_q=None, max_len=None, scale=0.0):
+def run_continue(c, q, starts, lens, out_dtype="f32", status=None, max_q=None, max_len=None, scale=0.0, shift=0):
     cache, table, _ = c.gpu()
     rows, batch, group = q.shape[0], len(lens), c.n_q // c.n_kv
     starts, lens = np.asarray(starts, dtype=np.int32), np.asarray(lens, dtype=np.int32)
     msl = max(int(max(lens)), 1) if max_len is None else max_len
     mq = int(np.diff(starts).max(initial=0)) if max_q is None else max_q
     if MODE != "rows":
-        more = max(305 - rows, 0 if MODE == "single" else 256 * batch // group + 1 - rows, 0)
+        more = max(FEW + 1 - rows, 0 if MODE == "single" else 256 * batch // group + 1 - rows, 0)
         empty = max(-(-(rows + more) * group // 256) - batch, 0) if MODE == "single" else 0
         q = torch.cat([q.cpu(), torch.zeros((more, *q.shape[1:]), dtype=q.dtype)])
         starts, lens = np.append(starts, [starts[-1]] * empty), np.append(lens, [0] * empty)
         table = torch.cat([table, table[:1].repeat(empty, 1)])
-        assert (q.shape[0] * group > 256 * len(lens)) == (MODE == "pair") and q.shape[0] * c.n_kv > 304
+        assert (q.shape[0] * group > 256 * len(lens)) == (MODE == "pair") and q.shape[0] * c.n_kv > FEW
     dev = lambda x: torch.from_numpy(np.asarray(x, dtype=np.int32)).cuda()      # noqa: E731
-    out = torch.full(q.shape, 123.0, dtype=DT[out_dtype], device="cuda")
-    n = c.tq.tq_kv16_continue_workspace_size(c.cfg, len(lens), q.shape[0], mq, msl)
-    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    out = shifted(q.shape, DT[out_dtype], 123.0, shift)
+    ws = shifted((c.tq.tq_kv16_continue_workspace_size(c.cfg, len(lens), q.shape[0], mq, msl),), torch.uint8, 255, shift)
     c.tq.tq_kv16_continue(c.cfg, q.cuda() if not q.is_cuda else q, dev(starts), mq, cache, table, dev(lens), msl, out, ws, scale=scale,
                           dev_status=status)
     torch.cuda.synchronize()
@@ -710,23 +735,12 @@ def test_one_position_is_its_value(tq, mode, dtype):
 
 
 @pytest.mark.parametrize("hist,dtype,out", [(20, "bf16", "bf16"), (2000, "fp16", "fp16"), (20, "bf16", "f32"), (2000, "bf16", "f32")])
-def test_output_on_16_bytes(tq, hist, dtype, out):
+def test_output_on_16_bytes(tq, mode, hist, dtype, out):
     """out and workspace may lie on any 16 bytes (whole and split histories)."""
     c = Case(tq, dtype, 32, 4, 1, [hist + 40], seed=44).fill([hist + 40])
-    cache, table, lens = c.gpu()
     q = c.draw(40, 4)
-    n = 40 * 4 * 128
-    room = torch.empty(n + 16, dtype=DT[out], device="cuda")
-    size = max(tq.tq_kv16_continue_workspace_size(c.cfg, 1, 40, 40, hist + 40), tq.tq_kv16_decode_workspace_size(c.cfg, 1, hist + 40))
-    ws = torch.empty(size + 16, dtype=torch.uint8, device="cuda")
-    off = 16 // room.element_size()
-    assert room.data_ptr() % 32 == 0 and ws.data_ptr() % 32 == 0
-    got = room[off:off + n].view(40, 4, 128)
-    starts = torch.tensor([0, 40], dtype=torch.int32, device="cuda")
-    tq.tq_kv16_continue(c.cfg, q.cuda(), starts, 40, cache, table, lens, hist + 40, got, ws[16:])
-    check_continue(c, q, got.float().cpu().numpy().astype(np.float64), [0, 40], [hist + 40], out, rows=6)
-    tq.tq_kv16_decode(c.cfg, q[:1].cuda(), cache, table, lens, hist + 40, got[:1], ws[16:])
-    check_decode(c, q[:1], got[:1].float().cpu().numpy().astype(np.float64), out)
+    check_continue(c, q, run_continue(c, q, [0, 40], [hist + 40], out, shift=16), [0, 40], [hist + 40], out, rows=6)
+    check_decode(c, q[:1], run_decode(c, q[:1], out_dtype=out, line=mode == "single", shift=16), out)
 
 
 @pytest.mark.parametrize("q_len", [4, 140])
@@ -813,19 +827,23 @@ def test_rows_that_were_not_stored(tq, mode, dtype, block, hist, q_len, max_q):
     check_decode(c, q[:1], run_decode(c, q[:1], [kept]), "f32", lens=[kept])
 
 
-def test_continue_on_streams_and_in_graphs(tq):
+@pytest.mark.parametrize("rows,empty", [(64, 0), (400, 5), (400, 0)])      # rows of their own, units of a CTA, of a pair
+def test_continue_on_streams_and_in_graphs(tq, rows, empty):
     """As for the decode: two streams, then a captured call replayed with other
     starts, lengths and queries in padded tensors; the same call gives the same bits."""
     c = Case(tq, "fp16", 16, 8, 2, [900] * 3, seed=60).fill([900] * 3)
     cache, table, _ = c.gpu()
-    rows, msl = 64, 900
+    msl, batch = 900, 3 + empty
+    table = torch.cat([table, table[:1].repeat(empty, 1)])
+    padded = lambda starts, lens: (starts + starts[-1:] * empty, lens + [0] * empty)      # noqa: E731
+    assert (rows * 4 > 256 * batch, rows * 2 > FEW) == ((False, False), (False, True), (True, True))[(rows > 64) + (rows > 64 and not empty)]
     calls = []
-    for starts, lens in (([0, 20, 20, 55], [900, 3, 500]), ([0, 1, 40, 64], [7, 899, 64])):
+    for starts, lens in (padded([0, 20, 20, 55], [900, 3, 500]), padded([0, 1, 40, 64], [7, 899, 64])):
         q = c.draw(rows, 8)
         calls.append((q, starts, lens, q.cuda(), torch.tensor(starts, dtype=torch.int32, device="cuda"),
                       torch.tensor(lens, dtype=torch.int32, device="cuda"),
                       torch.full((rows, 8, 128), 123.0, dtype=torch.float32, device="cuda"),
-                      torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, 3, rows, 48, msl), dtype=torch.uint8, device="cuda"),
+                      torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, batch, rows, 48, msl), dtype=torch.uint8, device="cuda"),
                       torch.cuda.Stream()))
     torch.cuda.synchronize()
     for _, _, _, q, starts, lens, out, ws, stream in calls:
@@ -843,7 +861,7 @@ def test_continue_on_streams_and_in_graphs(tq):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         tq.tq_kv16_continue(c.cfg, q_d, starts_d, 48, cache, table, lens_d, msl, out, ws)
-    for starts, lens in (([0, 48, 49, 60], [48, 800, 333]), ([0, 0, 0, 5], [10, 20, 700]), ([0, 0, 0, 0], [1, 2, 3])):
+    for starts, lens in (padded([0, 48, 49, 60], [48, 800, 333]), padded([0, 0, 0, 5], [10, 20, 700]), padded([0, 0, 0, 0], [1, 2, 3])):
         fresh = c.draw(rows, 8)
         q_d.copy_(fresh)
         starts_d.copy_(torch.tensor(starts, dtype=torch.int32))
@@ -881,7 +899,18 @@ def test_offsets_past_32_bits(tq):
         tq.tq_kv16_decode(cfg, turned[:2].contiguous(), cache, table, lens_d, 300, one, ws)
         many = torch.empty((377, n_q, 128), dtype=torch.float32, device="cuda")
         tq.tq_kv16_continue(cfg, turned, starts, 300, cache, table, lens_d, 300, many, ws)
-        results.append((cache[base * bb:].clone(), turned, one, many))
+        # the same where a decode is the line's, and where a unit is one CTA's
+        more = 40
+        wide = torch.cat([table, table[:1].repeat(more, 1)])
+        lens_w = torch.cat([lens_d, lens_d[:1].repeat(more)])
+        starts_w = torch.cat([starts, starts[-1:].repeat(more)])
+        ws = torch.empty(max(tq.tq_kv16_decode_workspace_size(cfg, 42, 300), tq.tq_kv16_continue_workspace_size(cfg, 42, 377, 300, 300)),
+                         dtype=torch.uint8, device="cuda")
+        line = torch.empty((42, n_q, 128), dtype=torch.float32, device="cuda")
+        tq.tq_kv16_decode(cfg, turned[:42].contiguous(), cache, wide, lens_w, 300, line, ws)
+        alone = torch.empty((377, n_q, 128), dtype=torch.float32, device="cuda")
+        tq.tq_kv16_continue(cfg, turned, starts_w, 300, cache, wide, lens_w, 300, alone, ws)
+        results.append((cache[base * bb:].clone(), turned, one, many, line, alone))
     for x, y in zip(*results):
         assert torch.equal(x, y)
 
@@ -956,16 +985,17 @@ def test_calls_in_a_context_after_the_first(tq, how):
 # ---------------------------------------------------------------- together
 
 
+@pytest.mark.parametrize("prompts,chunk", [([37, 150, 1], 64), ([700, 1, 433], 256)])
 @pytest.mark.parametrize("dtype,block,style", [("bf16", 16, "halves"), ("fp16", 128, "pairs")])
-def test_prompts_then_steps(tq, dtype, block, style):
+def test_prompts_then_steps(tq, dtype, block, style, prompts, chunk):
     """A batch served as a program would: prompts appended and attended in chunks,
     then decode steps (append, then decode, one captured graph replayed), queries
     rotated in place in one projection's output; attention against the cache as the
     GPU holds it, which is checked against the rotation and the places."""
     n_q, n_kv, steps = 8, 2, 20
-    prompts = [37, 150, 1]
+    most = max(prompts) + steps
     c = Case(tq, dtype, block, n_q, n_kv, [p + steps for p in prompts], seed=50)
-    angles = angle_table(200, 128)
+    angles = angle_table(most, 128)
     turn = torch.from_numpy(angles).cuda()
     cache, table, _ = c.gpu()
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -976,28 +1006,28 @@ def test_prompts_then_steps(tq, dtype, block, style):
         c.cache = cache.cpu().numpy()
 
     done = [0, 0, 0]
-    while any(d < p for d, p in zip(done, prompts)):                 # chunks of at most 64 tokens
-        q_lens = [min(64, p - d) for d, p in zip(done, prompts)]
+    while any(d < p for d, p in zip(done, prompts)):
+        q_lens = [min(chunk, p - d) for d, p in zip(done, prompts)]
         done = [d + n for d, n in zip(done, q_lens)]
         starts = starts_of(q_lens)
         fused = c.draw(int(starts[-1]), n_q + 2 * n_kv, outlier=True)
         dev, lens_d, starts_d = fused.cuda(), torch.tensor(done, dtype=torch.int32, device="cuda"), torch.from_numpy(starts).cuda()
         q, k, v = dev[:, :n_q], dev[:, n_q:n_q + n_kv], dev[:, n_q + n_kv:]
         out = torch.empty((fused.shape[0], n_q, 128), dtype=torch.float32, device="cuda")
-        ws = torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, 3, fused.shape[0], 64, 200), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, 3, fused.shape[0], chunk, most), dtype=torch.uint8, device="cuda")
         tq.tq_kv16_append(c.cfg, k, v, starts_d, cache, table, lens_d, cos_sin=turn, style=style, q=q, q_out=q, dev_status=status)
-        tq.tq_kv16_continue(c.cfg, q, starts_d, 64, cache, table, lens_d, 200, out, ws, dev_status=status)
+        tq.tq_kv16_continue(c.cfg, q, starts_d, chunk, cache, table, lens_d, most, out, ws, dev_status=status)
         after(fused, starts, done, q)
         check_continue(c, q.cpu(), out.cpu().numpy().astype(np.float64), starts, done, "f32", rows=6)
     fused_d = torch.empty((3, n_q + 2 * n_kv, 128), dtype=DT[dtype], device="cuda")
     lens_d, starts_d = torch.zeros(3, dtype=torch.int32, device="cuda"), torch.arange(4, dtype=torch.int32, device="cuda")
     out = torch.empty((3, n_q, 128), dtype=torch.float32, device="cuda")
-    ws = torch.empty(tq.tq_kv16_decode_workspace_size(c.cfg, 3, 200), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(tq.tq_kv16_decode_workspace_size(c.cfg, 3, most), dtype=torch.uint8, device="cuda")
     q, k, v = fused_d[:, :n_q], fused_d[:, n_q:n_q + n_kv], fused_d[:, n_q + n_kv:]
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         tq.tq_kv16_append(c.cfg, k, v, starts_d, cache, table, lens_d, cos_sin=turn, style=style, q=q, q_out=q, dev_status=status)
-        tq.tq_kv16_decode(c.cfg, q, cache, table, lens_d, 200, out, ws, dev_status=status)
+        tq.tq_kv16_decode(c.cfg, q, cache, table, lens_d, most, out, ws, dev_status=status)
     for step in range(steps):
         done = [d + 1 for d in done]
         fused = c.draw(3, n_q + 2 * n_kv, outlier=True)

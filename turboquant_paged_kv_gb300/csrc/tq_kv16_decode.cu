@@ -5,7 +5,8 @@
 // Work split: the line of all (sequence, KV head) pairs' tiles (tq_line.cuh), cut
 // evenly over the warps of a grid of one CTA per SM, and a merge of the warps'
 // records. A warp copies its own tiles, one bulk copy of 8192 bytes each into a
-// ring of its own, and waits on that copy's barrier.
+// ring of its own, and waits on that copy's barrier. Short work takes one launch
+// instead (kv16_short_kernel), and so do few queries of chunks.
 //
 // Math, per tile of 16 positions x 128 coordinates, on mma.sync.m16n8k16 in the
 // cache's type with fp32 sums:
@@ -19,6 +20,12 @@
 // Both operands come by ldmatrix (the values transposed); the cache's swizzle keeps
 // its rows in different banks. Softmax in log2 units, the running maximum moving
 // only when a score passes it by 2^8 (one warp vote a tile).
+//
+// Bound: memory, the cache being read once. 64 x 512-16384, 8 KV heads: 361 us, 6.63 TB/s
+// of 2.39 GB (0.98 of a measured copy); 4 x 131072, 4 KV heads: 336, 6.38; 32 x 4096: 91,
+// 5.9 (77 % of DRAM's cycles, tensor cores busy for 9 %), of which 4 to 5 us are the start
+// (lengths, table, first tiles, one after another) and 3 the merge; 1 x 301 in one launch
+// 5.1, a chain of those loads, the tiles and the cluster's merge.
 #include <climits>
 
 #include "tq_attn.cuh"
@@ -29,8 +36,11 @@
 namespace tq {
 namespace {
 
-constexpr int kWarps = 13;         // a CTA
-constexpr int kStages = 2;         // tiles in a warp's ring
+// Warps a CTA and tiles in a warp's ring; 32 x 4096, 64 x 512-16384, 4 x 131072: 13 x 2 91.0, 361, 338 us; 9 x 3 92.5, 381,
+// 337; 8 x 3 93.6, 378, 340; 7 x 4 94.7, 393, 364; 6 x 4 96, 386, 358. All of shared memory in each, so nearly as much asked
+// for at once: more warps share the products, which come between a tile and the next one's request.
+constexpr int kWarps = 13;
+constexpr int kStages = 2;
 constexpr int kMaxCtas = 256;      // grid cap: sizes the workspace without a device query
 constexpr int kMaxWarps = 4096;    // partial records beside one per pair
 constexpr int kSmem = kWarps * kStages * (kKvTileBytes + 8) + 128;   // and room to align to 128
@@ -339,7 +349,8 @@ __device__ __forceinline__ int row_of_chunk(const Kv16RowsArgs& a, int row, int 
 
 // Short work in one launch: a cluster of up to 8 CTAs per (sequence, KV head) pair, its
 // tiles dealt to their warps in turn; what the warps hold is merged in shared memory,
-// then what the CTAs hold, each CTA a part of the output.
+// then what the CTAs hold, each CTA a part of the output. Measured against the split
+// and the merge, or the chunks' kernel: see kShortMost here and in tq_kv16_continue.cu.
 template <typename T, typename TO, bool WIDE>
 __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const Kv16RowsArgs a) {
   constexpr int kParts = std::is_same<T, __nv_bfloat16>::value && std::is_same<TO, float>::value ? 3 : 2;
@@ -388,7 +399,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
   };
   for (int i = 0; i < kShortStages && i < todo; ++i) put(i);
   Heads<T, WIDE, kParts> heads;
-  heads.begin(static_cast<const T*>(a.q) + row * a.q_stride + h * a.group * kKvD, a.group, lane);
+  heads.begin(static_cast<const T*>(a.q) + row * a.q_stride + h * a.group * kKvD, ours ? a.group : 0, lane);
   unsigned phases = 0;   // a barrier's parity
   bool ok = true;
   for (int i = 0; i < todo; ++i) {
