@@ -448,16 +448,18 @@ def _kv16_block_bytes(preset: int, head_dim: int, block_size: int, num_kv_heads:
 _KV16_TYPES = {TQ_PRESET_KV_BF16: torch.bfloat16, TQ_PRESET_KV_F16: torch.float16}
 
 
-def _kv16_rows(name: str, t: torch.Tensor, kind: torch.dtype, heads: int, d: int) -> int:
-    """As _b8_rows, of the cache's own type (which it looks at first: the usual call is over at once)."""
-    if t.dtype is kind and t.dim() == 3:
-        _, have, last = t.shape
-        s0, s1, s2 = t.stride()
-        if have == heads and last == d and s2 == 1 and s1 == d and s0 >= heads * d and s0 % 8 == 0:
-            return s0
+def _kv16_rows(name: str, t: torch.Tensor, kind: torch.dtype, heads: int, d: int) -> tuple:
+    """As _b8_rows, of the cache's own type (which it looks at first: the usual call is over at once). Returns the
+    number of rows and their stride."""
     if t.dtype is not kind:
         raise ValueError(f"{name} must have the cache's type, got {t.dtype}")
-    return _b8_rows(name, t, heads, d)
+    shape = t.shape
+    if len(shape) == 3:
+        rows, have, last = shape
+        s0, s1, s2 = t.stride()
+        if have == heads and last == d and s2 == 1 and s1 == d and s0 >= heads * d and s0 % 8 == 0:
+            return rows, s0
+    return shape[0] if len(shape) else 0, _b8_rows(name, t, heads, d)
 
 
 def _kv16_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -468,10 +470,13 @@ def _kv16_common(cfg: tq_config, cache: torch.Tensor, num_blocks, block_table: t
             and seq_lens.is_contiguous() and seq_lens.dim() == 1):
         rows, width = block_table.shape
         dev = cache.get_device()
-        if (rows >= seq_lens.shape[0] and dev >= 0 and block_table.get_device() == dev and seq_lens.get_device() == dev
-                and all([t is None or t.get_device() == dev for t in others]) and dev == torch.cuda.current_device()):
-            return (cache.numel() // _kv16_block_bytes(cfg.preset, cfg.head_dim, cfg.block_size, cfg.num_kv_heads), width,
-                    torch._C._cuda_getCurrentRawStream(dev))
+        if rows >= seq_lens.shape[0] and dev >= 0 and dev == torch._C._cuda_getDevice():   # what current_device() asks
+            for t in (block_table, seq_lens, *others):
+                if t is not None and t.get_device() != dev:
+                    break
+            else:
+                return (cache.numel() // _kv16_block_bytes(cfg.preset, cfg.head_dim, cfg.block_size, cfg.num_kv_heads), width,
+                        torch._C._cuda_getCurrentRawStream(dev))
     return _b8_common(cfg, cache, num_blocks, block_table, seq_lens, others, stream, _kv16_block_bytes)
 
 
@@ -499,25 +504,26 @@ def tq_kv16_append(cfg: tq_config, key: torch.Tensor, value: torch.Tensor, query
     `style` says, "halves" or "pairs"; None: no rotation. q [total_q, n_q, d] is
     rotated into q_out (which may be q). Rows may be a stride apart."""
     kind, heads, d = _kv16_type(cfg), cfg.num_kv_heads, cfg.head_dim
-    ks = _kv16_rows("key", key, kind, heads, d)
-    vs = _kv16_rows("value", value, kind, heads, d)
-    rows = key.shape[0]
-    if value.shape[0] != rows:
+    rows, ks = _kv16_rows("key", key, kind, heads, d)
+    same, vs = _kv16_rows("value", value, kind, heads, d)
+    if same != rows:
         raise ValueError("key and value must have one number of rows")
     qs = os_ = rot = positions = 0
     q_at = out_at = angles = None
     if q is not None or q_out is not None:
         if q is None or q_out is None:
             raise ValueError("q and q_out must be given together")
-        qs = _kv16_rows("q", q, kind, cfg.num_q_heads, d)
-        os_ = _kv16_rows("q_out", q_out, kind, cfg.num_q_heads, d)
-        if q.shape[0] != rows or q_out.shape[0] != rows:
+        heads = cfg.num_q_heads
+        same, qs = _kv16_rows("q", q, kind, heads, d)
+        those, os_ = _kv16_rows("q_out", q_out, kind, heads, d)
+        if same != rows or those != rows:
             raise ValueError("q, q_out and key must have one number of rows")
         q_at, out_at = q.data_ptr(), q_out.data_ptr()
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+        shape = cos_sin.shape
+        if cos_sin.dtype != torch.float32 or len(shape) != 2 or not cos_sin.is_contiguous():
             raise ValueError("cos_sin must be a contiguous float32 matrix [positions, rot_dim]")
-        positions, rot = cos_sin.shape
+        positions, rot = shape
         if rot == 0:
             raise ValueError("cos_sin must have columns (None: no rotation)")
         angles = cos_sin.data_ptr()
@@ -543,13 +549,13 @@ def tq_kv16_decode(cfg: tq_config, q: torch.Tensor, cache: torch.Tensor, block_t
                    scale: float = 0.0, num_blocks: int | None = None, dev_status: torch.Tensor | None = None,
                    stream=None) -> None:
     """q [B, n_q, d] of the cache's type (rows may be a stride apart); out [B, n_q, d]; seq_lens [B] int32."""
-    qs = _kv16_rows("q", q, _kv16_type(cfg), cfg.num_q_heads, cfg.head_dim)
+    rows, qs = _kv16_rows("q", q, _kv16_type(cfg), cfg.num_q_heads, cfg.head_dim)
     out_type = _b8_out("out", out, q.shape)
-    if q.shape[0] != seq_lens.shape[0]:
+    if rows != seq_lens.shape[0]:
         raise ValueError("q must have one row per sequence")
     nb, width, raw = _kv16_common(cfg, cache, num_blocks, block_table, seq_lens, (q, out, workspace, dev_status), stream)
     st = _kv16_fn("tq_kv16_decode")(cfg, q.data_ptr(), qs, cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(),
-                             q.shape[0], max_seq_len, scale, out.data_ptr(), out_type, workspace.data_ptr(),
+                             rows, max_seq_len, scale, out.data_ptr(), out_type, workspace.data_ptr(),
                              _b8_workspace(workspace), _b8_status(dev_status), raw)
     if st:
         raise TQError("tq_kv16_decode", st)
@@ -567,11 +573,11 @@ def tq_kv16_continue(cfg: tq_config, q: torch.Tensor, query_start: torch.Tensor,
     n_q, d] of the cache's type (rows may be a stride apart), query_start int32
     [batch + 1], seq_lens int32 [batch] (lengths with the chunk), out [total_q,
     n_q, d]; rows of out from query_start[batch] on are left as they are."""
-    qs = _kv16_rows("q", q, _kv16_type(cfg), cfg.num_q_heads, cfg.head_dim)
+    rows, qs = _kv16_rows("q", q, _kv16_type(cfg), cfg.num_q_heads, cfg.head_dim)
     out_type = _b8_out("out", out, q.shape)
     _b8_starts(query_start, seq_lens)
     nb, width, raw = _kv16_common(cfg, cache, num_blocks, block_table, seq_lens, (q, query_start, out, workspace, dev_status), stream)
-    st = _kv16_fn("tq_kv16_continue")(cfg, q.data_ptr(), qs, query_start.data_ptr(), seq_lens.shape[0], q.shape[0], max_q_len,
+    st = _kv16_fn("tq_kv16_continue")(cfg, q.data_ptr(), qs, query_start.data_ptr(), seq_lens.shape[0], rows, max_q_len,
                                cache.data_ptr(), nb, block_table.data_ptr(), width, seq_lens.data_ptr(), max_seq_len, scale,
                                out.data_ptr(), out_type, workspace.data_ptr(), _b8_workspace(workspace), _b8_status(dev_status), raw)
     if st:
