@@ -84,6 +84,11 @@ constexpr int kPairRows = 256;
 // 19.3, 3 x 7 over 400 of 8 (4, two rounds) 10.1 for 12.9, 4 x 5 over 1000 (8, two rounds) 14.9 for 15.0, 1 x 16 over 4000
 // (31) 20.9 for 17.9, 8 x 5 over 500 (4, three rounds) 16.3 for 15.1
 constexpr int kShortMost = 22;
+// Steps of the longest history up to which units are not cut: so many are done while records are written and merged. (One
+// chunk of 416 over 445, 3 heads: 16.4 us whole, 19.7 cut; 4 of 50-150 over 97-391, 6 heads of 8: 19.7 and 26.2; 7 of 40-120
+// over 218-872, one head: 18.0 and 19.5; with 12: 2 of 364-1093 over few, 4 heads: 25.6, with 8 22.1.)
+constexpr int kNoSplit = 8;
+constexpr int kMergeThreads = 256, kMergeCtas = 3;   // an SM, of the merge: with 8 (2.7 waves of what fits) 32 x 128 takes 208 us for 197
 constexpr unsigned long long kStepNs = 100000;     // what a step may take, where a wait is for many
 
 struct ChunkArgs {
@@ -901,73 +906,117 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
   }
 }
 
-// Merges the parts of split units, most often two: a warp 4 rows of two parts at once,
-// 32 rows a CTA; where there are more, a warp a row, eight parts at once, 8 rows a CTA.
+// Merges the parts of split units. A warp takes a row, two or four at a time, by 8 loads
+// of records at once: four rows of two parts, two of up to four, one of eight. What there
+// is of that is dealt evenly to the warps of a grid of kMergeCtas CTAs an SM, which are
+// resident at once. (CTAs for 8 rows of every team's unit, split or whole, 4864 of them
+// that mostly found nothing to do, took 10 us: 4 chunks of 190-572 queries and few heads
+// 34.6 us for 30.0, 2 of 430-1291 23.0 for 21.6. CTAs for 32 rows were slow where there
+// are many parts: the latter 26.8.)
 template <typename TO>
-__global__ void __launch_bounds__(256) kv16_chunk_merge_kernel(const ChunkArgs a) {
+struct Merge {
+  const ChunkArgs& a;
+  int u, lane;
+  int4 unit;   // first row, rows, first head, parts
+  template <int ROWS, int PARTS>
+  __device__ __forceinline__ void rows(int row0) const {
+    static_assert(ROWS * PARTS == 8, "loads");
+    const int end = unit.y, parts = unit.w;
+    float m[ROWS], l[ROWS];
+    float4 o[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+      o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int z0 = 0; z0 < parts; z0 += PARTS) {
+      float lse[ROWS][PARTS];
+      float4 x[ROWS][PARTS];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+          const int z = z0 + k;
+          const bool in = z < parts && row0 + r < end;
+          const long long rec = static_cast<long long>(z == 0 ? 2 * u + 1 : 2 * (u + z)) * a.part_rows + row0 + r;
+          lse[r][k] = in ? ld_dep_f32(a.rec_lse + rec) : -INFINITY;
+          x[r][k] = in ? ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kKvD) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+          if (lse[r][k] == -INFINITY) continue;   // nothing seen there
+          const float top = fmaxf(m[r], lse[r][k]);
+          const float e = m[r] == -INFINITY ? 0.f : exp2f(m[r] - top), f = exp2f(lse[r][k] - top);
+          m[r] = top;
+          l[r] = l[r] * e + f;
+          o[r].x = o[r].x * e + x[r][k].x * f;
+          o[r].y = o[r].y * e + x[r][k].y * f;
+          o[r].z = o[r].z * e + x[r][k].z * f;
+          o[r].w = o[r].w * e + x[r][k].w * f;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int row = row0 + r;
+      if (row >= end) break;
+      const float s = l[r] == 0.f ? 0.f : 1.f / l[r];
+      const long long orow = (static_cast<long long>(unit.x) + row / a.group) * a.n_q + unit.z + row % a.group;
+      write4<TO>(static_cast<TO*>(a.out) + orow * kKvD + 4 * lane, make_float4(o[r].x * s, o[r].y * s, o[r].z * s, o[r].w * s));
+    }
+  }
+};
+// Rows that a warp takes at once of a unit of so many parts.
+__device__ __forceinline__ int rows_at_once(int parts) { return parts == 2 ? 4 : parts <= 4 ? 2 : 1; }
+template <typename TO>
+__global__ void __launch_bounds__(kMergeThreads, kMergeCtas) kv16_chunk_merge_kernel(const ChunkArgs a, int teams) {
+  constexpr int kGroups = (kCtas + 31) / 32;
+  static_assert(kGroups <= kMergeThreads / 32, "a warp a group of units");
+  __shared__ int4 s_unit[kGroups * 32];
+  __shared__ int s_end[kGroups * 32];   // pieces of work up to the unit's end, of its group of 32
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_unit = (a.part_rows + 7) / 8;
-  const int u = blockIdx.x / per_unit, at = blockIdx.x - u * per_unit;
   grid_dep_wait();
   grid_dep_launch();
-  const uint4 unit = ld_dep_u32x4(a.split_units + u);   // first row, rows, first head, parts
-  const int rows = unit.y, parts = unit.w;
-  if (parts == 0 || (parts == 2 && (at & 3))) return;
-  const int row0 = 8 * at + (parts == 2 ? 4 * warp : warp);
-  if (row0 >= rows) return;
-  auto record = [&](int z, int r) { return static_cast<long long>(z == 0 ? 2 * u + 1 : 2 * (u + z)) * a.part_rows + r; };
-  auto put = [&](int r, float4 o) {
-    const long long orow = (static_cast<long long>(unit.x) + r / a.group) * a.n_q + unit.z + r % a.group;
-    write4<TO>(static_cast<TO*>(a.out) + orow * kKvD + 4 * lane, o);
-  };
-  if (parts == 2) {
-    float lse[8];
-    float4 x[8];
+  if (warp < kGroups) {
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (static_cast<int>(threadIdx.x) < teams) x = ld_dep_u32x4(a.split_units + threadIdx.x);
+    const int4 unit = make_int4(x.x, x.y, x.z, x.w);
+    const int each = rows_at_once(unit.w);
+    int inc = unit.w ? (unit.y + each - 1) / each : 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const bool in = row0 + (k >> 1) < rows;
-      const long long rec = record(k & 1, in ? row0 + (k >> 1) : row0);
-      lse[k] = ld_dep_f32(a.rec_lse + rec);
-      x[k] = ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kKvD) + lane);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-#pragma unroll
-    for (int k = 0; k < 8; k += 2) {
-      if (row0 + (k >> 1) >= rows) break;
-      // nothing seen: a log2-sum of -infinity, zeros in the record
-      const float top = fmaxf(lse[k], lse[k + 1]);
-      const float e = lse[k] == -INFINITY ? 0.f : exp2f(lse[k] - top), f = lse[k + 1] == -INFINITY ? 0.f : exp2f(lse[k + 1] - top);
-      const float s = e + f == 0.f ? 0.f : 1.f / (e + f);
-      put(row0 + (k >> 1), make_float4((x[k].x * e + x[k + 1].x * f) * s, (x[k].y * e + x[k + 1].y * f) * s,
-                                       (x[k].z * e + x[k + 1].z * f) * s, (x[k].w * e + x[k + 1].w * f) * s));
-    }
-    return;
+    s_unit[threadIdx.x] = unit;
+    s_end[threadIdx.x] = inc;
   }
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int z0 = 0; z0 < parts; z0 += 8) {
-    float lse[8];
-    float4 x[8];
+  __syncthreads();
+  int end[kGroups], total = 0;   // of this lane's unit of each group
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const long long rec = record(z0 + k, row0);
-      lse[k] = z0 + k < parts ? ld_dep_f32(a.rec_lse + rec) : -INFINITY;
-      x[k] = z0 + k < parts ? ld_dep_f32x4(reinterpret_cast<const float4*>(a.rec_o + rec * kKvD) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (lse[k] == -INFINITY) continue;   // nothing seen there
-      const float top = fmaxf(m, lse[k]);
-      const float e = m == -INFINITY ? 0.f : exp2f(m - top), f = exp2f(lse[k] - top);
-      m = top;
-      l = l * e + f;
-      o.x = o.x * e + x[k].x * f;
-      o.y = o.y * e + x[k].y * f;
-      o.z = o.z * e + x[k].z * f;
-      o.w = o.w * e + x[k].w * f;
-    }
+  for (int k = 0; k < kGroups; ++k) {
+    end[k] = total + s_end[32 * k + lane];
+    total += s_end[32 * k + 31];
   }
-  const float s = l == 0.f ? 0.f : 1.f / l;
-  put(row0, make_float4(o.x * s, o.y * s, o.z * s, o.w * s));
+  for (int i = warp * gridDim.x + blockIdx.x; i < total; i += gridDim.x * (kMergeThreads / 32)) {
+    int u = 0;   // units that end before piece i
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) u += __popc(__ballot_sync(0xffffffffu, end[k] <= i));
+    int before = 0;
+#pragma unroll
+    for (int k = 0; k < kGroups; ++k) {
+      const int all = __shfl_sync(0xffffffffu, end[k], (u - 1) & 31);
+      if ((u - 1) >> 5 == k) before = all;
+    }
+    const int4 unit = s_unit[u];
+    const int row = (i - before) * rows_at_once(unit.w);
+    const Merge<TO> merge = {a, u, lane, unit};
+    if (unit.w == 2) merge.template rows<4, 2>(row);
+    else if (unit.w <= 4) merge.template rows<2, 4>(row);
+    else merge.template rows<1, 8>(row);
+  }
 }
 
 // The grid, and the workspace that split units take.
@@ -989,7 +1038,7 @@ Plan plan_for(const tq_config* cfg, int batch, int total_q, int max_q_len, int m
   long long tiles = static_cast<long long>(total_q) / per + (batch < total_q ? batch : total_q);
   if (tiles > most) tiles = most;
   p.units = tiles * cfg->num_kv_heads;
-  p.may_split = p.units > 0 && max_seq_len > 3 * kCols;   // three steps are done before a second kernel is
+  p.may_split = p.units > 0 && max_seq_len > kNoSplit * kCols;
   p.part_rows = longest < per ? longest * group : per * group;
   const size_t records = static_cast<size_t>(2 * kCtas / p.ctas) * p.part_rows;
   p.workspace = p.may_split ? (kCtas * sizeof(int4) + records * (kKvD + 1) * sizeof(float) + 15) / 16 * 16 : 16;
@@ -1010,7 +1059,7 @@ cudaError_t launch(const ChunkArgs& a, const Plan& p, cudaStream_t s) {
   if (CTAS == 2) err = launch_pdl_cluster(kv16_chunk_kernel<T, TO, CTAS>, dim3(2 * teams), dim3(kThreads), 2, kSmem, s, a);
   else err = launch_pdl(kv16_chunk_kernel<T, TO, CTAS>, dim3(teams), dim3(kThreads), kSmem, s, a);
   if (err != cudaSuccess || !p.may_split) return err;
-  return launch_pdl(kv16_chunk_merge_kernel<TO>, dim3(teams * ((p.part_rows + 7) / 8)), dim3(256), 0, s, a);
+  return launch_pdl(kv16_chunk_merge_kernel<TO>, dim3(kMergeCtas * most * CTAS), dim3(kMergeThreads), 0, s, a, teams);
 }
 template <typename T, typename TO>
 cudaError_t launch(const ChunkArgs& a, const Plan& p, cudaStream_t s) {
