@@ -427,13 +427,15 @@ def test_decode_few_and_empty_sequences(tq, dtype, lens, line):
     check_decode(c, q, run_decode(c, q, line=line), "f32")
 
 
-def test_decode_many_sequences(tq):
-    """More (sequence, head) pairs than warps, most of them one tile long."""
+@pytest.mark.parametrize("batch,n_kv,group,dtype,out,most", [
+    (1500, 2, 2, "bf16", "f32", 20), (777, 1, 5, "fp16", "bf16", 20), (199, 3, 7, "bf16", "fp16", 300), (300, 1, 3, "fp16", "f32", 200)])
+def test_decode_many_sequences(tq, batch, n_kv, group, dtype, out, most):
+    """More (sequence, head) pairs than warps, most of them one tile long; heads merged by a warp each, and (the last) by a CTA each."""
     rng = np.random.default_rng(8)
-    lens = [int(x) for x in rng.integers(0, 20, 1500)]
-    c = Case(tq, "bf16", 16, 4, 2, [max(x, 1) for x in lens], seed=8).fill(lens)
-    q = c.draw(len(lens), 4)
-    check_decode(c, q, run_decode(c, q), "f32")
+    lens = [int(x) for x in rng.integers(0, most, batch)]
+    c = Case(tq, dtype, 16, n_kv * group, n_kv, [max(x, 1) for x in lens], seed=8).fill(lens)
+    q = c.draw(len(lens), n_kv * group)
+    check_decode(c, q, run_decode(c, q, out_dtype=out), out)
 
 
 @pytest.mark.parametrize("lens", [[50, 20], [50, 20, 0, 33] * 40])      # one launch, or the split and the merge

@@ -51,6 +51,10 @@ constexpr int kShortSmem = kShortWarps * kShortStages * (kKvTileBytes + 8) + 128
 // 16 x 1024 of 8 heads (8 tiles) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9, 32 x 1200 (10, two rounds) 29.1 for
 // 31.6, 20 x 1000 (8, two rounds) 20.4 for 20.1, 64 x 100 (1, four rounds) 15.7 for 14.9
 constexpr int kShortMost = 35;
+// From more query heads than kManyHeads on, of at most kFewRecords records each, a warp merges one rather than a CTA:
+// 128 x 1000-3000 of 64 heads (1024 pairs, 3 records) 178 us for 195, 118 x 0-12 of 48 10.4 for 21.6, 48 x 300-900 of 32 (7
+// records) 24.2 for 25.2; 100 x 500-5000 of 8 heads 182.5 for 181, 26 x 1000-9000 of 48 (14 records) 73.7 for 68.9
+constexpr int kManyHeads = 152 * 8, kFewRecords = 8;
 constexpr float kStep = 8.f;       // the running maximum moves in steps of at least this, log2 units
 static_assert(kMaxCtas * kWarps <= kMaxWarps, "workspace");
 
@@ -519,6 +523,12 @@ cudaError_t launch_short(const Kv16RowsArgs& a, int out_dtype, int ctas, int dev
   return a.group > 4 ? launch_short<T, __nv_bfloat16, true>(a, ctas, dev, s) : launch_short<T, __nv_bfloat16, false>(a, ctas, dev, s);
 }
 
+template <typename TO>
+cudaError_t merge(const Kv16RowsArgs& a, long long records_each, cudaStream_t s) {
+  const bool many = static_cast<long long>(a.rows) * a.n_q > kManyHeads && records_each <= kFewRecords;
+  return many ? launch_merge_of<TO, 1, 8>(a, s) : launch_merge<TO>(a, records_each, s);
+}
+
 size_t split_workspace(const tq_config* cfg, long long rows) {
   const int group = cfg->num_q_heads / cfg->num_kv_heads;
   const size_t records = static_cast<size_t>(rows) * cfg->num_kv_heads + kMaxWarps;
@@ -546,9 +556,9 @@ cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* work
   // records of a pair, if the lengths are alike: all of them in one round of loads
   long long records_each = a.warps / pairs + 2;
   if (records_each > tiles) records_each = tiles;
-  if (out_dtype == TQ_DTYPE_F32) return launch_merge<float>(a, records_each, s);
-  if (out_dtype == TQ_DTYPE_F16) return launch_merge<__half>(a, records_each, s);
-  return launch_merge<__nv_bfloat16>(a, records_each, s);
+  if (out_dtype == TQ_DTYPE_F32) return merge<float>(a, records_each, s);
+  if (out_dtype == TQ_DTYPE_F16) return merge<__half>(a, records_each, s);
+  return merge<__nv_bfloat16>(a, records_each, s);
 }
 
 }  // namespace

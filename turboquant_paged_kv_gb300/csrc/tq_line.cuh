@@ -109,15 +109,18 @@ __device__ __forceinline__ Place find_tile(const Args& a, long long x, int lane,
   return p;
 }
 
-// A CTA of WARPS warps per (sequence, query head): the records of the pair are
-// those of the warps whose parts of the line meet it; warp k takes every
-// WARPS-th one, four at a time, a lane 4 coordinates.
-template <typename TO, int WARPS, typename Args>
-__global__ void __launch_bounds__(WARPS * 32) line_merge_kernel(const Args a) {
+// WARPS warps per (sequence, query head), HEADS of these a CTA (several: of one warp
+// each): the records of the pair are those of the warps whose parts of the line meet it;
+// warp k takes every WARPS-th one, four at a time, a lane 4 coordinates.
+template <typename TO, int WARPS, int HEADS, typename Args>
+__global__ void __launch_bounds__(WARPS * HEADS * 32) line_merge_kernel(const Args a) {
+  static_assert(WARPS == 1 || HEADS == 1, "warps of one head meet at the CTA's barrier");
   __shared__ float s_m[WARPS], s_l[WARPS];
   __shared__ float4 s_o[WARPS][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x / a.n_q, qh = blockIdx.x - row * a.n_q;
+  const int warp = HEADS > 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int index = HEADS > 1 ? blockIdx.x * HEADS + (threadIdx.x >> 5) : blockIdx.x;
+  const int row = index / a.n_q, qh = index - row * a.n_q;
+  if (HEADS > 1 && row >= a.rows) return;
   const int h = qh / a.group, gg = qh - h * a.group;
   // lengths and starts are not written by the split kernel, which let this
   // launch go only after its own wait: they may be read before this one's
@@ -170,13 +173,15 @@ __global__ void __launch_bounds__(WARPS * 32) line_merge_kernel(const Args a) {
       o.w = o.w * e + x[i].w * f;
     }
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+  if constexpr (WARPS > 1) {
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+    s_o[warp][lane] = o;
+    __syncthreads();
+    if (warp) return;
   }
-  s_o[warp][lane] = o;
-  __syncthreads();
-  if (warp) return;
 #pragma unroll
   for (int k = 1; k < WARPS; ++k) {
     const float mk = s_m[k];
@@ -195,15 +200,19 @@ __global__ void __launch_bounds__(WARPS * 32) line_merge_kernel(const Args a) {
   write4<TO>(out, make_float4(o.x * r, o.y * r, o.z * r, o.w * r));
 }
 
+template <typename TO, int WARPS, int HEADS = 1, typename Args>
+cudaError_t launch_merge_of(const Args& a, cudaStream_t s) {
+  const unsigned heads = static_cast<unsigned>(a.rows) * static_cast<unsigned>(a.n_q);
+  return launch_pdl(line_merge_kernel<TO, WARPS, HEADS, Args>, dim3((heads + HEADS - 1) / HEADS), dim3(WARPS * HEADS * 32), 0, s, a);
+}
 template <typename TO, typename Args>
 cudaError_t launch_merge(const Args& a, long long records_each, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.rows) * static_cast<unsigned>(a.n_q));
   // the whole decode of the 8-bit cache: 4 x 131072 (59 records) 170.3 us with 4 warps, 166.7 with 16; one sequence
   // of 301 (19 records) 6.39 with 4, 6.15 with 8; 32 x 4096 (9 records) 50.0 with 4, 51.5 with 8,
   // 57.3 with 16
-  if (records_each > 32) return launch_pdl(line_merge_kernel<TO, 16, Args>, grid, dim3(16 * 32), 0, s, a);
-  if (records_each > 16) return launch_pdl(line_merge_kernel<TO, 8, Args>, grid, dim3(8 * 32), 0, s, a);
-  return launch_pdl(line_merge_kernel<TO, 4, Args>, grid, dim3(4 * 32), 0, s, a);
+  if (records_each > 32) return launch_merge_of<TO, 16>(a, s);
+  if (records_each > 16) return launch_merge_of<TO, 8>(a, s);
+  return launch_merge_of<TO, 4>(a, s);
 }
 
 }  // namespace
