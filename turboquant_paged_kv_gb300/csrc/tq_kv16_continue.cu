@@ -57,6 +57,7 @@
 // products are issued (202 for 199), 5 stages for a pair (223 for 222 over seconds).
 #include <climits>
 
+#include "tq_attn.cuh"
 #include "tq_kv16.cuh"
 #include "tq_tc.cuh"
 
@@ -227,8 +228,8 @@ struct Line {
     // The step where a cut at x (within the unit) comes to be. Fewer than `least` steps from an end are not worth a record:
     // the cut moves there.
     __device__ int step_of(long long x, int least) const {
-      const long long s = (x - base) / each;
-      return s < min(least, steps) ? 0 : s > steps - least ? steps : static_cast<int>(s);
+      const int s = static_cast<int>(static_cast<unsigned>(x - base) / static_cast<unsigned>(each));   // x - base: at most a unit's cost
+      return s < min(least, steps) ? 0 : s > steps - least ? steps : s;
     }
   } at = {};
   int least = 1;
@@ -251,19 +252,13 @@ struct Line {
     const int s = steps_of(a, ch, j, per);
     return s ? static_cast<unsigned>(s) * each_of(j) + kUnit : 0u;
   }
-  // The unit of tile index j that place x of the 32 sequences' is in; they begin at `base`.
-  __device__ Unit locate(long long x, int j, long long base) {
-    const unsigned c = cost(j);
-    unsigned inc = c;   // at most 32 * (4 * 2^24 + 10)
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
+  // The unit of tile index j that place x of the 32 sequences' is in; they begin at `base`, and cost `c` each, `inc` up to
+  // and with their own.
+  __device__ Unit locate(long long x, int j, long long base, unsigned c, unsigned inc) {
     const int src = __ffs(__ballot_sync(0xffffffffu, x - base < static_cast<long long>(inc) * a.c.n_kv)) - 1;
     const unsigned here = __shfl_sync(0xffffffffu, c, src);
     base += static_cast<long long>(__shfl_sync(0xffffffffu, inc, src) - here) * a.c.n_kv;
-    const int h = static_cast<int>((x - base) / here);
+    const int h = static_cast<int>(divide(x - base, here));
     return {j, b0 + src, h, __shfl_sync(0xffffffffu, steps_of(a, ch, j, per), src), __shfl_sync(0xffffffffu, each_of(j), src),
             base + static_cast<long long>(h) * here};
   }
@@ -277,16 +272,28 @@ struct Line {
     for (int j = 0; j < tiles_most && !(found && ended); ++j) {
       for (int i = 0; i < a.batch; i += 32) {
         group(i);
-        const long long behind = before + static_cast<long long>(__reduce_add_sync(0xffffffffu, cost(j))) * a.c.n_kv;
-        if (!found && x0 < behind) {
-          found = true;
-          at = locate(x0, j, before);
-        }
-        if (!ended && x1 < behind) {
-          ended = true;
-          const Unit u = locate(x1, j, before);
-          last = u.base;
-          last_step = u.step_of(x1, least);
+        const unsigned c = cost(j);
+        const long long behind = before + static_cast<long long>(__reduce_add_sync(0xffffffffu, c)) * a.c.n_kv;
+        const bool first = !found && x0 < behind, final = !ended && x1 < behind;
+        if (first || final) {
+          unsigned inc = c;   // at most 32 * (4 * 2^24 + 10)
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          found |= first;
+          ended |= final;
+#pragma unroll 1   // (not unrolled: fetching the code is what takes time here)
+          for (int k = first ? 0 : 1; k < (final ? 2 : 1); ++k) {
+            const Unit u = locate(k ? x1 : x0, j, before, c, inc);
+            if (k) {
+              last = u.base;
+              last_step = u.step_of(x1, least);
+            } else {
+              at = u;
+            }
+          }
         }
         before = behind;
       }
@@ -372,11 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
   };
   // A wait for a whole part of `steps` steps.
   auto long_wait = [&](int b, uint32_t parity, int steps) {
-    const uint64_t t0 = global_ns(), most = kWaitNs + kStepNs * static_cast<uint64_t>(steps);
-    bool ok;
-    do {
-      ok = mbar_try(bar(b), parity);
-    } while (!ok && global_ns() - t0 < most);
+    bool ok = mbar_try(bar(b), parity);
+    if (!ok) {
+      const uint64_t t0 = global_ns(), most = kWaitNs + kStepNs * static_cast<uint64_t>(steps);
+      do {
+        ok = mbar_try(bar(b), parity);
+      } while (!ok && global_ns() - t0 < most);
+    }
     if (!ok) b8_flag(a.status, TQ_DEV_TIMEOUT);
     return __all_sync(0xffffffffu, ok) != 0;
   };
@@ -720,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     const long long cut = line.total / 5;   // one step and more a team
     const long long ctas = cut < 1 ? 1 : (cut < teams ? cut : teams);
     line.least = !a.may_split ? INT_MAX : line.total < 16ll * teams ? 1 : 2;
-    auto cut_of = [&](long long team_) { return line.total * team_ / ctas; };
+    auto cut_of = [&](long long team_) { return divide(line.total * team_, ctas); };
     int from = 0, last_step = 0;   // steps of the unit at hand that are done, or others'; and those up to which to go in the last unit
     long long last = 0;            // where that begins
     const bool works = team < ctas && line.total > 0;
@@ -770,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
           b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
         if (from == 0 && to < u.steps && speaks) {
           // the last team whose cut is in the unit, and stays there
-          long long owner = (u.behind() * ctas - 1) / line.total;
+          long long owner = divide(u.behind() * ctas - 1, line.total);
           while (owner > team && u.step_of(cut_of(owner), line.least) == u.steps) --owner;
           a.split_units[team] = make_int4(w.q0, w.rows, w.h * a.group, static_cast<int>(owner) - team + 1);
         }
@@ -878,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         const int qi = static_cast<int>(r * by_group >> 16);
         return static_cast<const T*>(a.q) + (q0 + qi) * a.q_stride + static_cast<long long>(head0 + r - qi * a.group) * kKvD;
       };
-      for (int k = threadIdx.x & 127; k < 2 * last; k += 128) {   // to L2, while the queries before are still in use
+      for (int k = threadIdx.x & 127; k < 2 * last && filled; k += 128) {   // to L2, while the queries before are still in use
         const int r = unit_row(k >> 1);
         if (r < rows) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(row_at(r) + 64 * (k & 1)));
       }

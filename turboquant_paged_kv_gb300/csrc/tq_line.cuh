@@ -75,12 +75,6 @@ __device__ __forceinline__ void count_tiles(const Args& a, int upto, int lane, l
   *too_long = __any_sync(0xffffffffu, tl);
 }
 
-// x / y; most lines are short enough for 32 bits.
-__device__ __forceinline__ long long divide(long long x, long long y) {
-  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-  return x / y;
-}
-
 // The place of tile x of the line (x < total).
 template <typename Args>
 __device__ __forceinline__ Place find_tile(const Args& a, long long x, int lane, const Rows& first) {
