@@ -44,15 +44,15 @@
 // TQ_DEV_TIMEOUT and ends the CTA, after its products and copies in flight.
 //
 // Bound: tensor cores by its operations. 4 chunks of 2001-2048 queries over 0-6144, 32
-// query heads, fp16: 533 us, 1590 TFLOP/s, 0.84 of a measured bf16 GEMM (603 us, 1407,
+// query heads, fp16: 540 us, 1570 TFLOP/s, 0.83 of a measured bf16 GEMM (592 us, 1432,
 // over seconds, where the power limit takes the clock to 1.7 GHz); 32 chunks of 128 over
-// 4096, bf16: 199 us, 1403 (212 us); 12 of 1-500 over 0-16384, 64 heads: 405 us, 1325.
+// 4096, bf16: 197 us, 1417 (212 us); 12 of 1-500 over 0-16384, 64 heads: 405 us, 1325.
 // A step of two tiles takes about 2800 cycles, 2304 of them products (64 a product,
 // 40 instead of 32 where only 64 positions stand against Q). Steps that led here, on the
 // second case: one CTA, a warp that issues for both tiles, S single 237 us; two threads a
 // row 236; pairs of CTAs 249, with S double 237; an issuing warp a tile 214; in turn, with
 // one barrier a load, 211; a line cut by cost, two-part merges 209; rows by way of shared
-// memory 202; queries asked for early 199. Tried and left out: S of the next half loaded
+// memory 202; queries asked for early 199; the merge dealt evenly 197. Tried and left out: S of the next half loaded
 // into registers before P is handed over (222 for 214), the turn given before the last
 // products are issued (202 for 199), 5 stages for a pair (223 for 222 over seconds).
 #include <climits>

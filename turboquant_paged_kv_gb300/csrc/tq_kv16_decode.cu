@@ -25,7 +25,7 @@
 // of 2.39 GB (0.98 of a measured copy); 4 x 131072, 4 KV heads: 336, 6.38; 32 x 4096: 91,
 // 5.9 (77 % of DRAM's cycles, tensor cores busy for 9 %), of which 4 to 5 us are the start
 // (lengths, table, first tiles, one after another) and 3 the merge; 1 x 301 in one launch
-// 5.1, a chain of those loads, the tiles and the cluster's merge.
+// 5.7, a chain of those loads, the tiles and the cluster's merge.
 #include <climits>
 
 #include "tq_attn.cuh"
