@@ -917,6 +917,42 @@ def test_offsets_past_32_bits(tq):
         assert torch.equal(x, y)
 
 
+def f32_error(c, q, got, seen):
+    """2-norm of the difference over that of the exact result, of rows that see `seen` positions of sequence 0."""
+    k, v = c.kv(0, max(seen))
+    ref = np.stack([o8.attend(q[i].double().numpy(), k[:n], v[:n], SCALE)[0] for i, n in enumerate(seen)])
+    return np.sqrt(np.square(got - ref).sum() / np.square(ref).sum())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_long_sums_in_f32(tq, dtype):
+    """The tensor cores cut off what they add to a sum, by half a step of it (2^-24 to 2^-23 of it) on average: 2^-25 of
+    the final sum, as the sums before are smaller, for each of the additions. A chunk's sums are of no more than 20 x 8
+    additions in 2 parts (320 2^-25), a decode's of 128 in 2 parts or 3 (384 2^-25); the scores' roundings and the
+    joining's come to less than half of that. Over 16384 positions in one sum it would be six times as much."""
+    n, rows = 16384 + 40, 400
+    c = Case(tq, dtype, 128, 8, 1, [n], seed=90).fill([n])
+    cache, table, _ = c.gpu()
+    batch = 24            # chunks of one sequence: units enough that most are whole
+    q = c.draw(64, 8)
+    dev = lambda x: torch.from_numpy(np.asarray(x, dtype=np.int32)).cuda()      # noqa: E731
+    for q_len in (64, 32):                                                      # a pair's units, and a CTA's
+        lens, starts = dev([n] * 8 * batch), dev(np.arange(8 * batch + 1) * q_len)
+        out = torch.empty((8 * batch * q_len, 8, 128), dtype=torch.float32, device="cuda")
+        ws = torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, 8 * batch, out.shape[0], q_len, n), dtype=torch.uint8, device="cuda")
+        tq.tq_kv16_continue(c.cfg, q[:q_len].cuda().repeat(8 * batch, 1, 1), starts, q_len, cache, table.repeat(8 * batch, 1), lens, n, out, ws)
+        got = out.view(8 * batch, q_len, 8, 128)
+        for b in (0, 95, 191):
+            pick = [0, q_len - 1]
+            assert f32_error(c, q[pick], got[b, pick].cpu().numpy().astype(np.float64), [n - q_len + 1 + i for i in pick]) < 320 * 2.0 ** -25 * 1.5
+    lens = dev([n] * rows)
+    out = torch.empty((rows, 8, 128), dtype=torch.float32, device="cuda")
+    ws = torch.empty(tq.tq_kv16_decode_workspace_size(c.cfg, rows, n), dtype=torch.uint8, device="cuda")
+    tq.tq_kv16_decode(c.cfg, q[:1].cuda().repeat(rows, 1, 1), cache, table.repeat(rows, 1), lens, n, out, ws)
+    for b in (0, 200, 399):
+        assert f32_error(c, q[:1], out[b:b + 1].cpu().numpy().astype(np.float64), [n]) < 384 * 2.0 ** -25 * 1.5
+
+
 _CONTEXT_CHILD = """
 import ctypes, importlib.util, sys
 import numpy as np

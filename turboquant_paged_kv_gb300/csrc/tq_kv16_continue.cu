@@ -28,7 +28,9 @@
 // by 2^-11 and no finer than 2^-25), as a 16-bit output is: against 64 bits, 2.3e-3
 // instead of the output's own 1.7e-3 in bf16, 2.9e-4 instead of 2.1e-4 in fp16. With
 // f32 output it is held in two parts (bf16 2^-16, fp16 2^-22), for twice the products
-// of P V.
+// of P V. The tensor cores cut what they add to O off rather than round it, about 2^-25 of
+// O each time: with f32 output no more than kPiece steps are summed there, and the pieces
+// of a unit joined in fp32 (against 64 bits, over 16384 positions: 6.5e-6, else 3.6e-5).
 //
 // A pair of CTAs shares one tile of keys and values (cta_group::2: each loads half of
 // the keys' positions and half of the values' coordinates). A CTA alone needs all of
@@ -73,7 +75,7 @@ constexpr uint32_t kTileOp = 32768;    // a 128 x 128 operand
 constexpr uint32_t kHalfQ = 16384;     // Q: two halves of 64 columns, 128 bytes a row
 constexpr uint32_t kStage = 32768;     // what is loaded at once: 16 KB of keys, then 16 KB of values
 // behind Q and the stages: room for a pair's output, or one more stage for one CTA, whose few rows wait for loads (32 x 5
-// queries over 4096: 102 us with 5 stages, 120 with 4)
+// queries over 4096: 102 us with 5 stages, 120 with 4; f32 output, which is read again by the next piece, has the room)
 constexpr uint32_t kOffLoads = 2 * kTileOp, kOffOut = kOffLoads + 4 * kStage, kOffBar = kOffOut + kStage;
 constexpr uint32_t kSmem = kOffBar + 512 + 1024;   // and room to align to 1024
 constexpr int kBad = 16;               // loads whose bad blocks are remembered (more than are between the loads and the softmax)
@@ -90,6 +92,7 @@ constexpr int kShortMost = 22;
 // over 218-872, one head: 18.0 and 19.5; with 12: 2 of 364-1093 over few, 4 heads: 25.6, with 8 22.1.)
 constexpr int kNoSplit = 8;
 constexpr int kMergeThreads = 256, kMergeCtas = 3;   // an SM, of the merge: with 8 (2.7 waves of what fits) 32 x 128 takes 208 us for 197
+constexpr int kPiece = 20;                         // steps; 32 x 128 over 4096, f32: 294 us, with 16 311, with 24 294, in one piece 276
 constexpr unsigned long long kStepNs = 100000;     // what a step may take, where a wait is for many
 
 struct ChunkArgs {
@@ -180,6 +183,7 @@ struct Work {
   int halves;          // of them, those that anybody sees
   int loads;           // that bring them: CTAS halves each
   int zero0, zeros;    // queries that nobody serves
+  int more, keep;      // this team's steps of the unit before tile0 are there already, where these come to be; the queries stay for the next part
   unsigned load0;      // loads of the CTA before
 };
 
@@ -326,7 +330,8 @@ struct Line {
 template <typename T, typename TO, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs a) {
   constexpr bool kTwo = std::is_same<TO, float>::value;   // P in two parts
-  constexpr int kStages = CTAS == 2 ? 4 : 5;
+  constexpr bool kStaged = CTAS == 2 || kTwo;   // output by way of shared memory
+  constexpr int kStages = kStaged ? 4 : 5;
   extern __shared__ uint8_t s_raw[];
   __shared__ uint32_t s_tmem;
   __shared__ Work s_work[2];
@@ -401,6 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_o = tmem + lanes + kColO + t * 128;
     const float f = fmaxf(a.qscale, 0x1p-126f);   // never 0, which would make NaN of a masked place
+    float seen = -INFINITY;       // the log2-sum of the row's pieces before
     unsigned n = 0, served = 0;   // halves of this tile so far (their S comes in that order), and parts
     int before = 0;
     bool ok = true;
@@ -541,17 +547,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       }
       if (!ok || !(ok = warp_wait(kODone0 + t, served++ & 1))) break;
       fence_after();
-      const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
+      float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);   // NaN stays
       const bool whole = w.slot < 0;
       const long long rec = static_cast<long long>(w.slot) * a.part_rows + r;
       auto row_of = [&](int q, int hd) { return (static_cast<long long>(w.q0 + q) * a.n_q + w.h * a.group + hd) * kKvD; };
+      float sum = l == 0.f ? -INFINITY : m - 3.f + __log2f(l), of_old = 0.f;   // the row's log2-sum; what its pieces before count
+      if constexpr (kTwo) {
+        if (w.more) {
+          const float top = fmaxf(seen, sum);
+          const float e = seen == -INFINITY ? 0.f : exp2f(seen - top), g = sum == -INFINITY ? 0.f : exp2f(sum - top);
+          const float all = e + g == 0.f ? 0.f : 1.f / (e + g);
+          sum = e + g == 0.f ? -INFINITY : top + __log2f(e + g);
+          inv *= g * all;
+          of_old = e * all;
+        }
+        seen = sum;
+      }
       auto read = [&](float (&o)[32], int col) {
         load32(t_o + col, o);
         wait_ld(o);
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = l == 0.f ? 0.f : o[j] * inv;
       };
-      if constexpr (CTAS == 2) {
+      if constexpr (kStaged) {
         // by way of shared memory, 128 bytes a row: a store then covers whole lines of 4 rows (a row a thread, it took a
         // line for every lane: 1.9 us a unit instead of 0.9)
         const uint32_t room = base + kOffOut + warp * 4096;
@@ -559,6 +577,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
           using E = typename std::remove_pointer<decltype(out)>::type;
           constexpr int kEach = 16 / sizeof(E);
           float o[32];
+          [[maybe_unused]] float4 old[kTwo ? 8 : 1];   // the pieces before, as they are stored
+          if constexpr (kTwo) {
+            if (w.more) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int row = r - lane + 4 * k + (lane >> 3);
+                old[k] = row < w.rows ? ld_dep_f32x4(reinterpret_cast<const float4*>(out + at(row) + col) + (lane & 7)) : make_float4(0.f, 0.f, 0.f, 0.f);
+              }
+            }
+          }
 #pragma unroll
           for (int c = 0; c < 4 / static_cast<int>(sizeof(E)); ++c) {
             read(o, col + 32 * c);
@@ -578,7 +606,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int mine = 4 * k + (lane >> 3), unit = lane & 7, row = r - lane + mine;
-            const uint4 v = lds128(room + mine * 128 + ((unit ^ (mine & 7)) << 4));
+            uint4 v = lds128(room + mine * 128 + ((unit ^ (mine & 7)) << 4));
+            if constexpr (kTwo) {
+              if (w.more) {
+                const float e = __shfl_sync(0xffffffffu, of_old, mine);
+                v.x = __float_as_uint(fmaf(old[k].x, e, __uint_as_float(v.x)));
+                v.y = __float_as_uint(fmaf(old[k].y, e, __uint_as_float(v.y)));
+                v.z = __float_as_uint(fmaf(old[k].z, e, __uint_as_float(v.z)));
+                v.w = __float_as_uint(fmaf(old[k].w, e, __uint_as_float(v.w)));
+              }
+            }
             if (row < w.rows) *reinterpret_cast<uint4*>(out + at(row) + col + kEach * unit) = v;
           }
           __syncwarp();
@@ -606,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
           }
         }
       }
-      if (live && !whole) a.rec_lse[rec] = l == 0.f ? -INFINITY : m - 3.f + __log2f(l);
+      if (live && !whole) a.rec_lse[rec] = sum;
     }
   } else if (warp < 10 && rank == 0) {
     // ---- products, of tile warp - 8. The whole warp walks the halves of steps, so that
@@ -625,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     for (unsigned part = 0; ok; ++part) {
       if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
       const int seq = s_work[part & 1].seq, halves = s_work[part & 1].tiles ? s_work[part & 1].halves : 0;
-      const int rows = s_work[part & 1].rows;
+      const int rows = s_work[part & 1].rows, more = s_work[part & 1].more, keep = s_work[part & 1].keep;
       const bool mine = rows > t * CTAS * 128;   // else this warp only says that it is done with what is loaded
       const bool both = rows > CTAS * 128;
       before = s_work[part & 1].tiles;
@@ -652,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         if (both && lane == 0) mbar_arrive(bar(kTurn0 + (t ^ 1)));
       };
       // Half i - 2's weights times values, half i's scores, when both are there.
-      if (!(ok = warp_wait(kQFull, filled++ & 1))) break;
+      if (!more && !(ok = warp_wait(kQFull, filled++ & 1))) break;
       for (int i = 0; i < halves + 2; ++i) {
         const bool load = i < halves && i % CTAS == 0, weights = i >= 2;
         const unsigned count = n + i - 2;
@@ -692,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
             if (i == halves + 1) commit(kODone0 + t);
           }
           if (frees) commit(kEmpty0 + weighed.stage);
-          if (i + 1 == halves) commit(kQEmpty);
+          if (i + 1 == halves && !keep) commit(kQEmpty);
         }
         __syncwarp();
         your_turn();
@@ -730,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     const long long ctas = cut < 1 ? 1 : (cut < teams ? cut : teams);
     line.least = !a.may_split ? INT_MAX : line.total < 16ll * teams ? 1 : 2;
     auto cut_of = [&](long long team_) { return divide(line.total * team_, ctas); };
-    int from = 0, last_step = 0;   // steps of the unit at hand that are done, or others'; and those up to which to go in the last unit
+    int from = 0, last_step = 0;   // steps of the unit at hand that are others'; and those up to which to go in the last unit
     long long last = 0;            // where that begins
     const bool works = team < ctas && line.total > 0;
     if (works) {
@@ -746,6 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     const int group16 = lane & (kGroups - 1);
     Turn<kStages> load;
     unsigned loads = 0;
+    int done = from;               // steps of the unit at hand that are done, or others'
     int before = 0, before2 = 0;   // steps of the parts that the slot's last reader may be at
     bool ok = true;
     for (unsigned part = 0;; ++part) {
@@ -754,6 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       w.seq = -1;
       const auto& u = line.at;
       const int to = u.base < last ? u.steps : last_step;
+      // in one piece, or in several of about a size
+      const int pieces = kTwo ? max((to - done + kPiece - 1) / kPiece, 1) : 1;
+      const int upto = done + (to - done + pieces - 1) / pieces;
       if (works && u.base <= last && from < to) {
         const int src = u.b & 31;
         Chunk ch;
@@ -767,17 +808,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         w.rows = min(per, served - first) * a.group;
         w.pos0 = ch.len - ch.n + first;
         w.limit = limit_of(a, ch, u.j, per);
-        w.tile0 = from;
-        w.tiles = w.limit == 0 ? 0 : to - from;
+        w.tile0 = done;
+        w.tiles = w.limit == 0 ? 0 : upto - done;
+        w.more = done > from;
+        w.keep = upto < to;
         w.halves = min((w.limit + 63) / 64 - 2 * w.tile0, 2 * w.tiles);
         w.loads = w.tiles ? (w.halves + CTAS - 1) / CTAS : 0;
         w.slot = from > 0 ? 2 * team : (to < u.steps ? 2 * team + 1 : -1);
         w.zero0 = ch.q0 + served;
-        w.zeros = u.j == 0 && from == 0 ? ch.n - served : 0;   // queries past max_q_len
+        w.zeros = u.j == 0 && done == 0 ? ch.n - served : 0;   // queries past max_q_len
         w.load0 = loads;
-        if (u.j == 0 && from == 0 && u.h == 0 && speaks && (ch.n > a.max_q_len || ch.len > a.limit))
+        if (u.j == 0 && done == 0 && u.h == 0 && speaks && (ch.n > a.max_q_len || ch.len > a.limit))
           b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
-        if (from == 0 && to < u.steps && speaks) {
+        if (done == 0 && to < u.steps && speaks) {
           // the last team whose cut is in the unit, and stays there
           long long owner = divide(u.behind() * ctas - 1, line.total);
           while (owner > team && u.step_of(cut_of(owner), line.least) == u.steps) --owner;
@@ -853,8 +896,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         blk = blk_next;
       }
       if (!ok) break;
-      line.next();
-      from = 0;
+      if (kTwo && upto < to) {
+        done = upto;
+      } else {
+        line.next();
+        from = done = 0;
+      }
     }
     // the copies in flight end before their memory goes (in the first CTA of a pair, the second one's too), and so do the
     // products that read them and what these signal to either CTA
@@ -874,10 +921,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     for (unsigned part = 0; ok; ++part) {
       if (!(ok = long_wait(kWFull0 + (part & 1), part >> 1 & 1, before))) break;
       const int seq = s_work[part & 1].seq, tiles = s_work[part & 1].tiles, rows = s_work[part & 1].rows, q0 = s_work[part & 1].q0;
-      const int head0 = s_work[part & 1].h * a.group;
+      const int head0 = s_work[part & 1].h * a.group, more = s_work[part & 1].more;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
       if (seq < 0) break;
+      if (more) {   // they are there
+        before += tiles;
+        continue;
+      }
       const int wait_for = before;
       before = tiles;
       if (tiles == 0) continue;

@@ -55,6 +55,11 @@ constexpr int kShortMost = 35;
 // 128 x 1000-3000 of 64 heads (1024 pairs, 3 records) 178 us for 195, 118 x 0-12 of 48 10.4 for 21.6, 48 x 300-900 of 32 (7
 // records) 24.2 for 25.2; 100 x 500-5000 of 8 heads 182.5 for 181, 26 x 1000-9000 of 48 (14 records) 73.7 for 68.9
 constexpr int kManyHeads = 152 * 8, kFewRecords = 8;
+// Tiles that are summed in one go. The tensor cores cut what they add off rather than round it, about 2^-25 of the sum each
+// time; with f32 output a warp that walks a long history joins the sums of its runs in fp32, in its record (against 64 bits,
+// 128 x 16384 of 8 heads, bf16: 4.0e-6, else 1.3e-5). Beside a 16-bit output's rounding that is nothing, and it takes 2 % of
+// 4 x 131072 to look for the ends of runs.
+constexpr int kRun = 128;
 constexpr float kStep = 8.f;       // the running maximum moves in steps of at least this, log2 units
 static_assert(kMaxCtas * kWarps <= kMaxWarps, "workspace");
 
@@ -215,7 +220,8 @@ struct Heads {
   }
 };
 
-template <typename T, bool WIDE, int PARTS>
+// RUNS: sums of no more than kRun tiles, joined in the record.
+template <typename T, bool WIDE, int PARTS, bool RUNS>
 __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16RowsArgs a) {
   extern __shared__ uint8_t s_raw[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -280,11 +286,13 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16Ro
   for (int i = 0; i < kStages; ++i) put_one();
 
   Heads<T, WIDE, PARTS> heads;
-  bool fresh = true;
-  int stage = 0;
+  bool fresh = true, again = false;   // begin anew; with the same pair
+  float seen[2] = {0.f, 0.f};         // if again, the log2-sums of heads 2 t and 2 t + 1 so far
+  int stage = 0, run = 0;             // run: tiles since the beginning
   for (; todo > 0; --todo) {
-    if (fresh) {   // a new (row, head) pair: its query heads
+    if (fresh) {   // a new (row, head) pair, or a new run of one: its query heads
       fresh = false;
+      run = 0;
       heads.begin(static_cast<const T*>(a.q) + get.row * a.q_stride + get.h * a.group * kKvD, a.group, lane);
     }
 
@@ -304,8 +312,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16Ro
     put_one();
     stage = stage + 1 == kStages ? 0 : stage + 1;
 
-    // the end of the pair, or of this warp's part of it
-    if (get.t + 1 == get.tiles || todo == 1) {
+    // the end of the pair, of this warp's part of it, or of a run
+    const bool ends = get.t + 1 == get.tiles || todo == 1;
+    if (ends || (RUNS && ++run == kRun)) {
       heads.end();
       const long long rec = (static_cast<long long>(get.row) * a.n_kv + get.h + wid) * a.group;
 #pragma unroll
@@ -313,17 +322,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) kv16_split_kernel(const Kv16Ro
         const int head = 2 * t + k;
         const float l = k ? heads.l1 : heads.l0, m = k ? heads.m1 : heads.m0;
         if (head < a.group) {
-          const float f = l > 0.f ? 0.125f / l : (l == 0.f ? 0.f : l);   // NaN stays
+          float f = l > 0.f ? 0.125f / l : (l == 0.f ? 0.f : l);   // NaN stays
+          float sum = l == 0.f ? -INFINITY : m + __log2f(l);
           float* o = a.rec_o + (rec + head) * kKvD + g;
+          if (RUNS && again) {   // what the runs before left, this lane's own
+            const float top = fmaxf(seen[k], sum);
+            const float e = seen[k] == -INFINITY ? 0.f : exp2f(seen[k] - top), w = sum == -INFINITY ? 0.f : exp2f(sum - top);
+            const float all = e + w == 0.f ? 0.f : 1.f / (e + w);
+            sum = e + w == 0.f ? -INFINITY : top + __log2f(e + w);
+            f *= w * all;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o[16 * j] = heads.acc[j][k] * f;
-            o[16 * j + 8] = heads.acc[j][k + 2] * f;
+            for (int j = 0; j < 8; ++j) {
+              o[16 * j] = fmaf(ld_dep_f32(o + 16 * j), e * all, heads.acc[j][k] * f);
+              o[16 * j + 8] = fmaf(ld_dep_f32(o + 16 * j + 8), e * all, heads.acc[j][k + 2] * f);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              o[16 * j] = heads.acc[j][k] * f;
+              o[16 * j + 8] = heads.acc[j][k + 2] * f;
+            }
           }
-          if (g == 0) a.rec_lse[rec + head] = l == 0.f ? -INFINITY : m + __log2f(l);
+          if (RUNS) seen[k] = sum;
+          if (g == 0) a.rec_lse[rec + head] = sum;
         }
       }
       fresh = true;
+      again = !ends;
     }
     if (todo > 1) next_tile(a, get);
   }
@@ -495,16 +520,16 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
   cluster_sync();   // nobody goes while its sums are read
 }
 
-template <typename T, bool WIDE, int PARTS>
+template <typename T, bool WIDE, int PARTS, bool RUNS>
 cudaError_t launch_split(const Kv16RowsArgs& a, int ctas, int dev, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t err = b8_allow_smem(kv16_split_kernel<T, WIDE, PARTS>, kSmem, dev, &done);
+  const cudaError_t err = b8_allow_smem(kv16_split_kernel<T, WIDE, PARTS, RUNS>, kSmem, dev, &done);
   if (err != cudaSuccess) return err;
-  return launch_pdl(kv16_split_kernel<T, WIDE, PARTS>, dim3(ctas), dim3(kWarps * 32), kSmem, s, a);
+  return launch_pdl(kv16_split_kernel<T, WIDE, PARTS, RUNS>, dim3(ctas), dim3(kWarps * 32), kSmem, s, a);
 }
-template <typename T, int PARTS>
+template <typename T, int PARTS, bool RUNS>
 cudaError_t launch_split(const Kv16RowsArgs& a, int ctas, int dev, cudaStream_t s) {
-  return a.group > 4 ? launch_split<T, true, PARTS>(a, ctas, dev, s) : launch_split<T, false, PARTS>(a, ctas, dev, s);
+  return a.group > 4 ? launch_split<T, true, PARTS, RUNS>(a, ctas, dev, s) : launch_split<T, false, PARTS, RUNS>(a, ctas, dev, s);
 }
 
 template <typename T, typename TO, bool WIDE>
@@ -549,9 +574,8 @@ cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* work
   const size_t records = static_cast<size_t>(a.rows) * a.n_kv + kMaxWarps;
   a.rec_o = static_cast<float*>(workspace);
   a.rec_lse = a.rec_o + records * a.group * kKvD;
-  if (!is_bf16) err = launch_split<__half, 2>(a, ctas, dev, s);
-  else if (out_dtype == TQ_DTYPE_F32) err = launch_split<__nv_bfloat16, 3>(a, ctas, dev, s);
-  else err = launch_split<__nv_bfloat16, 2>(a, ctas, dev, s);
+  if (out_dtype == TQ_DTYPE_F32) err = is_bf16 ? launch_split<__nv_bfloat16, 3, true>(a, ctas, dev, s) : launch_split<__half, 2, true>(a, ctas, dev, s);
+  else err = is_bf16 ? launch_split<__nv_bfloat16, 2, false>(a, ctas, dev, s) : launch_split<__half, 2, false>(a, ctas, dev, s);
   if (err != cudaSuccess) return err;
   // records of a pair, if the lengths are alike: all of them in one round of loads
   long long records_each = a.warps / pairs + 2;
