@@ -942,6 +942,8 @@ def test_long_sums_in_f32(tq, dtype):
         ws = torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, 8 * batch, out.shape[0], q_len, n), dtype=torch.uint8, device="cuda")
         tq.tq_kv16_continue(c.cfg, q[:q_len].cuda().repeat(8 * batch, 1, 1), starts, q_len, cache, table.repeat(8 * batch, 1), lens, n, out, ws)
         got = out.view(8 * batch, q_len, 8, 128)
+        # all chunks are the same one: whole or cut anywhere
+        assert ((got - got[0]).flatten(1).norm(dim=1) < 2 * 320 * 2.0 ** -25 * 1.5 * got[0].norm()).all()
         for b in (0, 95, 191):
             pick = [0, q_len - 1]
             assert f32_error(c, q[pick], got[b, pick].cpu().numpy().astype(np.float64), [n - q_len + 1 + i for i in pick]) < 320 * 2.0 ** -25 * 1.5
@@ -949,6 +951,7 @@ def test_long_sums_in_f32(tq, dtype):
     out = torch.empty((rows, 8, 128), dtype=torch.float32, device="cuda")
     ws = torch.empty(tq.tq_kv16_decode_workspace_size(c.cfg, rows, n), dtype=torch.uint8, device="cuda")
     tq.tq_kv16_decode(c.cfg, q[:1].cuda().repeat(rows, 1, 1), cache, table.repeat(rows, 1), lens, n, out, ws)
+    assert ((out - out[0]).flatten(1).norm(dim=1) < 2 * 384 * 2.0 ** -25 * 1.5 * out[0].norm()).all()
     for b in (0, 200, 399):
         assert f32_error(c, q[:1], out[b:b + 1].cpu().numpy().astype(np.float64), [n]) < 384 * 2.0 ** -25 * 1.5
 
