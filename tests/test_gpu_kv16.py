@@ -373,19 +373,20 @@ def shifted(shape, dtype, value, shift):
     return room[off:off + n].view(shape)
 
 
-# More (sequence, head) pairs than this are not one launch's work on any of the sizes here
-FEW = 2 * 152
+# More (sequence, head) pairs than the second are not one launch's work, more than the first that of CTAs with an SM each
+ONE, FEW = 152, 2 * 152
 
 
 def run_decode(c, q, lens=None, out_dtype="f32", status=None, max_len=None, scale=0.0, line=False, shift=0):
-    """`line`: with empty sequences behind the others until the line's split and merge take the call."""
+    """`line`: with empty sequences behind the others until the line's split and merge take the call, or (half) the short
+    kernel's CTAs of four warps."""
     cache, table, _ = c.gpu()
     rows = q.shape[0]
     lens = c.lens if lens is None else np.asarray(lens, dtype=np.int32)
     msl = max(int(lens.max(initial=0)), 1) if max_len is None else max_len
     q = q.cuda()
     if line:
-        more = max(FEW // c.n_kv + 1 - rows, 0)
+        more = max((ONE if line == "half" else FEW) // c.n_kv + 1 - rows, 0)
         q = torch.cat([q, q[:1].repeat(more, 1, 1)])
         lens, table = np.append(lens, np.zeros(more, dtype=np.int32)), torch.cat([table, table[:1].repeat(more, 1)])
     out = shifted(q.shape, DT[out_dtype], float("nan"), shift)
@@ -406,7 +407,7 @@ def check_decode(c, q, got, out_dtype, lens=None, scale=SCALE):
 @pytest.mark.parametrize("block,n_kv,group,dtype,out", [
     (16, 8, 4, "bf16", "bf16"), (32, 2, 1, "fp16", "fp16"), (64, 1, 8, "bf16", "f32"), (128, 2, 3, "fp16", "f32"),
     (16, 1, 5, "bf16", "f32"), (64, 3, 2, "fp16", "bf16"), (16, 2, 7, "bf16", "fp16"), (32, 1, 6, "fp16", "f32"), (16, 2, 4, "fp16", "f32")])
-@pytest.mark.parametrize("line", [False, True])
+@pytest.mark.parametrize("line", [False, "half", True])
 def test_decode(tq, block, n_kv, group, dtype, out, line):
     lens = [0, 1, 15, 16, 17, 63, 64, 65, 200, 333]
     c = Case(tq, dtype, block, n_kv * group, n_kv, [max(x, 1) for x in lens], seed=group).fill(lens)
@@ -420,7 +421,7 @@ def test_decode(tq, block, n_kv, group, dtype, out, line):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("lens", [[1], [0], [0, 0, 0], [2100], [700, 0, 0, 1, 900], [9000, 3]])
-@pytest.mark.parametrize("line", [False, True])
+@pytest.mark.parametrize("line", [False, "half", True])
 def test_decode_few_and_empty_sequences(tq, dtype, lens, line):
     c = Case(tq, dtype, 16, 4, 1, [max(x, 1) for x in lens], seed=3).fill(lens)
     q = c.draw(len(lens), 4)
@@ -448,7 +449,7 @@ def test_decode_scale_argument_and_strided_queries(tq, lens):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("gain", [1e-3, 30.0])
-@pytest.mark.parametrize("line", [False, True])
+@pytest.mark.parametrize("line", [False, "half", True])
 def test_decode_scores_that_rise(tq, dtype, gain, line):
     """Keys that grow along the sequence: the running maximum moves again and again, by little or by much."""
     n = 700
@@ -462,7 +463,7 @@ def test_decode_scores_that_rise(tq, dtype, gain, line):
     check_continue(c, q.repeat(40, 1, 1), got, [0, 40], [n], "f32")
 
 
-@pytest.mark.parametrize("line", [False, True])
+@pytest.mark.parametrize("line", [False, "half", True])
 def test_decode_device_errors(tq, line):
     c = Case(tq, "bf16", 16, 4, 2, [100, 40], seed=14).fill([100, 40])
     c.table[0, 2], c.table[1, :] = -1, 2 ** 31 - 1
@@ -576,11 +577,12 @@ def test_refusals_with_tensors_on_the_gpu(tq):
 MODE = "rows"
 
 
-@pytest.fixture(params=["rows", "single", "pair"])
+@pytest.fixture(params=["rows", "half", "single", "pair"])
 def mode(request):
-    """Which of its kernels a chunk runs on goes by the sizes of the call: few queries are rows of their own; of more, a
+    """Which of its kernels a chunk runs on goes by the sizes of the call: few queries are rows of their own (of CTAs of
+    eight warps or, half, of four); of more, a
     CTA takes 256 rows, or a pair of CTAs 512 where chunks have more than 256 on average. The same chunks come to the
-    latter two with rows behind the last sequence, and sequences without queries."""
+    latter three with rows behind the last sequence, and sequences without queries."""
     global MODE
     MODE = request.param
     yield MODE
@@ -593,7 +595,10 @@ def run_continue(c, q, starts, lens, out_dtype="f32", status=None, max_q=None, m
     starts, lens = np.asarray(starts, dtype=np.int32), np.asarray(lens, dtype=np.int32)
     msl = max(int(max(lens)), 1) if max_len is None else max_len
     mq = int(np.diff(starts).max(initial=0)) if max_q is None else max_q
-    if MODE != "rows":
+    if MODE == "half":
+        more = max(ONE // c.n_kv + 1 - rows, 0)
+        q = torch.cat([q.cpu(), torch.zeros((more, *q.shape[1:]), dtype=q.dtype)])
+    elif MODE != "rows":
         more = max(FEW + 1 - rows, 0 if MODE == "single" else 256 * batch // group + 1 - rows, 0)
         empty = max(-(-(rows + more) * group // 256) - batch, 0) if MODE == "single" else 0
         q = torch.cat([q.cpu(), torch.zeros((more, *q.shape[1:]), dtype=q.dtype)])

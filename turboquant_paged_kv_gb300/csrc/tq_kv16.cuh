@@ -84,11 +84,15 @@ struct Kv16RowsArgs {
   int early_indices;
   float qscale;             // softmax scale * log2(e)
 };
-// Whether so many rows over so many positions are served by one launch of clusters, a
-// cluster a (row, KV head), rather than by what costs `most` (rounds of clusters x tiles a
-// warp and 3); if so, `ctas` is their size.
-bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int* ctas);
-cudaError_t kv16_short_launch(const Kv16RowsArgs& a, bool is_bf16, int out_dtype, int ctas, int dev, cudaStream_t s);
+// How many rows over so many positions are served by one launch, all of it resident at once: a cluster of `ctas` CTAs of 8
+// warps a (row, KV head), one an SM, or where there are more of these than SMs, a CTA of 4 warps each, two an SM. False:
+// there are more still, or more than `most` (`most_half`) tiles a warp; at most 32 each, a lane of the kernel.
+struct Kv16Short {
+  int ctas;
+  bool half;
+};
+bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int most_half, Kv16Short* how);
+cudaError_t kv16_short_launch(const Kv16RowsArgs& a, bool is_bf16, int out_dtype, const Kv16Short& how, int dev, cudaStream_t s);
 
 }  // namespace tq
 

@@ -83,10 +83,10 @@ constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: two
 // Rows a chunk, on average, above which pairs of CTAs are used: 16 x 96 queries of 32 heads over 8192 (384 rows) 193 us for
 // 217, 16 x 64 (256) 150 for 135, where a pair's units are half empty
 constexpr int kPairRows = 256;
-// Up to which cost (tq_kv16.cuh) queries are rows of their own: 1 x 64 over 2000 of 2 heads (16 tiles a warp) 12.4 us for
-// 19.3, 3 x 7 over 400 of 8 (4, two rounds) 10.1 for 12.9, 4 x 5 over 1000 (8, two rounds) 14.9 for 15.0, 1 x 16 over 4000
-// (31) 20.9 for 17.9, 8 x 5 over 500 (4, three rounds) 16.3 for 15.1
-constexpr int kShortMost = 22;
+// Up to which tiles a warp (tq_kv16.cuh) queries are rows of their own, by CTAs of 8 warps and of 4: 1 x 64 over
+// 2000 of 2 heads (16 tiles a warp of 8) 12.4 us for 19.3, 1 x 16 over 4000 (31) 20.9 for 17.9; 3 x 7 over 400 of 8 (7 of 4)
+// 8.4 for 13.6, over 1000 (16) 13.2 for 20.0, over 1400 (22) 16.5 for 15.8
+constexpr int kShortMost = 19, kShortMostHalf = 20;
 // Steps of the longest history up to which units are not cut: so many are done while records are written and merged. (One
 // chunk of 416 over 445, 3 heads: 16.4 us whole, 19.7 cut; 4 of 50-150 over 97-391, 6 heads of 8: 19.7 and 26.2; 7 of 40-120
 // over 218-872, one head: 18.0 and 19.5; with 12: 2 of 364-1093 over few, 4 heads: 25.6, with 8 22.1.)
@@ -1167,9 +1167,10 @@ tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stri
   const int cap = b8_cap(cfg, bt_stride);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // A few queries: each a row of its own over the cache, in one launch (one that this kernel's start and merge outlast).
-  int dev = 0, sms = 0, each = 0;
+  int dev = 0, sms = 0;
+  Kv16Short how;
   if (b8_current_device(&dev, &sms) != cudaSuccess) return TQ_ERR_CUDA;
-  if (kv16_short(total_q, cfg->num_kv_heads, max_seq_len < cap ? max_seq_len : cap, sms < kCtas ? sms : kCtas, kShortMost, &each)) {
+  if (kv16_short(total_q, cfg->num_kv_heads, max_seq_len < cap ? max_seq_len : cap, sms < kCtas ? sms : kCtas, kShortMost, kShortMostHalf, &how)) {
     Kv16RowsArgs r = {};
     r.c = kv16_cache(cfg, L, cache, num_blocks, bt_stride);
     r.q = q;
@@ -1188,7 +1189,7 @@ tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stri
     r.batch = batch;
     r.max_q_len = max_q_len;
     r.qscale = b8_qscale(scale);
-    return kv16_short_launch(r, L.is_bf16, out_dtype, each, dev, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    return kv16_short_launch(r, L.is_bf16, out_dtype, how, dev, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
   }
   ChunkArgs a = {};
   a.c = kv16_cache(cfg, L, cache, num_blocks, bt_stride);

@@ -44,13 +44,12 @@ constexpr int kStages = 2;
 constexpr int kMaxCtas = 256;      // grid cap: sizes the workspace without a device query
 constexpr int kMaxWarps = 4096;    // partial records beside one per pair
 constexpr int kSmem = kWarps * kStages * (kKvTileBytes + 8) + 128;   // and room to align to 128
-constexpr int kShortWarps = 8;     // a CTA of kv16_short_kernel
-constexpr int kShortStages = 3;
-constexpr int kShortSmem = kShortWarps * kShortStages * (kKvTileBytes + 8) + 128;
-// Up to which rounds x (tiles a warp + 3) the short kernel is used in place of the split and the merge, 2 rounds at most:
-// 16 x 1024 of 8 heads (8 tiles) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9, 32 x 1200 (10, two rounds) 29.1 for
-// 31.6, 20 x 1000 (8, two rounds) 20.4 for 20.1, 64 x 100 (1, four rounds) 15.7 for 14.9
-constexpr int kShortMost = 35;
+constexpr int kShortStages = 3;    // of kv16_short_kernel, a warp
+constexpr int short_smem(int warps) { return warps * kShortStages * (kKvTileBytes + 8) + 128; }
+// Up to which tiles a warp the short kernel is used in place of the split and the merge, by CTAs of 8 warps and of 4:
+// 16 x 1024 of 8 heads (8 tiles a warp of 8) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9; 20 x 500 (8 of 4) 9.3 for
+// 12.8, 20 x 2000 (32) 28.2 for 32.8, 37 x 1000 (16) 26.2 for 31.4. No more than 32: a lane of the kernel each.
+constexpr int kShortMost = 32, kShortMostHalf = 32;
 // From more query heads than kManyHeads on, of at most kFewRecords records each, a warp merges one rather than a CTA:
 // 128 x 1000-3000 of 64 heads (1024 pairs, 3 records) 178 us for 195, 118 x 0-12 of 48 10.4 for 21.6, 48 x 300-900 of 32 (7
 // records) 24.2 for 25.2; 100 x 500-5000 of 8 heads 182.5 for 181, 26 x 1000-9000 of 48 (14 records) 73.7 for 68.9
@@ -380,17 +379,17 @@ __device__ __forceinline__ int row_of_chunk(const Kv16RowsArgs& a, int row, int 
 // tiles dealt to their warps in turn; what the warps hold is merged in shared memory,
 // then what the CTAs hold, each CTA a part of the output. Measured against the split
 // and the merge, or the chunks' kernel: see kShortMost here and in tq_kv16_continue.cu.
-template <typename T, typename TO, bool WIDE>
-__global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const Kv16RowsArgs a) {
+template <typename T, typename TO, bool WIDE, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) kv16_short_kernel(const Kv16RowsArgs a) {
   constexpr int kParts = std::is_same<T, __nv_bfloat16>::value && std::is_same<TO, float>::value ? 3 : 2;
   extern __shared__ uint8_t s_raw[];
-  __shared__ float s_m[kShortWarps][kB8MaxGroup], s_l[kShortWarps][kB8MaxGroup];
+  __shared__ float s_m[WARPS][kB8MaxGroup], s_l[WARPS][kB8MaxGroup];
   __shared__ float s_o[kB8MaxGroup * kKvD], s_om[kB8MaxGroup], s_ol[kB8MaxGroup];   // the CTA's
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const uint32_t smem = (static_cast<uint32_t>(__cvta_generic_to_shared(s_raw)) + 127u) & ~127u;
   const uint32_t ring = smem + warp * kShortStages * kKvTileBytes;
-  const uint32_t bars = smem + kShortWarps * kShortStages * kKvTileBytes + warp * kShortStages * 8;
+  const uint32_t bars = smem + WARPS * kShortStages * kKvTileBytes + warp * kShortStages * 8;
   if (lane == 0) {
 #pragma unroll
     for (int i = 0; i < kShortStages; ++i) mbar_init(bars + 8 * i, 1);
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
   __syncwarp();
   const int ctas = a.warps, rank = blockIdx.x % ctas, pair = blockIdx.x / ctas;   // CTAs of a pair
   const int row = pair / a.n_kv, h = pair - row * a.n_kv;
-  const int first = rank * kShortWarps + warp, step = ctas * kShortWarps;   // of the pair's tiles
+  const int first = rank * WARPS + warp, step = ctas * WARPS;   // of the pair's tiles
   if (!a.early_indices) grid_dep_wait();
   bool too_long, ours = true;   // ours: the row is somebody's
   int len, seq = row;
@@ -469,13 +468,13 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
   const float* rings = reinterpret_cast<const float*>(s_raw + (smem - static_cast<uint32_t>(__cvta_generic_to_shared(s_raw))));
   TO* out = static_cast<TO*>(a.out) + (static_cast<long long>(row) * a.n_q + h * a.group) * kKvD;
   if (!ours && ctas == 1) return;
-  for (int e = threadIdx.x; e < all; e += kShortWarps * 32) {
+  for (int e = threadIdx.x; e < all; e += WARPS * 32) {
     const int head = e >> 7;
     float m = -INFINITY, l = 0.f, o = 0.f;
 #pragma unroll
-    for (int w = 0; w < kShortWarps; ++w) m = fmaxf(m, s_m[w][head]);
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][head]);
 #pragma unroll
-    for (int w = 0; w < kShortWarps; ++w) {
+    for (int w = 0; w < WARPS; ++w) {
       const float lw = s_l[w][head];
       if (lw == 0.f) continue;   // nothing seen, and nothing in the ring
       const float f = exp2f(s_m[w][head] - m);
@@ -496,7 +495,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) kv16_short_kernel(const K
   cluster_sync();
   const uint32_t at_o = static_cast<uint32_t>(__cvta_generic_to_shared(s_o)), at_m = static_cast<uint32_t>(__cvta_generic_to_shared(s_om)),
                  at_l = static_cast<uint32_t>(__cvta_generic_to_shared(s_ol));
-  for (int e = rank * (kShortWarps * 32) + threadIdx.x; e < all; e += ctas * kShortWarps * 32) {
+  for (int e = rank * (WARPS * 32) + threadIdx.x; e < all; e += ctas * WARPS * 32) {
     const int head = e >> 7;
     float mk[8], lk[8], ok_[8], m = -INFINITY, l = 0.f, o = 0.f;
 #pragma unroll
@@ -532,20 +531,25 @@ cudaError_t launch_split(const Kv16RowsArgs& a, int ctas, int dev, cudaStream_t 
   return a.group > 4 ? launch_split<T, true, PARTS, RUNS>(a, ctas, dev, s) : launch_split<T, false, PARTS, RUNS>(a, ctas, dev, s);
 }
 
-template <typename T, typename TO, bool WIDE>
-cudaError_t launch_short(Kv16RowsArgs a, int ctas, int dev, cudaStream_t s) {
+template <typename T, typename TO, bool WIDE, int WARPS>
+cudaError_t launch_short(const Kv16RowsArgs& a, int dev, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t err = b8_allow_smem(kv16_short_kernel<T, TO, WIDE>, kShortSmem, dev, &done);
+  const cudaError_t err = b8_allow_smem(kv16_short_kernel<T, TO, WIDE, WARPS>, short_smem(WARPS), dev, &done);
   if (err != cudaSuccess) return err;
-  a.warps = ctas;
-  const dim3 grid(static_cast<unsigned>(a.rows) * a.n_kv * ctas);
-  return launch_pdl_cluster(kv16_short_kernel<T, TO, WIDE>, grid, dim3(kShortWarps * 32), ctas, kShortSmem, s, a);
+  const dim3 grid(static_cast<unsigned>(a.rows) * a.n_kv * a.warps);
+  return launch_pdl_cluster(kv16_short_kernel<T, TO, WIDE, WARPS>, grid, dim3(WARPS * 32), a.warps, short_smem(WARPS), s, a);
+}
+template <typename T, typename TO>
+cudaError_t launch_short(Kv16RowsArgs a, const Kv16Short& how, int dev, cudaStream_t s) {
+  a.warps = how.ctas;
+  if (how.half) return a.group > 4 ? launch_short<T, TO, true, 4>(a, dev, s) : launch_short<T, TO, false, 4>(a, dev, s);
+  return a.group > 4 ? launch_short<T, TO, true, 8>(a, dev, s) : launch_short<T, TO, false, 8>(a, dev, s);
 }
 template <typename T>
-cudaError_t launch_short(const Kv16RowsArgs& a, int out_dtype, int ctas, int dev, cudaStream_t s) {
-  if (out_dtype == TQ_DTYPE_F32) return a.group > 4 ? launch_short<T, float, true>(a, ctas, dev, s) : launch_short<T, float, false>(a, ctas, dev, s);
-  if (out_dtype == TQ_DTYPE_F16) return a.group > 4 ? launch_short<T, __half, true>(a, ctas, dev, s) : launch_short<T, __half, false>(a, ctas, dev, s);
-  return a.group > 4 ? launch_short<T, __nv_bfloat16, true>(a, ctas, dev, s) : launch_short<T, __nv_bfloat16, false>(a, ctas, dev, s);
+cudaError_t launch_short(const Kv16RowsArgs& a, int out_dtype, const Kv16Short& how, int dev, cudaStream_t s) {
+  if (out_dtype == TQ_DTYPE_F32) return launch_short<T, float>(a, how, dev, s);
+  if (out_dtype == TQ_DTYPE_F16) return launch_short<T, __half>(a, how, dev, s);
+  return launch_short<T, __nv_bfloat16>(a, how, dev, s);
 }
 
 template <typename TO>
@@ -567,9 +571,9 @@ cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* work
   const int ctas = sms < kMaxCtas ? sms : kMaxCtas;
   const long long tiles = (static_cast<long long>(a.max_seq_len) + kKvRows - 1) / kKvRows;
   const long long pairs = static_cast<long long>(a.rows) * a.n_kv;
-  int each;
-  if (kv16_short(a.rows, a.n_kv, a.max_seq_len < a.cap ? a.max_seq_len : a.cap, ctas, kShortMost, &each))
-    return kv16_short_launch(a, is_bf16, out_dtype, each, dev, s);
+  Kv16Short how;
+  if (kv16_short(a.rows, a.n_kv, a.max_seq_len < a.cap ? a.max_seq_len : a.cap, ctas, kShortMost, kShortMostHalf, &how))
+    return kv16_short_launch(a, is_bf16, out_dtype, how, dev, s);
   a.warps = ctas * kWarps;
   const size_t records = static_cast<size_t>(a.rows) * a.n_kv + kMaxWarps;
   a.rec_o = static_cast<float*>(workspace);
@@ -587,17 +591,18 @@ cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* work
 
 }  // namespace
 
-bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int* ctas) {
+bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int most_half, Kv16Short* how) {
   const long long pairs = rows * n_kv, tiles = (static_cast<long long>(max_len) + kKvRows - 1) / kKvRows;
-  int each = 8;   // as many as have an SM each, and a tile a warp
-  while (each > 1 && (pairs * each > sms || tiles <= static_cast<long long>(each / 2) * kShortWarps)) each /= 2;
-  *ctas = each;
-  const long long rounds = (pairs * each + sms - 1) / sms, of_warp = (tiles + each * kShortWarps - 1) / (each * kShortWarps);
-  return rounds <= 2 && of_warp <= 32 && rounds * (of_warp + 3) <= most;   // (32 tiles: a lane of the kernel each)
+  how->half = pairs > sms;
+  how->ctas = 1;
+  if (how->half) return pairs <= 2 * sms && tiles <= 4ll * most_half;
+  how->ctas = 8;   // as many as have an SM each, and a tile a warp
+  while (how->ctas > 1 && (pairs * how->ctas > sms || tiles <= how->ctas / 2 * 8ll)) how->ctas /= 2;
+  return tiles <= how->ctas * 8ll * most;
 }
 
-cudaError_t kv16_short_launch(const Kv16RowsArgs& a, bool is_bf16, int out_dtype, int ctas, int dev, cudaStream_t s) {
-  return is_bf16 ? launch_short<__nv_bfloat16>(a, out_dtype, ctas, dev, s) : launch_short<__half>(a, out_dtype, ctas, dev, s);
+cudaError_t kv16_short_launch(const Kv16RowsArgs& a, bool is_bf16, int out_dtype, const Kv16Short& how, int dev, cudaStream_t s) {
+  return is_bf16 ? launch_short<__nv_bfloat16>(a, out_dtype, how, dev, s) : launch_short<__half>(a, out_dtype, how, dev, s);
 }
 
 }  // namespace tq
