@@ -373,22 +373,32 @@ def shifted(shape, dtype, value, shift):
     return room[off:off + n].view(shape)
 
 
-# More (sequence, head) pairs than the second are not one launch's work, more than the first that of CTAs with an SM each
-ONE, FEW = 152, 2 * 152
+# Up to so many (sequence, head) pairs go to CTAs of eight, four and two warps; more queries of chunks, and decodes over more
+# than 32 tiles a warp, to other kernels
+ONE, TWO, FEW = 152, 2 * 152, 4 * 152
+LONG = 1040
+
+
+def widened(table, block):
+    """With room for LONG positions a sequence."""
+    return torch.nn.functional.pad(table, (0, max(-(-LONG // block) - table.shape[1], 0)), value=-1)
 
 
 def run_decode(c, q, lens=None, out_dtype="f32", status=None, max_len=None, scale=0.0, line=False, shift=0):
-    """`line`: with empty sequences behind the others until the line's split and merge take the call, or (half) the short
-    kernel's CTAs of four warps."""
+    """`line`: 4 or 2, with empty sequences behind the others until the short kernel's CTAs of so many warps take the call;
+    True, and with room for more positions, so that the split and the merge of the line do."""
     cache, table, _ = c.gpu()
     rows = q.shape[0]
     lens = c.lens if lens is None else np.asarray(lens, dtype=np.int32)
     msl = max(int(lens.max(initial=0)), 1) if max_len is None else max_len
     q = q.cuda()
     if line:
-        more = max((ONE if line == "half" else FEW) // c.n_kv + 1 - rows, 0)
+        more = max((ONE if line == 4 else TWO) // c.n_kv + 1 - rows, 0)
         q = torch.cat([q, q[:1].repeat(more, 1, 1)])
         lens, table = np.append(lens, np.zeros(more, dtype=np.int32)), torch.cat([table, table[:1].repeat(more, 1)])
+    if line is True:
+        table = widened(table, c.block)
+        msl = max(msl, LONG) if max_len is None else max_len
     out = shifted(q.shape, DT[out_dtype], float("nan"), shift)
     ws = shifted((c.tq.tq_kv16_decode_workspace_size(c.cfg, q.shape[0], msl),), torch.uint8, 255, shift)
     c.tq.tq_kv16_decode(c.cfg, q, cache, table, torch.from_numpy(lens).cuda(), msl, out, ws, scale=scale, dev_status=status)
@@ -407,7 +417,7 @@ def check_decode(c, q, got, out_dtype, lens=None, scale=SCALE):
 @pytest.mark.parametrize("block,n_kv,group,dtype,out", [
     (16, 8, 4, "bf16", "bf16"), (32, 2, 1, "fp16", "fp16"), (64, 1, 8, "bf16", "f32"), (128, 2, 3, "fp16", "f32"),
     (16, 1, 5, "bf16", "f32"), (64, 3, 2, "fp16", "bf16"), (16, 2, 7, "bf16", "fp16"), (32, 1, 6, "fp16", "f32"), (16, 2, 4, "fp16", "f32")])
-@pytest.mark.parametrize("line", [False, "half", True])
+@pytest.mark.parametrize("line", [False, 4, 2, True])
 def test_decode(tq, block, n_kv, group, dtype, out, line):
     lens = [0, 1, 15, 16, 17, 63, 64, 65, 200, 333]
     c = Case(tq, dtype, block, n_kv * group, n_kv, [max(x, 1) for x in lens], seed=group).fill(lens)
@@ -421,7 +431,7 @@ def test_decode(tq, block, n_kv, group, dtype, out, line):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("lens", [[1], [0], [0, 0, 0], [2100], [700, 0, 0, 1, 900], [9000, 3]])
-@pytest.mark.parametrize("line", [False, "half", True])
+@pytest.mark.parametrize("line", [False, 4, 2, True])
 def test_decode_few_and_empty_sequences(tq, dtype, lens, line):
     c = Case(tq, dtype, 16, 4, 1, [max(x, 1) for x in lens], seed=3).fill(lens)
     q = c.draw(len(lens), 4)
@@ -430,16 +440,17 @@ def test_decode_few_and_empty_sequences(tq, dtype, lens, line):
 
 @pytest.mark.parametrize("batch,n_kv,group,dtype,out,most", [
     (1500, 2, 2, "bf16", "f32", 20), (777, 1, 5, "fp16", "bf16", 20), (199, 3, 7, "bf16", "fp16", 300), (300, 1, 3, "fp16", "f32", 200)])
-def test_decode_many_sequences(tq, batch, n_kv, group, dtype, out, most):
+@pytest.mark.parametrize("line", [False, True])
+def test_decode_many_sequences(tq, batch, n_kv, group, dtype, out, most, line):
     """More (sequence, head) pairs than warps, most of them one tile long; heads merged by a warp each, and (the last) by a CTA each."""
     rng = np.random.default_rng(8)
     lens = [int(x) for x in rng.integers(0, most, batch)]
     c = Case(tq, dtype, 16, n_kv * group, n_kv, [max(x, 1) for x in lens], seed=8).fill(lens)
     q = c.draw(len(lens), n_kv * group)
-    check_decode(c, q, run_decode(c, q, out_dtype=out), out)
+    check_decode(c, q, run_decode(c, q, out_dtype=out, line=line), out)
 
 
-@pytest.mark.parametrize("lens", [[50, 20], [50, 20, 0, 33] * 40])      # one launch, or the split and the merge
+@pytest.mark.parametrize("lens", [[50, 20], [50, 20, 0, 33] * 40, [1100, 20, 0, 33] * 40])
 def test_decode_scale_argument_and_strided_queries(tq, lens):
     c = Case(tq, "fp16", 32, 8, 2, lens, seed=12).fill(lens)
     fused = c.draw(len(lens), 12).cuda()
@@ -449,7 +460,7 @@ def test_decode_scale_argument_and_strided_queries(tq, lens):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("gain", [1e-3, 30.0])
-@pytest.mark.parametrize("line", [False, "half", True])
+@pytest.mark.parametrize("line", [False, 4, 2, True])
 def test_decode_scores_that_rise(tq, dtype, gain, line):
     """Keys that grow along the sequence: the running maximum moves again and again, by little or by much."""
     n = 700
@@ -463,15 +474,16 @@ def test_decode_scores_that_rise(tq, dtype, gain, line):
     check_continue(c, q.repeat(40, 1, 1), got, [0, 40], [n], "f32")
 
 
-@pytest.mark.parametrize("line", [False, "half", True])
+@pytest.mark.parametrize("line", [False, 4, 2, True])
 def test_decode_device_errors(tq, line):
-    c = Case(tq, "bf16", 16, 4, 2, [100, 40], seed=14).fill([100, 40])
+    length, cut = (1200, 1100) if line is True else (100, 90)
+    c = Case(tq, "bf16", 16, 4, 2, [length, 40], seed=14).fill([length, 40])
     c.table[0, 2], c.table[1, :] = -1, 2 ** 31 - 1
     q = c.draw(2, 4)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    got = run_decode(c, q, status=status, max_len=90, line=line)
+    got = run_decode(c, q, status=status, max_len=cut, line=line)
     assert int(status) == tq.TQ_DEV_BLOCK_OUT_OF_RANGE | tq.TQ_DEV_SEQ_TOO_LONG
-    check_decode(c, q, got, "f32", lens=[90, 40])      # positions of bad blocks are left out; nothing left: zeros
+    check_decode(c, q, got, "f32", lens=[cut, 40])      # positions of bad blocks are left out; nothing left: zeros
     assert not got[1].any()
 
 
@@ -481,7 +493,7 @@ def test_not_a_number_query_stays_in_its_row(tq, mode, dtype):
     c = Case(tq, dtype, 16, 4, 1, lens, seed=15).fill(lens)
     q = c.draw(2, 4)
     q[0, 1, 3] = float("nan")
-    for line in (False, True):
+    for line in (False, 4, 2, True):
         got = run_decode(c, q, line=line)
         assert np.isnan(got[0, 1]).all() and np.isfinite(got[0, [0, 2, 3]]).all() and np.isfinite(got[1]).all()
     q = c.draw(20, 4)
@@ -494,8 +506,8 @@ def test_not_a_number_query_stays_in_its_row(tq, mode, dtype):
         assert np.isfinite(got[fine]).all()
 
 
-@pytest.mark.parametrize("pad", [0, 80])      # one launch, or the split and the merge
-def test_decode_on_streams_and_in_graphs(tq, pad):
+@pytest.mark.parametrize("pad,most", [(0, 400), (40, 400), (80, 400), (80, 1100)])      # one launch, or the split and the merge
+def test_decode_on_streams_and_in_graphs(tq, pad, most):
     """Two calls on two streams with a workspace each, and a captured call
     replayed after the lengths and the query changed, with the indices known
     early too; the same call twice gives the same bits."""
@@ -503,28 +515,29 @@ def test_decode_on_streams_and_in_graphs(tq, pad):
     c = Case(tq, "bf16", 32, 16, 4, [400] * 4, seed=16).fill([400] * 4)
     cache, table, _ = c.gpu()
     table = torch.cat([table, table[:1].repeat(pad, 1)])
+    table = widened(table, 32) if most > LONG else table
     lens_d = torch.tensor(lens + [0] * pad, dtype=torch.int32, device="cuda")
     q = [c.draw(rows, 16).cuda() for _ in range(2)]
-    n = tq.tq_kv16_decode_workspace_size(c.cfg, rows, 400)
+    n = tq.tq_kv16_decode_workspace_size(c.cfg, rows, most)
     ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
     out = [torch.empty((rows, 16, 128), dtype=torch.float32, device="cuda") for _ in range(2)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
     for i in range(2):
         with torch.cuda.stream(streams[i]):
-            tq.tq_kv16_decode(c.cfg, q[i], cache, table, lens_d, 400, out[i], ws[i])
+            tq.tq_kv16_decode(c.cfg, q[i], cache, table, lens_d, most, out[i], ws[i])
     torch.cuda.synchronize()
     for i in range(2):
         check_decode(c, q[i][:4].cpu(), out[i].cpu().numpy().astype(np.float64), "f32", lens=lens)
     first = out[0].clone()
-    tq.tq_kv16_decode(c.cfg, q[0], cache, table, lens_d, 400, out[0], ws[0])
+    tq.tq_kv16_decode(c.cfg, q[0], cache, table, lens_d, most, out[0], ws[0])
     assert torch.equal(first, out[0])
     graphs = []
     for flags in (0, tq.TQ_FLAG_INDICES_READY):      # (the two graphs share a workspace)
         cfg = tq.make_config("kv_bf16", 16, 4, block_size=32, flags=flags)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            tq.tq_kv16_decode(cfg, q[0], cache, table, lens_d, 400, out[0], ws[0])
+            tq.tq_kv16_decode(cfg, q[0], cache, table, lens_d, most, out[0], ws[0])
         graphs.append(graph)
     for new in ([400, 1, 33, 0], [17, 399, 64, 250]):
         lens_d[:4].copy_(torch.tensor(new, dtype=torch.int32))
@@ -577,12 +590,12 @@ def test_refusals_with_tensors_on_the_gpu(tq):
 MODE = "rows"
 
 
-@pytest.fixture(params=["rows", "half", "single", "pair"])
+@pytest.fixture(params=["rows", 4, 2, "single", "pair"])
 def mode(request):
     """Which of its kernels a chunk runs on goes by the sizes of the call: few queries are rows of their own (of CTAs of
-    eight warps or, half, of four); of more, a
+    eight warps, 4 or 2); of more, a
     CTA takes 256 rows, or a pair of CTAs 512 where chunks have more than 256 on average. The same chunks come to the
-    latter three with rows behind the last sequence, and sequences without queries."""
+    latter four with rows behind the last sequence, and sequences without queries."""
     global MODE
     MODE = request.param
     yield MODE
@@ -595,8 +608,8 @@ def run_continue(c, q, starts, lens, out_dtype="f32", status=None, max_q=None, m
     starts, lens = np.asarray(starts, dtype=np.int32), np.asarray(lens, dtype=np.int32)
     msl = max(int(max(lens)), 1) if max_len is None else max_len
     mq = int(np.diff(starts).max(initial=0)) if max_q is None else max_q
-    if MODE == "half":
-        more = max(ONE // c.n_kv + 1 - rows, 0)
+    if MODE in (4, 2):
+        more = max((ONE if MODE == 4 else TWO) // c.n_kv + 1 - rows, 0)
         q = torch.cat([q.cpu(), torch.zeros((more, *q.shape[1:]), dtype=q.dtype)])
     elif MODE != "rows":
         more = max(FEW + 1 - rows, 0 if MODE == "single" else 256 * batch // group + 1 - rows, 0)
@@ -834,7 +847,7 @@ def test_rows_that_were_not_stored(tq, mode, dtype, block, hist, q_len, max_q):
     check_decode(c, q[:1], run_decode(c, q[:1], [kept]), "f32", lens=[kept])
 
 
-@pytest.mark.parametrize("rows,empty", [(64, 0), (400, 5), (400, 0)])      # rows of their own, units of a CTA, of a pair
+@pytest.mark.parametrize("rows,empty", [(64, 0), (200, 0), (400, 5), (400, 0)])      # rows of their own, units of a CTA, of a pair
 def test_continue_on_streams_and_in_graphs(tq, rows, empty):
     """As for the decode: two streams, then a captured call replayed with other
     starts, lengths and queries in padded tensors; the same call gives the same bits."""
@@ -843,7 +856,7 @@ def test_continue_on_streams_and_in_graphs(tq, rows, empty):
     msl, batch = 900, 3 + empty
     table = torch.cat([table, table[:1].repeat(empty, 1)])
     padded = lambda starts, lens: (starts + starts[-1:] * empty, lens + [0] * empty)      # noqa: E731
-    assert (rows * 4 > 256 * batch, rows * 2 > FEW) == ((False, False), (False, True), (True, True))[(rows > 64) + (rows > 64 and not empty)]
+    assert (rows * 4 > 256 * batch, rows * 2 > FEW) == {64: (False, False), 200: (True, False), 400: (not empty, True)}[rows]
     calls = []
     for starts, lens in (padded([0, 20, 20, 55], [900, 3, 500]), padded([0, 1, 40, 64], [7, 899, 64])):
         q = c.draw(rows, 8)
@@ -908,13 +921,13 @@ def test_offsets_past_32_bits(tq):
         tq.tq_kv16_continue(cfg, turned, starts, 300, cache, table, lens_d, 300, many, ws)
         # the same where a decode is the line's, and where a unit is one CTA's
         more = 40
-        wide = torch.cat([table, table[:1].repeat(more, 1)])
+        wide = torch.nn.functional.pad(torch.cat([table, table[:1].repeat(more, 1)]), (0, 6), value=base)
         lens_w = torch.cat([lens_d, lens_d[:1].repeat(more)])
         starts_w = torch.cat([starts, starts[-1:].repeat(more)])
-        ws = torch.empty(max(tq.tq_kv16_decode_workspace_size(cfg, 42, 300), tq.tq_kv16_continue_workspace_size(cfg, 42, 377, 300, 300)),
+        ws = torch.empty(max(tq.tq_kv16_decode_workspace_size(cfg, 42, LONG), tq.tq_kv16_continue_workspace_size(cfg, 42, 377, 300, 300)),
                          dtype=torch.uint8, device="cuda")
         line = torch.empty((42, n_q, 128), dtype=torch.float32, device="cuda")
-        tq.tq_kv16_decode(cfg, turned[:42].contiguous(), cache, wide, lens_w, 300, line, ws)
+        tq.tq_kv16_decode(cfg, turned[:42].contiguous(), cache, wide, lens_w, LONG, line, ws)
         alone = torch.empty((377, n_q, 128), dtype=torch.float32, device="cuda")
         tq.tq_kv16_continue(cfg, turned, starts_w, 300, cache, wide, lens_w, 300, alone, ws)
         results.append((cache[base * bb:].clone(), turned, one, many, line, alone))

@@ -84,14 +84,14 @@ struct Kv16RowsArgs {
   int early_indices;
   float qscale;             // softmax scale * log2(e)
 };
-// How many rows over so many positions are served by one launch, all of it resident at once: a cluster of `ctas` CTAs of 8
-// warps a (row, KV head), one an SM, or where there are more of these than SMs, a CTA of 4 warps each, two an SM. False:
-// there are more still, or more than `most` (`most_half`) tiles a warp; at most 32 each, a lane of the kernel.
+// How so many rows over so many positions are served by one launch: a cluster of `ctas` CTAs of 8 warps a (row, KV head),
+// one an SM; where there are more of these than SMs, a CTA of 4 warps each, two an SM, or of 2, four an SM. False: there are
+// more than are resident at once (unless `more`), or more than `most` (`most_small`: of 4 or 2) tiles a warp, 32 at most.
 struct Kv16Short {
   int ctas;
-  bool half;
+  int warps;
 };
-bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int most_half, Kv16Short* how);
+bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int most_small, bool more, Kv16Short* how);
 cudaError_t kv16_short_launch(const Kv16RowsArgs& a, bool is_bf16, int out_dtype, const Kv16Short& how, int dev, cudaStream_t s);
 
 }  // namespace tq

@@ -83,10 +83,11 @@ constexpr uint32_t kColS = 0, kColO = 256;         // tensor memory columns: two
 // Rows a chunk, on average, above which pairs of CTAs are used: 16 x 96 queries of 32 heads over 8192 (384 rows) 193 us for
 // 217, 16 x 64 (256) 150 for 135, where a pair's units are half empty
 constexpr int kPairRows = 256;
-// Up to which tiles a warp (tq_kv16.cuh) queries are rows of their own, by CTAs of 8 warps and of 4: 1 x 64 over
+// Up to which tiles a warp (tq_kv16.cuh) queries are rows of their own, by CTAs of 8 warps, and of 4 or 2: 1 x 64 over
 // 2000 of 2 heads (16 tiles a warp of 8) 12.4 us for 19.3, 1 x 16 over 4000 (31) 20.9 for 17.9; 3 x 7 over 400 of 8 (7 of 4)
-// 8.4 for 13.6, over 1000 (16) 13.2 for 20.0, over 1400 (22) 16.5 for 15.8
-constexpr int kShortMost = 19, kShortMostHalf = 20;
+// 8.4 for 13.6, over 1000 (16) 13.2 for 20.0, over 1400 (22) 16.5 for 15.8; 6 x 12 over 300
+// of 8 (10 of 2) 10.6 for 12.3, over 600 (19) 15.9 for 16.1
+constexpr int kShortMost = 19, kShortMostSmall = 20;
 // Steps of the longest history up to which units are not cut: so many are done while records are written and merged. (One
 // chunk of 416 over 445, 3 heads: 16.4 us whole, 19.7 cut; 4 of 50-150 over 97-391, 6 heads of 8: 19.7 and 26.2; 7 of 40-120
 // over 218-872, one head: 18.0 and 19.5; with 12: 2 of 364-1093 over few, 4 heads: 25.6, with 8 22.1.)
@@ -1170,7 +1171,7 @@ tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stri
   int dev = 0, sms = 0;
   Kv16Short how;
   if (b8_current_device(&dev, &sms) != cudaSuccess) return TQ_ERR_CUDA;
-  if (kv16_short(total_q, cfg->num_kv_heads, max_seq_len < cap ? max_seq_len : cap, sms < kCtas ? sms : kCtas, kShortMost, kShortMostHalf, &how)) {
+  if (kv16_short(total_q, cfg->num_kv_heads, max_seq_len < cap ? max_seq_len : cap, sms < kCtas ? sms : kCtas, kShortMost, kShortMostSmall, false, &how)) {
     Kv16RowsArgs r = {};
     r.c = kv16_cache(cfg, L, cache, num_blocks, bt_stride);
     r.q = q;

@@ -46,13 +46,16 @@ constexpr int kMaxWarps = 4096;    // partial records beside one per pair
 constexpr int kSmem = kWarps * kStages * (kKvTileBytes + 8) + 128;   // and room to align to 128
 constexpr int kShortStages = 3;    // of kv16_short_kernel, a warp
 constexpr int short_smem(int warps) { return warps * kShortStages * (kKvTileBytes + 8) + 128; }
-// Up to which tiles a warp the short kernel is used in place of the split and the merge, by CTAs of 8 warps and of 4:
+// Up to which tiles a warp the short kernel is used in place of the split and the merge, by CTAs of 8 warps, 4 and 2:
 // 16 x 1024 of 8 heads (8 tiles a warp of 8) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9; 20 x 500 (8 of 4) 9.3 for
-// 12.8, 20 x 2000 (32) 28.2 for 32.8, 37 x 1000 (16) 26.2 for 31.4. No more than 32: a lane of the kernel each.
-constexpr int kShortMost = 32, kShortMostHalf = 32;
+// 12.8, 20 x 2000 (32) 28.2 for 32.8, 37 x 1000 (16) 26.2 for 31.4;
+// 64 x 300 (10 of 2) 10.6 for 16.3, 75 x 1000 (32) 46.2 for 51.3, 75 x 0-1000 29.3 for 33.9; beyond what is resident, 80 x
+// 1000 (640 CTAs of 608) 59.1 for 56.4, 80 x 0-1000 30.4 for 35.8, 256 x 100-600 62 for 73, 1000 x 300 of 2 heads 50 for 64.
+// No more than 32: a lane of the kernel each.
+constexpr int kShortMost = 32;
 // From more query heads than kManyHeads on, of at most kFewRecords records each, a warp merges one rather than a CTA:
-// 128 x 1000-3000 of 64 heads (1024 pairs, 3 records) 178 us for 195, 118 x 0-12 of 48 10.4 for 21.6, 48 x 300-900 of 32 (7
-// records) 24.2 for 25.2; 100 x 500-5000 of 8 heads 182.5 for 181, 26 x 1000-9000 of 48 (14 records) 73.7 for 68.9
+// 128 x 1000-3000 of 64 heads (1024 pairs, 3 records) 178 us for 195, 100 x 500-5000 of 32 (6 records) 99.9 for 105.7;
+// 100 x 500-5000 of 8 heads 182.5 for 181, 26 x 1000-9000 of 48 (14 records) 73.7 for 68.9
 constexpr int kManyHeads = 152 * 8, kFewRecords = 8;
 // Tiles that are summed in one go. The tensor cores cut what they add off rather than round it, about 2^-25 of the sum each
 // time; with f32 output a warp that walks a long history joins the sums of its runs in fp32, in its record (against 64 bits,
@@ -542,7 +545,8 @@ cudaError_t launch_short(const Kv16RowsArgs& a, int dev, cudaStream_t s) {
 template <typename T, typename TO>
 cudaError_t launch_short(Kv16RowsArgs a, const Kv16Short& how, int dev, cudaStream_t s) {
   a.warps = how.ctas;
-  if (how.half) return a.group > 4 ? launch_short<T, TO, true, 4>(a, dev, s) : launch_short<T, TO, false, 4>(a, dev, s);
+  if (how.warps == 2) return a.group > 4 ? launch_short<T, TO, true, 2>(a, dev, s) : launch_short<T, TO, false, 2>(a, dev, s);
+  if (how.warps == 4) return a.group > 4 ? launch_short<T, TO, true, 4>(a, dev, s) : launch_short<T, TO, false, 4>(a, dev, s);
   return a.group > 4 ? launch_short<T, TO, true, 8>(a, dev, s) : launch_short<T, TO, false, 8>(a, dev, s);
 }
 template <typename T>
@@ -572,7 +576,7 @@ cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* work
   const long long tiles = (static_cast<long long>(a.max_seq_len) + kKvRows - 1) / kKvRows;
   const long long pairs = static_cast<long long>(a.rows) * a.n_kv;
   Kv16Short how;
-  if (kv16_short(a.rows, a.n_kv, a.max_seq_len < a.cap ? a.max_seq_len : a.cap, ctas, kShortMost, kShortMostHalf, &how))
+  if (kv16_short(a.rows, a.n_kv, a.max_seq_len < a.cap ? a.max_seq_len : a.cap, ctas, kShortMost, kShortMost, true, &how))
     return kv16_short_launch(a, is_bf16, out_dtype, how, dev, s);
   a.warps = ctas * kWarps;
   const size_t records = static_cast<size_t>(a.rows) * a.n_kv + kMaxWarps;
@@ -591,11 +595,11 @@ cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* work
 
 }  // namespace
 
-bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int most_half, Kv16Short* how) {
+bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int most_small, bool more, Kv16Short* how) {
   const long long pairs = rows * n_kv, tiles = (static_cast<long long>(max_len) + kKvRows - 1) / kKvRows;
-  how->half = pairs > sms;
+  how->warps = pairs > 2 * sms ? 2 : pairs > sms ? 4 : 8;
   how->ctas = 1;
-  if (how->half) return pairs <= 2 * sms && tiles <= 4ll * most_half;
+  if (how->warps < 8) return (more || pairs <= 4 * sms) && tiles <= how->warps * static_cast<long long>(most_small);
   how->ctas = 8;   // as many as have an SM each, and a tile a warp
   while (how->ctas > 1 && (pairs * how->ctas > sms || tiles <= how->ctas / 2 * 8ll)) how->ctas /= 2;
   return tiles <= how->ctas * 8ll * most;
