@@ -374,9 +374,9 @@ def shifted(shape, dtype, value, shift):
 
 
 # Up to so many (sequence, head) pairs go to CTAs of eight, four and two warps; more queries of chunks, and decodes over more
-# than 32 tiles a warp, to other kernels
+# than 64 tiles a warp, to other kernels
 ONE, TWO, FEW = 152, 2 * 152, 4 * 152
-LONG = 1040
+LONG = 2064
 
 
 def widened(table, block):
@@ -430,7 +430,7 @@ def test_decode(tq, block, n_kv, group, dtype, out, line):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("lens", [[1], [0], [0, 0, 0], [2100], [700, 0, 0, 1, 900], [9000, 3]])
+@pytest.mark.parametrize("lens", [[1], [0], [0, 0, 0], [2100], [700, 0, 0, 1, 900], [1500], [9000, 3]])
 @pytest.mark.parametrize("line", [False, 4, 2, True])
 def test_decode_few_and_empty_sequences(tq, dtype, lens, line):
     c = Case(tq, dtype, 16, 4, 1, [max(x, 1) for x in lens], seed=3).fill(lens)
@@ -450,7 +450,7 @@ def test_decode_many_sequences(tq, batch, n_kv, group, dtype, out, most, line):
     check_decode(c, q, run_decode(c, q, out_dtype=out, line=line), out)
 
 
-@pytest.mark.parametrize("lens", [[50, 20], [50, 20, 0, 33] * 40, [1100, 20, 0, 33] * 40])
+@pytest.mark.parametrize("lens", [[50, 20], [50, 20, 0, 33] * 40, [2100, 20, 0, 33] * 40])
 def test_decode_scale_argument_and_strided_queries(tq, lens):
     c = Case(tq, "fp16", 32, 8, 2, lens, seed=12).fill(lens)
     fused = c.draw(len(lens), 12).cuda()
@@ -476,9 +476,9 @@ def test_decode_scores_that_rise(tq, dtype, gain, line):
 
 @pytest.mark.parametrize("line", [False, 4, 2, True])
 def test_decode_device_errors(tq, line):
-    length, cut = (1200, 1100) if line is True else (100, 90)
+    length, cut = (2200, 2100) if line is True else (1700, 1600)
     c = Case(tq, "bf16", 16, 4, 2, [length, 40], seed=14).fill([length, 40])
-    c.table[0, 2], c.table[1, :] = -1, 2 ** 31 - 1
+    c.table[0, 2], c.table[0, 95], c.table[1, :] = -1, c.blocks, 2 ** 31 - 1
     q = c.draw(2, 4)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     got = run_decode(c, q, status=status, max_len=cut, line=line)
@@ -506,7 +506,7 @@ def test_not_a_number_query_stays_in_its_row(tq, mode, dtype):
         assert np.isfinite(got[fine]).all()
 
 
-@pytest.mark.parametrize("pad,most", [(0, 400), (40, 400), (80, 400), (80, 1100)])      # one launch, or the split and the merge
+@pytest.mark.parametrize("pad,most", [(0, 400), (40, 400), (80, 400), (80, 2100)])      # one launch, or the split and the merge
 def test_decode_on_streams_and_in_graphs(tq, pad, most):
     """Two calls on two streams with a workspace each, and a captured call
     replayed after the lengths and the query changed, with the indices known
@@ -921,7 +921,7 @@ def test_offsets_past_32_bits(tq):
         tq.tq_kv16_continue(cfg, turned, starts, 300, cache, table, lens_d, 300, many, ws)
         # the same where a decode is the line's, and where a unit is one CTA's
         more = 40
-        wide = torch.nn.functional.pad(torch.cat([table, table[:1].repeat(more, 1)]), (0, 6), value=base)
+        wide = torch.nn.functional.pad(torch.cat([table, table[:1].repeat(more, 1)]), (0, 14), value=base)
         lens_w = torch.cat([lens_d, lens_d[:1].repeat(more)])
         starts_w = torch.cat([starts, starts[-1:].repeat(more)])
         ws = torch.empty(max(tq.tq_kv16_decode_workspace_size(cfg, 42, LONG), tq.tq_kv16_continue_workspace_size(cfg, 42, 377, 300, 300)),

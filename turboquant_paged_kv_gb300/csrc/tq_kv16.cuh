@@ -86,7 +86,8 @@ struct Kv16RowsArgs {
 };
 // How so many rows over so many positions are served by one launch: a cluster of `ctas` CTAs of 8 warps a (row, KV head),
 // one an SM; where there are more of these than SMs, a CTA of 4 warps each, two an SM, or of 2, four an SM. False: there are
-// more than are resident at once (unless `more`), or more than `most` (`most_small`: of 4 or 2) tiles a warp, 32 at most.
+// more than are resident at once (unless `more`), or more than `most` (`most_small`: of 4 or 2, if resident) tiles a warp, 64 at
+// most.
 struct Kv16Short {
   int ctas;
   int warps;

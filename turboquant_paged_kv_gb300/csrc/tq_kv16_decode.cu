@@ -6,7 +6,7 @@
 // evenly over the warps of a grid of one CTA per SM, and a merge of the warps'
 // records. A warp copies its own tiles, one bulk copy of 8192 bytes each into a
 // ring of its own, and waits on that copy's barrier. Short work takes one launch
-// instead (kv16_short_kernel), and so do few queries of chunks.
+// instead (kv16_short_kernel), a CTA or a cluster a pair, and so do few queries of chunks.
 //
 // Math, per tile of 16 positions x 128 coordinates, on mma.sync.m16n8k16 in the
 // cache's type with fp32 sums:
@@ -22,10 +22,11 @@
 // only when a score passes it by 2^8 (one warp vote a tile).
 //
 // Bound: memory, the cache being read once. 64 x 512-16384, 8 KV heads: 361 us, 6.63 TB/s
-// of 2.39 GB (0.98 of a measured copy); 4 x 131072, 4 KV heads: 336, 6.38; 32 x 4096: 91,
-// 5.9 (77 % of DRAM's cycles, tensor cores busy for 9 %), of which 4 to 5 us are the start
-// (lengths, table, first tiles, one after another) and 3 the merge; 1 x 301 in one launch
-// 5.7, a chain of those loads, the tiles and the cluster's merge.
+// of 2.39 GB (0.98 of a measured copy); 4 x 131072, 4 KV heads: 336, 6.43. (32 x 4096 by the
+// line: 90 us, 5.96 TB/s, 77 % of DRAM's cycles, tensor cores busy for 9 %, of which 4 to 5
+// us are the start, lengths, table and first tiles one after another, and 3 the merge; in
+// one launch 81, 6.6 TB/s.) 1 x 301 5.7, a chain of those loads, the tiles and the
+// cluster's merge.
 #include <climits>
 
 #include "tq_attn.cuh"
@@ -46,13 +47,13 @@ constexpr int kMaxWarps = 4096;    // partial records beside one per pair
 constexpr int kSmem = kWarps * kStages * (kKvTileBytes + 8) + 128;   // and room to align to 128
 constexpr int kShortStages = 3;    // of kv16_short_kernel, a warp
 constexpr int short_smem(int warps) { return warps * kShortStages * (kKvTileBytes + 8) + 128; }
-// Up to which tiles a warp the short kernel is used in place of the split and the merge, by CTAs of 8 warps, 4 and 2:
-// 16 x 1024 of 8 heads (8 tiles a warp of 8) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9; 20 x 500 (8 of 4) 9.3 for
-// 12.8, 20 x 2000 (32) 28.2 for 32.8, 37 x 1000 (16) 26.2 for 31.4;
-// 64 x 300 (10 of 2) 10.6 for 16.3, 75 x 1000 (32) 46.2 for 51.3, 75 x 0-1000 29.3 for 33.9; beyond what is resident, 80 x
-// 1000 (640 CTAs of 608) 59.1 for 56.4, 80 x 0-1000 30.4 for 35.8, 256 x 100-600 62 for 73, 1000 x 300 of 2 heads 50 for 64.
-// No more than 32: a lane of the kernel each.
-constexpr int kShortMost = 32;
+// Up to which tiles a warp the short kernel is used in place of the split and the merge. By CTAs of 8 warps, and of 2 where
+// there are more than are resident at once: 16 x 1024 of 8 heads (8 tiles) 13.4 us for 17.4, 1 x 16000 (16) 16.6 for 20.9;
+// 80 x 1000 (640 CTAs of 608) 59.1 for 56.4, 80 x 0-1000 30.4 for 35.8, 256 x 100-600 62 for 73, 1000 x 300 of 2 heads 50 for
+// 64. By CTAs of 4 and 2, all resident (64 at most: two ids a lane): 20 x 1000 13.1 for 15.9, 32 x 4096 79 for 88, 32 x 0-4096
+// 44.2 for 45.2, 20 x 0-4096 37.7 for 36.5, 64 x 300 10.6 for 16.3, 64 x 2000 75 for 83, 75 x 0-2000 50 for 53, 26 x 0-3000
+// 30.1 for 28.7. What a line cut evenly gains where lengths differ, its records and their merge cost.
+constexpr int kShortMost = 32, kShortMostSmall = 64;
 // From more query heads than kManyHeads on, of at most kFewRecords records each, a warp merges one rather than a CTA:
 // 128 x 1000-3000 of 64 heads (1024 pairs, 3 records) 178 us for 195, 100 x 500-5000 of 32 (6 records) 99.9 for 105.7;
 // 100 x 500-5000 of 8 heads 182.5 for 181, 26 x 1000-9000 of 48 (14 records) 73.7 for 68.9
@@ -378,7 +379,7 @@ __device__ __forceinline__ int row_of_chunk(const Kv16RowsArgs& a, int row, int 
   return 0;
 }
 
-// Short work in one launch: a cluster of up to 8 CTAs per (sequence, KV head) pair, its
+// Work in one launch: a CTA, or a cluster of up to 8, per (sequence, KV head) pair, its
 // tiles dealt to their warps in turn; what the warps hold is merged in shared memory,
 // then what the CTAs hold, each CTA a part of the output. Measured against the split
 // and the merge, or the chunks' kernel: see kShortMost here and in tq_kv16_continue.cu.
@@ -412,16 +413,19 @@ __global__ void __launch_bounds__(WARPS * 32, 8 / WARPS) kv16_short_kernel(const
   }
   const int tiles = (len + kKvRows - 1) / kKvRows;
   const int todo = tiles > first ? (tiles - first + step - 1) / step : 0;
-  // a block id a lane: this warp's tile number `lane` (no more than 32: see the launch)
-  const int ids = ldg_or(a.block_table + static_cast<long long>(seq) * a.c.bt_stride + ((first + lane * step) >> (a.c.log2_bs - 4)), lane < todo, -1);
+  // two block ids a lane: this warp's tiles number `lane` and lane + 32 (no more than 64: see the launch)
+  const int* table = a.block_table + static_cast<long long>(seq) * a.c.bt_stride;
+  const int ids = ldg_or(table + ((first + lane * step) >> (a.c.log2_bs - 4)), lane < todo, -1);
+  const int ids2 = ldg_or(table + ((first + (lane + 32) * step) >> (a.c.log2_bs - 4)), lane + 32 < todo, -1);
   if (a.early_indices) grid_dep_wait();
   grid_dep_launch();
   if (too_long && h == 0 && rank == 0 && threadIdx.x == 0) b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
   const uint64_t policy = evict_first_policy();
-  const unsigned bad = __ballot_sync(0xffffffffu, lane < todo && !a.c.good(ids));   // tiles that are left out
+  const unsigned long long bad = __ballot_sync(0xffffffffu, lane < todo && !a.c.good(ids)) |   // tiles that are left out
+                                 static_cast<unsigned long long>(__ballot_sync(0xffffffffu, lane + 32 < todo && !a.c.good(ids2))) << 32;
   if (bad && lane == 0) b8_flag(a.status, TQ_DEV_BLOCK_OUT_OF_RANGE);
   auto put = [&](int i) {   // tile i of this warp's to stage i % kShortStages
-    const int blk = __shfl_sync(0xffffffffu, ids, i);
+    const int blk = __shfl_sync(0xffffffffu, i < 32 ? ids : ids2, i & 31);
     const uint32_t bar = bars + 8 * (i % kShortStages);
     if (lane == 0 && !(bad >> i & 1)) {
       mbar_expect(bar, kKvTileBytes);
@@ -576,7 +580,7 @@ cudaError_t split_launch(Kv16RowsArgs a, bool is_bf16, int out_dtype, void* work
   const long long tiles = (static_cast<long long>(a.max_seq_len) + kKvRows - 1) / kKvRows;
   const long long pairs = static_cast<long long>(a.rows) * a.n_kv;
   Kv16Short how;
-  if (kv16_short(a.rows, a.n_kv, a.max_seq_len < a.cap ? a.max_seq_len : a.cap, ctas, kShortMost, kShortMost, true, &how))
+  if (kv16_short(a.rows, a.n_kv, a.max_seq_len < a.cap ? a.max_seq_len : a.cap, ctas, kShortMost, kShortMostSmall, true, &how))
     return kv16_short_launch(a, is_bf16, out_dtype, how, dev, s);
   a.warps = ctas * kWarps;
   const size_t records = static_cast<size_t>(a.rows) * a.n_kv + kMaxWarps;
@@ -599,7 +603,7 @@ bool kv16_short(long long rows, int n_kv, int max_len, int sms, int most, int mo
   const long long pairs = rows * n_kv, tiles = (static_cast<long long>(max_len) + kKvRows - 1) / kKvRows;
   how->warps = pairs > 2 * sms ? 2 : pairs > sms ? 4 : 8;
   how->ctas = 1;
-  if (how->warps < 8) return (more || pairs <= 4 * sms) && tiles <= how->warps * static_cast<long long>(most_small);
+  if (how->warps < 8) return (more || pairs <= 4 * sms) && tiles <= how->warps * static_cast<long long>(pairs > 4 * sms ? most : most_small);
   how->ctas = 8;   // as many as have an SM each, and a tile a warp
   while (how->ctas > 1 && (pairs * how->ctas > sms || tiles <= how->ctas / 2 * 8ll)) how->ctas /= 2;
   return tiles <= how->ctas * 8ll * most;
