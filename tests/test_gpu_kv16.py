@@ -1129,3 +1129,89 @@ def test_beside_the_other_caches(tq):
     check_continue(c, q.cpu(), outs[0], [0, 70, 103], lens, "f32", rows=10)
     # e4m3 keys and values are off by up to 2^-4 each: the two layers agree to about that
     assert np.abs(outs[0] - outs[1]).max() < 0.5 and np.corrcoef(outs[0].ravel(), outs[1].ravel())[0, 1] > 0.99
+
+
+# ---------------------------------------------------------------- steps of many sequences
+
+
+@pytest.fixture(params=["single", "pair"])
+def units(request):
+    """A CTA's units or a pair's, as in `mode`."""
+    global MODE
+    MODE = request.param
+    yield MODE
+    MODE = "rows"
+
+
+def mixed_lengths(rng, batch, chunks, most):
+    """One query a sequence, none for every ninth, and `chunks` longer ones anywhere."""
+    q_lens = np.ones(batch, dtype=np.int64)
+    q_lens[::9] = 0
+    for b, n in zip(rng.permutation(batch)[:len(chunks)], chunks):
+        q_lens[b] = n
+    return q_lens, np.maximum(rng.integers(1, most + 1, batch), q_lens)
+
+
+@pytest.mark.parametrize("batch,n_kv,group,chunks,most,dtype,out", [
+    (33, 2, 8, [200, 150, 70], 900, "bf16", "bf16"), (130, 1, 8, [300, 1, 97, 260, 129, 33, 200], 3000, "fp16", "f32"),
+    (257, 1, 7, [350, 220, 180], 2500, "bf16", "f32"), (300, 3, 4, [500, 260, 129], 1500, "fp16", "fp16"),
+    (1100, 1, 5, [400, 130, 420], 1300, "bf16", "bf16"), (1100, 1, 3, [600, 171, 90], 400, "fp16", "f32")])
+def test_continue_chunks_of_several_tiles_among_many_sequences(tq, units, batch, n_kv, group, chunks, most, dtype, out):
+    """More sequences than a warp has lanes (1100: than it has for groups of 32), some of three tiles of queries and more."""
+    room = max(most, *chunks)
+    c = Case(tq, dtype, 32, n_kv * group, n_kv, [room], seed=batch + group).fill([room])
+    c.table = np.repeat(c.table, batch, 0)
+    q_lens, lens = mixed_lengths(c.rng, batch, chunks, most)
+    c.lens = lens.astype(np.int32)
+    starts = starts_of(q_lens)
+    q = c.draw(int(starts[-1]), n_kv * group)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, starts, lens, out, status)
+    assert int(status) == 0
+    check_continue(c, q, got, starts, lens, out, rows=10)
+
+
+def test_continue_more_sequences_than_are_kept(tq):
+    """Beyond 16384 sequences chunks are read anew for every sum: long ones on both sides of that."""
+    batch, most = 16500, 700
+    c = Case(tq, "bf16", 32, 8, 1, [most], seed=5).fill([most])
+    c.table = np.repeat(c.table, batch, 0)
+    q_lens = (np.arange(batch) % 9 == 0).astype(np.int64)
+    lens = np.maximum(c.rng.integers(1, most + 1, batch), q_lens)
+    for b, n in ((3, 100), (9000, 65), (16383, 300), (16384, 129), (16499, 260)):
+        q_lens[b], lens[b] = n, max(lens[b], n)
+    c.lens = lens.astype(np.int32)
+    starts = starts_of(q_lens)
+    q = c.draw(int(starts[-1]), 8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, starts, lens, "bf16", status)
+    assert int(status) == 0
+    check_continue(c, q, got, starts, lens, "bf16", rows=10)
+
+
+@pytest.mark.parametrize("batch,q_len,group", [(4096, 131072, 8), (2048, 32768, 8)])      # pairs' units, a CTA's
+def test_continue_a_long_prompt_among_thousands(tq, batch, q_len, group):
+    """The search for a team's work is over long before the others stop waiting for it."""
+    at = batch - 7                                     # whose chunk is the prompt
+    c = Case(tq, "bf16", 128, group, 1, [q_len], seed=6).fill([q_len])
+    c.table = np.repeat(c.table, batch, 0)
+    q_lens, lens = np.ones(batch, dtype=np.int64), c.rng.integers(1, 300, batch)
+    q_lens[at], lens[at] = q_len, q_len
+    starts = starts_of(q_lens)
+    rows = int(starts[-1])
+    assert (rows * group > 256 * batch) == (batch == 4096)
+    q = torch.randn((rows, group, 128), dtype=torch.bfloat16, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    cache, table, _ = c.gpu()
+    out = torch.full_like(q, 123.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, batch, rows, q_len, q_len), dtype=torch.uint8, device="cuda")
+    tq.tq_kv16_continue(c.cfg, q, torch.from_numpy(starts).cuda(), q_len, cache, table, torch.from_numpy(lens.astype(np.int32)).cuda(), q_len,
+                        out, ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    assert not torch.any(torch.all(out.view(rows, -1) == 123.0, dim=1))       # every row is written
+    k, v = c.kv(0, q_len)
+    first = int(starts[at])
+    for row, seen in ([(b, int(lens[b])) for b in (0, 31, 32, 1000, at - 1)] + [(first + i, i + 1) for i in (0, 63, q_len // 2 + 5, q_len - 1)] +
+                      [(int(starts[b]), int(lens[b])) for b in (at + 1, batch - 1)]):
+        check_row(c, q[row].cpu(), k[:seen], v[:seen], out[row].double().cpu().numpy(), "bf16", SCALE, True, (row, seen))

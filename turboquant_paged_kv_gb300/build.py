@@ -46,6 +46,7 @@ def _deps():
                          os.path.join(CSRC, "tq_kv16.cuh"),
                          os.path.join(CSRC, "tq_line.cuh"),
                          os.path.join(CSRC, "tq_tc.cuh"),
+                         os.path.join(CSRC, "tq_chunk_cost.h"),
                          os.path.join(INCLUDE, "tq.h"),
                          os.path.abspath(__file__)]
 

@@ -60,6 +60,7 @@
 #include <climits>
 
 #include "tq_attn.cuh"
+#include "tq_chunk_cost.h"
 #include "tq_kv16.cuh"
 #include "tq_tc.cuh"
 
@@ -67,7 +68,7 @@ namespace tq {
 namespace {
 
 constexpr int kRows = 256;             // of a unit, a CTA: two tiles of 128
-constexpr int kCols = 128;             // positions a step, in two halves
+constexpr int kCols = kChunkCols;      // positions a step, in two halves
 constexpr int kThreads = 512;
 constexpr int kCtas = 152;             // grid, one an SM: sizes the workspace without a device query
 constexpr float kMost = 60000.f;       // sums of P up to this: every P fits in fp16
@@ -94,7 +95,7 @@ constexpr int kShortMost = 19, kShortMostSmall = 20;
 constexpr int kNoSplit = 8;
 constexpr int kMergeThreads = 256, kMergeCtas = 3;   // an SM, of the merge: with 8 (2.7 waves of what fits) 32 x 128 takes 208 us for 197
 constexpr int kPiece = 20;                         // steps; 32 x 128 over 4096, f32: 294 us, with 16 311, with 24 294, in one piece 276
-constexpr unsigned long long kStepNs = 100000;     // what a step may take, where a wait is for many
+constexpr unsigned long long kStepNs = 100000;     // what a step may take, where a wait is for many; and the search for work among 32 sequences or 512 tile indexes
 
 struct ChunkArgs {
   Kv16Cache c;
@@ -110,6 +111,7 @@ struct ChunkArgs {
   float *rec_o, *rec_lse;
   int batch, total_q, max_q_len, n_q, group, limit, may_split, part_rows;   // limit: positions at most
   float qscale;                        // softmax scale * log2(e)
+  unsigned long long search_ns;        // a wait's, with the search for work
 };
 
 // barriers, 8 bytes each from kOffBar
@@ -188,25 +190,18 @@ struct Work {
   unsigned load0;      // loads of the CTA before
 };
 
-// A sequence's chunk: its first row, queries, length and tiles of queries.
+// A sequence's chunk: its first row, queries and length.
 struct Chunk {
-  int q0, n, len, tiles;
+  int q0, n, len;
 };
-__device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, int b, int per) {
+__device__ __forceinline__ Chunk chunk_of(const ChunkArgs& a, int q0, int q1, int len) {
   Chunk c;
-  c.q0 = min(max(ldg_or(a.query_start + b, b < a.batch, 0), 0), a.total_q);
-  c.n = min(max(ldg_or(a.query_start + b + 1, b < a.batch, 0), c.q0), a.total_q) - c.q0;
-  c.len = max(ldg_or(a.seq_lens + b, b < a.batch, 0), 0);
-  c.tiles = (min(c.n, a.max_q_len) + per - 1) / per;
+  c.q0 = min(max(q0, 0), a.total_q);
+  c.n = min(max(q1, c.q0), a.total_q) - c.q0;
+  c.len = max(len, 0);
   return c;
 }
-// Positions that the last query of tile j sees, and the unit's steps: one at least, though it may see nothing.
-__device__ __forceinline__ int limit_of(const ChunkArgs& a, const Chunk& c, int j, int per) {
-  return max(min(c.len - c.n + min((j + 1) * per, min(c.n, a.max_q_len)), a.limit), 0);
-}
-__device__ __forceinline__ int steps_of(const ChunkArgs& a, const Chunk& c, int j, int per) {
-  return j < c.tiles ? max((limit_of(a, c, j, per) + kCols - 1) / kCols, 1) : 0;
-}
+__device__ __forceinline__ ChunkSize size_of(const ChunkArgs& a, const Chunk& c) { return {c.len - c.n, min(c.n, a.max_q_len)}; }
 __device__ __forceinline__ long long warp_sum(long long x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -214,14 +209,28 @@ __device__ __forceinline__ long long warp_sum(long long x) {
 }
 
 // The line: for each tile index j, each sequence that has such a tile, each KV head,
-// the cost of the unit. (Units that read the same keys and values, tiles of one chunk,
+// the cost of the unit (tq_chunk_cost.h). (Units that read the same keys and values, tiles of one chunk,
 // are then a fixed part of the line apart, so that teams of CTAs meet them at the same
-// time where chunks are alike.) A step costs 4, or 3 where one row tile is at work, and
-// a unit 10 more (1.45, 1.14 and 3 to 4 us). A warp walks it, the lanes together.
+// time where chunks are alike.) A warp finds its places, the lanes together, a sequence a lane.
+// MANY: more than 32 sequences. These are read once, into shared memory that no load has
+// come to yet (up to kKept; behind these they are read anew whenever they are asked for). Where there
+// are more than kClose tile indexes, a place's is found by bisection, from what all sequences cost up
+// to one, and a walk over the last few; groups of 32 without a chunk of so many tiles are passed
+// over. (4095 sequences of one query and one of 131072, 8 heads: at most 17 sums over 128
+// groups. A walk over tile indexes and groups, each a round trip to L2, took 2048 x 128 of
+// these, 45 ms at the least, which outlasts the other warps' waits; 512 with one of 16384, one KV head: 507 us for
+// 2089, 256 with one of 8192, 8 KV heads: 1768 for 2026.) With up to 32 a walk over tile indexes alone is soon over,
+// and a kernel without the rest starts sooner: 7 chunks of one query and one of 300, 13.0 us for 14.3.
+template <bool MANY>
 struct Line {
-  static constexpr int kUnit = 10;
+  static constexpr int kKept = 4 * kStage / 8;
+  static constexpr int kClose = 8;   // tile indexes that are walked: a sum for one takes several times as long as going on by one
   const ChunkArgs& a;
-  int per, full_rows, lane, tiles_most = 0;   // full_rows: more need both row tiles
+  const ChunkCall call;
+  int lane, tiles_most = 0;
+  uint32_t kept;       // shared memory: (first position, queries served) of the first kKept sequences
+  int span = 0;        // 2^span groups of 32 sequences a lane: the most tiles of a chunk there
+  int most = 0;
   long long total = 0;
   int b0 = -1;
   Chunk ch = {};       // lane's chunk of the 32 from b0 on
@@ -229,7 +238,7 @@ struct Line {
   struct Unit {
     int j, b, h, steps, each;
     long long base;
-    __device__ long long behind() const { return base + static_cast<long long>(steps) * each + kUnit; }
+    __device__ long long behind() const { return base + static_cast<long long>(steps) * each + kChunkUnit; }
     // The step where a cut at x (within the unit) comes to be. Fewer than `least` steps from an end are not worth a record:
     // the cut moves there.
     __device__ int step_of(long long x, int least) const {
@@ -239,32 +248,77 @@ struct Line {
   } at = {};
   int least = 1;
 
-  __device__ Line(const ChunkArgs& args, int per_, int full, int lane_) : a(args), per(per_), full_rows(full), lane(lane_) {
-    for (int i = 0; i < a.batch; i += 32) {
-      group(i);
-      for (int k = 0; k < ch.tiles; ++k) total += cost(k);
-      tiles_most = max(tiles_most, __reduce_max_sync(0xffffffffu, ch.tiles));
+  __device__ Line(const ChunkArgs& args, const ChunkCall& call_, uint32_t room, int lane_) : a(args), call(call_), lane(lane_), kept(room) {
+    if constexpr (MANY) {
+      while ((a.batch - 1) >> 5 >> span >= 32) ++span;
+      for (int i = 0; i < min(a.batch, kKept); i += 128) {   // four round trips in one
+        int q0[4], q1[4], len[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) read(i + 32 * k, q0[k], q1[k], len[k]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const ChunkSize z = size_of(a, chunk_of(a, q0[k], q1[k], len[k]));
+          if (i + 32 * k < kKept) sts64(kept + 8 * (i + 32 * k + lane), make_uint2(z.first, z.served));
+        }
+      }
+    } else {
+      group(0);
+    }
+    for (int i = 0; i < end(); i += 32) {
+      const ChunkSize z = size(i);
+      const int tiles = chunk_tiles(z, call.per), tiles_here = __reduce_max_sync(0xffffffffu, tiles);
+      if (MANY && tiles_here > kClose) {
+        total += chunk_cost_before(z, call, INT_MAX);
+      } else {
+        for (int j = 0; j < tiles; ++j) total += chunk_cost(z, call, j);
+      }
+      if (MANY && i >> 5 >> span == lane) most = max(most, tiles_here);
+      tiles_most = max(tiles_most, tiles_here);
     }
     total = warp_sum(total) * a.c.n_kv;
+  }
+  __device__ __forceinline__ int end() const { return MANY ? a.batch : 32; }   // (of a group of 32, lanes behind the last sequence have none)
+  __device__ __forceinline__ void read(int first, int& q0, int& q1, int& len) const {
+    const int b = first + lane;
+    q0 = ldg_or(a.query_start + b, b < a.batch, 0);
+    q1 = ldg_or(a.query_start + b + 1, b < a.batch, 0);
+    len = ldg_or(a.seq_lens + b, b < a.batch, 0);
   }
   __device__ void group(int first) {
     if (first == b0) return;
     b0 = first;
-    ch = chunk_of(a, first + lane, per);
+    int q0, q1, len;
+    read(first, q0, q1, len);
+    ch = chunk_of(a, q0, q1, len);
   }
-  __device__ int each_of(int j) const { return (min(ch.n, a.max_q_len) - j * per) * a.group > full_rows ? 4 : 3; }
-  __device__ unsigned cost(int j) const {
-    const int s = steps_of(a, ch, j, per);
-    return s ? static_cast<unsigned>(s) * each_of(j) + kUnit : 0u;
+  // Sequence i + lane, i a multiple of 32 (each lane reads what it kept itself).
+  __device__ ChunkSize size(int i) const {
+    if constexpr (!MANY) return size_of(a, ch);
+    if (i < kKept) {
+      const uint2 z = lds64(kept + 8 * (i + lane));
+      return {static_cast<int>(z.x), static_cast<int>(z.y)};
+    }
+    int q0, q1, len;
+    read(i, q0, q1, len);
+    return size_of(a, chunk_of(a, q0, q1, len));
   }
-  // The unit of tile index j that place x of the 32 sequences' is in; they begin at `base`, and cost `c` each, `inc` up to
-  // and with their own.
-  __device__ Unit locate(long long x, int j, long long base, unsigned c, unsigned inc) {
+  // Which spans have a sequence with a tile j, and whether that of the 32 sequences from i on has none.
+  __device__ unsigned tiles_past(int j) const { return MANY ? __ballot_sync(0xffffffffu, most > j) : 1u; }
+  __device__ bool passes(unsigned live, int i) const { return MANY && !(live >> (i >> 5 >> span) & 1); }
+  // What all sequences cost before tile index j.
+  __device__ long long before_tile(int j) const {
+    long long sum = 0;
+    for (int i = 0; i < a.batch; i += 32) sum += chunk_cost_before(size(i), call, j);
+    return warp_sum(sum) * a.c.n_kv;
+  }
+  // The unit of tile index j that place x is in, one of the 32 sequences from i on; these, `z`, begin at `base`, and cost
+  // `c` each, `inc` up to and with their own.
+  __device__ Unit locate(long long x, int j, int i, const ChunkSize& z, long long base, unsigned c, unsigned inc) const {
     const int src = __ffs(__ballot_sync(0xffffffffu, x - base < static_cast<long long>(inc) * a.c.n_kv)) - 1;
     const unsigned here = __shfl_sync(0xffffffffu, c, src);
     base += static_cast<long long>(__shfl_sync(0xffffffffu, inc, src) - here) * a.c.n_kv;
     const int h = static_cast<int>(divide(x - base, here));
-    return {j, b0 + src, h, __shfl_sync(0xffffffffu, steps_of(a, ch, j, per), src), __shfl_sync(0xffffffffu, each_of(j), src),
+    return {j, i + src, h, __shfl_sync(0xffffffffu, chunk_steps(z, call, j), src), __shfl_sync(0xffffffffu, chunk_each(z, call, j), src),
             base + static_cast<long long>(h) * here};
   }
   // Goes to the unit of place x0, whose step `step` the cut there comes to be; last, last_step: the unit where x1 is, and
@@ -274,10 +328,20 @@ struct Line {
     bool found = false, ended = x1 >= total;
     last = total;
     last_step = 0;
+    [[maybe_unused]] int walk = tiles_most > kClose ? 0 : kClose;   // tile indexes to go on by before the next one is searched for
     for (int j = 0; j < tiles_most && !(found && ended); ++j) {
-      for (int i = 0; i < a.batch; i += 32) {
-        group(i);
-        const unsigned c = cost(j);
+      if constexpr (MANY) {
+        if (walk == 0) {
+          chunk_seek(found ? x1 : x0, tiles_most, kClose, found, j, before, [&](int to) { return before_tile(to); });
+          walk = kClose;
+        }
+        --walk;
+      }
+      const unsigned live = tiles_past(j);
+      for (int i = 0; i < end(); i += 32) {
+        if (passes(live, i)) continue;
+        const ChunkSize z = size(i);
+        const unsigned c = chunk_cost(z, call, j);
         const long long behind = before + static_cast<long long>(__reduce_add_sync(0xffffffffu, c)) * a.c.n_kv;
         const bool first = !found && x0 < behind, final = !ended && x1 < behind;
         if (first || final) {
@@ -291,7 +355,7 @@ struct Line {
           ended |= final;
 #pragma unroll 1   // (not unrolled: fetching the code is what takes time here)
           for (int k = first ? 0 : 1; k < (final ? 2 : 1); ++k) {
-            const Unit u = locate(k ? x1 : x0, j, before, c, inc);
+            const Unit u = locate(k ? x1 : x0, j, i, z, before, c, inc);
             if (k) {
               last = u.base;
               last_step = u.step_of(x1, least);
@@ -312,13 +376,16 @@ struct Line {
     at.h = 0;
     ++at.b;
     while (at.j < tiles_most) {
-      for (int i = at.b & ~31; i < a.batch; i += 32) {
+      const unsigned live = tiles_past(at.j);
+      for (int i = at.b & ~31; i < end(); i += 32) {
+        if (passes(live, i)) continue;
         group(i);
-        const unsigned more = __ballot_sync(0xffffffffu, i + lane >= at.b && ch.tiles > at.j);
+        const ChunkSize z = size_of(a, ch);
+        const unsigned more = __ballot_sync(0xffffffffu, i + lane >= at.b && chunk_steps(z, call, at.j) > 0);
         if (more) {
           at.b = i + __ffs(more) - 1;
-          at.steps = __shfl_sync(0xffffffffu, steps_of(a, ch, at.j, per), at.b & 31);
-          at.each = __shfl_sync(0xffffffffu, each_of(at.j), at.b & 31);
+          at.steps = __shfl_sync(0xffffffffu, chunk_steps(z, call, at.j), at.b & 31);
+          at.each = __shfl_sync(0xffffffffu, chunk_each(z, call, at.j), at.b & 31);
           return;
         }
       }
@@ -328,7 +395,7 @@ struct Line {
   }
 };
 
-template <typename T, typename TO, int CTAS>
+template <typename T, typename TO, int CTAS, bool MANY>
 __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs a) {
   constexpr bool kTwo = std::is_same<TO, float>::value;   // P in two parts
   constexpr bool kStaged = CTAS == 2 || kTwo;   // output by way of shared memory
@@ -383,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     if constexpr (CTAS == 2) mma_commit2(bar(b));
     else mma_commit(bar(b));
   };
-  // A wait for a whole part of `steps` steps.
+  // A wait for a whole part of `steps` steps, and for the search for the next one.
   auto long_wait = [&](int b, uint32_t parity, int steps) {
     bool ok = mbar_try(bar(b), parity);
     if (!ok) {
@@ -763,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     }
   } else if (warp == 10) {
     // ---- the work, keys and values
-    Line line(a, per, CTAS * 128, lane);
+    Line<MANY> line(a, {per, a.limit, a.group, CTAS * 128}, base + kOffLoads, lane);
     const long long cut = line.total / 5;   // one step and more a team
     const long long ctas = cut < 1 ? 1 : (cut < teams ? cut : teams);
     line.least = !a.may_split ? INT_MAX : line.total < 16ll * teams ? 1 : 2;
@@ -777,6 +844,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         line.next();
         from = 0;
       }
+    }
+    if constexpr (MANY) {   // chunks that were kept, before loads come to their place
+      fence_smem_async();
+      __syncwarp();
     }
     const bool speaks = rank == 0 && lane == 0;
     if (a.may_split && speaks) a.split_units[team] = make_int4(0, 0, 0, 0);
@@ -808,7 +879,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         w.q0 = ch.q0 + first;
         w.rows = min(per, served - first) * a.group;
         w.pos0 = ch.len - ch.n + first;
-        w.limit = limit_of(a, ch, u.j, per);
+        w.limit = chunk_limit(size_of(a, ch), line.call, u.j);
         w.tile0 = done;
         w.tiles = w.limit == 0 ? 0 : upto - done;
         w.more = done > from;
@@ -1106,25 +1177,26 @@ Plan plan_for(const tq_config* cfg, int batch, int total_q, int max_q_len, int m
   return p;
 }
 
-template <typename T, typename TO, int CTAS>
+template <typename T, typename TO, int CTAS, bool MANY>
 cudaError_t launch(const ChunkArgs& a, const Plan& p, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   int dev = 0, sms = 0;
   cudaError_t err = b8_current_device(&dev, &sms);
-  if (err == cudaSuccess) err = b8_allow_smem(kv16_chunk_kernel<T, TO, CTAS>, kSmem, dev, &done);
+  if (err == cudaSuccess) err = b8_allow_smem(kv16_chunk_kernel<T, TO, CTAS, MANY>, kSmem, dev, &done);
   if (err != cudaSuccess) return err;
   const int most = (sms < kCtas ? sms : kCtas) / CTAS;
   // starts that go backwards may name more units than these: they are served all the same
   const long long steps = p.units * ((static_cast<long long>(a.limit) + kCols - 1) / kCols + 1);
   const int teams = steps < most ? static_cast<int>(steps) : most;
-  if (CTAS == 2) err = launch_pdl_cluster(kv16_chunk_kernel<T, TO, CTAS>, dim3(2 * teams), dim3(kThreads), 2, kSmem, s, a);
-  else err = launch_pdl(kv16_chunk_kernel<T, TO, CTAS>, dim3(teams), dim3(kThreads), kSmem, s, a);
+  if (CTAS == 2) err = launch_pdl_cluster(kv16_chunk_kernel<T, TO, CTAS, MANY>, dim3(2 * teams), dim3(kThreads), 2, kSmem, s, a);
+  else err = launch_pdl(kv16_chunk_kernel<T, TO, CTAS, MANY>, dim3(teams), dim3(kThreads), kSmem, s, a);
   if (err != cudaSuccess || !p.may_split) return err;
   return launch_pdl(kv16_chunk_merge_kernel<TO>, dim3(kMergeCtas * most * CTAS), dim3(kMergeThreads), 0, s, a, teams);
 }
 template <typename T, typename TO>
 cudaError_t launch(const ChunkArgs& a, const Plan& p, cudaStream_t s) {
-  return p.ctas == 2 ? launch<T, TO, 2>(a, p, s) : launch<T, TO, 1>(a, p, s);
+  if (a.batch > 32) return p.ctas == 2 ? launch<T, TO, 2, true>(a, p, s) : launch<T, TO, 1, true>(a, p, s);
+  return p.ctas == 2 ? launch<T, TO, 2, false>(a, p, s) : launch<T, TO, 1, false>(a, p, s);
 }
 template <typename T>
 cudaError_t launch(const ChunkArgs& a, const Plan& p, int out_dtype, cudaStream_t s) {
@@ -1210,6 +1282,7 @@ tq_status tq_kv16_continue(const tq_config* cfg, const void* q, long long q_stri
   a.may_split = p.may_split;
   a.part_rows = p.part_rows;
   a.qscale = b8_qscale(scale);
+  a.search_ns = kWaitNs + kStepNs * (batch / 32 + p.units / cfg->num_kv_heads / 512);
   a.split_units = static_cast<int4*>(workspace);
   a.rec_o = reinterpret_cast<float*>(a.split_units + kCtas);
   a.rec_lse = a.rec_o + static_cast<size_t>(2 * kCtas / p.ctas) * p.part_rows * kKvD;
