@@ -1215,3 +1215,25 @@ def test_continue_a_long_prompt_among_thousands(tq, batch, q_len, group):
     for row, seen in ([(b, int(lens[b])) for b in (0, 31, 32, 1000, at - 1)] + [(first + i, i + 1) for i in (0, 63, q_len // 2 + 5, q_len - 1)] +
                       [(int(starts[b]), int(lens[b])) for b in (at + 1, batch - 1)]):
         check_row(c, q[row].cpu(), k[:seen], v[:seen], out[row].double().cpu().numpy(), "bf16", SCALE, True, (row, seen))
+
+
+def test_continue_zeros_for_many_queries_past_max_q_len(tq):
+    """However many queries are not served: their zeros hold nobody up."""
+    rows, group = 600000, 8
+    c = Case(tq, "bf16", 64, group, 1, [3000], seed=7).fill([3000])
+    c.table = np.repeat(c.table, 3, 0)
+    starts, lens = np.array([0, 90, rows - 100, rows], dtype=np.int32), np.array([3000, 2500, 100], dtype=np.int32)
+    q = torch.randn((rows, group, 128), dtype=torch.bfloat16, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    cache, table, _ = c.gpu()
+    out = torch.full_like(q, 123.0)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(tq.tq_kv16_continue_workspace_size(c.cfg, 3, rows, 200, 3000), dtype=torch.uint8, device="cuda")
+    tq.tq_kv16_continue(c.cfg, q, torch.from_numpy(starts).cuda(), 200, cache, table, torch.from_numpy(lens).cuda(), 3000, out, ws, dev_status=status)
+    torch.cuda.synchronize()
+    assert int(status) == tq.TQ_DEV_SEQ_TOO_LONG
+    assert not out[90 + 200:rows - 100].any()
+    k, v = c.kv(0, 3000)
+    # row and positions seen: the middle chunk's queries lie past position 0 from its last 2500 on, so those served see none
+    for row, seen in ((0, 2911), (89, 3000), (rows - 100, 1), (rows - 1, 100)):
+        check_row(c, q[row].cpu(), k[:seen], v[:seen], out[row].double().cpu().numpy(), "bf16", SCALE, True, (row, seen))
+    assert not out[90:290].any()

@@ -40,8 +40,8 @@
 // Warps: 0-3 and 4-7 the softmax of tile 0 and 1; 8 and 9 issue the products of tile 0
 // and 1 (of both CTAs of a pair, in its first), in turn, so that the two tiles stay half
 // a round apart; 10 finds the work and loads keys and values; 11, in the second CTA of
-// a pair, tells the first what has come; 12-15 load queries. Keys and values come by
-// bulk copies: they lie in the cache as the tensor cores read them (128-byte swizzle; K
+// a pair, tells the first what has come, and in the first writes the zeros of queries past
+// max_q_len; 12-15 load queries. Keys and values come by bulk copies: they lie in the cache as the tensor cores read them (128-byte swizzle; K
 // a K-major operand, V an MN-major one). Every wait is bounded; one that runs out sets
 // TQ_DEV_TIMEOUT and ends the CTA, after its products and copies in flight.
 //
@@ -185,7 +185,6 @@ struct Work {
   int tile0, tiles;    // steps: [tile0, tile0 + tiles); none: zeros are written
   int halves;          // of them, those that anybody sees
   int loads;           // that bring them: CTAS halves each
-  int zero0, zeros;    // queries that nobody serves
   int more, keep;      // this team's steps of the unit before tile0 are there already, where these come to be; the queries stay for the next part
   unsigned load0;      // loads of the CTA before
 };
@@ -485,17 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
       if (w.seq < 0) break;
       before = w.tiles;
-      auto zero_rows = [&](int q0, int count) {   // `count` queries from q0 on, this KV head's part
-        const long long all = static_cast<long long>(count) * a.group * (kKvD / 4);
-        for (long long i = threadIdx.x; i < all; i += 256) {
-          const long long x = i / (kKvD / 4);
-          write4<TO>(static_cast<TO*>(a.out) + ((q0 + x / a.group) * a.n_q + w.h * a.group + x % a.group) * kKvD + 4 * (i % (kKvD / 4)),
-                     make_float4(0.f, 0.f, 0.f, 0.f));
+      if (w.tiles == 0) {   // nothing is seen: zeros
+        if (rank == 0) {
+          for (int i = threadIdx.x; i < w.rows * (kKvD / 4); i += 256) {
+            const int row = i / (kKvD / 4), q = static_cast<int>(row * by_group >> 16);
+            write4<TO>(static_cast<TO*>(a.out) + (static_cast<long long>(w.q0 + q) * a.n_q + w.h * a.group + row - q * a.group) * kKvD + 4 * (i % (kKvD / 4)),
+                       make_float4(0.f, 0.f, 0.f, 0.f));
+          }
         }
-      };
-      if (w.zeros && rank == 0) zero_rows(w.zero0, w.zeros);
-      if (w.tiles == 0) {
-        if (rank == 0) zero_rows(w.q0, w.rows / a.group);
         continue;
       }
       if (t * CTAS * 128 >= w.rows) continue;
@@ -812,7 +808,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
     }
     __syncwarp();
   } else if (warp < 10 || warp == 11) {
-    // ---- the second CTA of a pair tells the first what it has loaded (and the other warps here only pass)
+    // ---- the second CTA of a pair tells the first what it has loaded (and the other warps here only pass).
+    // In the first one warp 11 writes zeros where queries are past max_q_len, row by row with the other
+    // teams' and after all else: nobody waits for these, however many they are. (100000 of 8 heads 0.15 ms; by
+    // the softmax warps of one CTA 13.6, and the waits for these give up after 20.)
+    auto unserved = [&](int i) {   // of sequence i + lane: its chunk, if it has such
+      const int b = i + lane;
+      const bool in = b < a.batch;
+      return chunk_of(a, ldg_or(a.query_start + b, in, 0), ldg_or(a.query_start + b + 1, in, 0), 0);
+    };
+    unsigned any = 0;
+    for (int i = 0; i < a.batch && warp == 11 && rank == 0 && a.max_q_len < a.total_q; i += 32) any |= __ballot_sync(0xffffffffu, unserved(i).n > a.max_q_len);
     Turn<kStages> loaded;
     int before = 0;
     bool ok = true;
@@ -826,6 +832,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       for (int i = 0; i < loads && warp == 11 && rank == 1; ++i, loaded.next()) {
         if (!(ok = warp_wait(kFull0 + loaded.stage, loaded.round))) break;
         if (lane == 0) arrive_first(kFull0 + loaded.stage);
+      }
+    }
+    for (int i = 0; i < a.batch && any; i += 32) {
+      const Chunk c = unserved(i);
+      for (unsigned m = __ballot_sync(0xffffffffu, c.n > a.max_q_len); m; m &= m - 1) {
+        const int q0 = __shfl_sync(0xffffffffu, c.q0, __ffs(m) - 1), n = __shfl_sync(0xffffffffu, c.n, __ffs(m) - 1);
+        for (int q = a.max_q_len + team; q < n; q += teams) {
+          uint4* row = reinterpret_cast<uint4*>(static_cast<TO*>(a.out) + static_cast<long long>(q0 + q) * a.n_q * kKvD);
+          for (int k = lane; k < a.n_q * kKvD * static_cast<int>(sizeof(TO)) / 16; k += 32) row[k] = make_uint4(0u, 0u, 0u, 0u);
+        }
       }
     }
   } else if (warp == 10) {
@@ -887,8 +903,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
         w.halves = min((w.limit + 63) / 64 - 2 * w.tile0, 2 * w.tiles);
         w.loads = w.tiles ? (w.halves + CTAS - 1) / CTAS : 0;
         w.slot = from > 0 ? 2 * team : (to < u.steps ? 2 * team + 1 : -1);
-        w.zero0 = ch.q0 + served;
-        w.zeros = u.j == 0 && done == 0 ? ch.n - served : 0;   // queries past max_q_len
         w.load0 = loads;
         if (u.j == 0 && done == 0 && u.h == 0 && speaks && (ch.n > a.max_q_len || ch.len > a.limit))
           b8_flag(a.status, TQ_DEV_SEQ_TOO_LONG);
