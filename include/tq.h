@@ -692,8 +692,8 @@ tq_status tq_kv16_decode(const tq_config* cfg, const void* q, long long q_stride
                          void* out, int out_dtype, void* workspace, size_t workspace_bytes,
                          unsigned int* dev_status, tq_stream_t stream);
 
-/* Host. Bytes of workspace of tq_kv16_continue for the same sizes. 0 on bad
- * input. */
+/* Host. Bytes of workspace of tq_kv16_continue for these sizes or smaller ones.
+ * 0 on bad input. */
 size_t tq_kv16_continue_workspace_size(const tq_config* cfg, int batch, int total_q, int max_q_len,
                                        int max_seq_len);
 

@@ -222,3 +222,16 @@ def test_binding_refusals(tq):
         tq.tq_kv16_decode(cfg, q[:1], cache, table, lens, 64, out[:1], ws)
     with pytest.raises(ValueError, match="query_start"):
         tq.tq_kv16_continue(cfg, q, starts.long(), 1, cache, table, lens, 64, out, ws)
+
+
+@pytest.mark.parametrize("group", [1, 3, 4, 5, 8])
+def test_continue_workspace_of_the_largest_step_serves_smaller_ones(tq, group):
+    """A server keeps one workspace, of its largest step, whatever shape a smaller step's units then have."""
+    cfg = tq.make_config("kv_bf16", 2 * group, 2)
+    size = lambda *x: tq.tq_kv16_continue_workspace_size(cfg, *x)      # noqa: E731
+    steps = [(b, t, m, s) for b in (1, 7, 32, 300) for t in (1, 30, 64, 100, 300, 1000, 9000) for m in (1, 31, 60, 64, 90, 100, 130, 2000)
+             for s in (0, 1, 1024, 1025, 50000)]
+    for big in [(32, 9000, m, 50000) for m in (31, 64, 90, 100, 130, 2000)] + [(300, 1000, 60, 1025), (7, 100, 100, 1024)]:
+        for small in steps:
+            if all(x <= y for x, y in zip(small, big)):
+                assert size(*small) <= size(*big), (small, big)

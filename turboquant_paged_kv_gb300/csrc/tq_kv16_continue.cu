@@ -1186,7 +1186,8 @@ Plan plan_for(const tq_config* cfg, int batch, int total_q, int max_q_len, int m
   p.units = tiles * cfg->num_kv_heads;
   p.may_split = p.units > 0 && max_seq_len > kNoSplit * kCols;
   p.part_rows = longest < per ? longest * group : per * group;
-  const size_t records = static_cast<size_t>(2 * kCtas / p.ctas) * p.part_rows;
+  // as many rows as either shape of units has, so that a workspace serves all smaller calls too
+  const size_t records = static_cast<size_t>(2 * kCtas) * (longest * static_cast<long long>(group) < kRows ? longest * group : kRows);
   p.workspace = p.may_split ? (kCtas * sizeof(int4) + records * (kKvD + 1) * sizeof(float) + 15) / 16 * 16 : 16;
   return p;
 }
