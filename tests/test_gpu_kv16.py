@@ -1237,3 +1237,54 @@ def test_continue_zeros_for_many_queries_past_max_q_len(tq):
     for row, seen in ((0, 2911), (89, 3000), (rows - 100, 1), (rows - 1, 100)):
         check_row(c, q[row].cpu(), k[:seen], v[:seen], out[row].double().cpu().numpy(), "bf16", SCALE, True, (row, seen))
     assert not out[90:290].any()
+
+
+# ---------------------------------------------------------------- prompts: warps of several rounds
+
+
+def rounds_of(rows, heads):
+    """Rounds of 8 head rows that a warp of the append takes, and warps a token."""
+    most = -(-heads // 8)
+    rounds = min(max(rows * most // (152 * 48), 1), most)
+    return rounds, -(-most // rounds)
+
+
+PROMPTS = [
+    # n_kv, group, q_lens, dtype, block, rot, style: the last warp's last rounds lie past the heads, or just end with them
+    (8, 4, [1200, 0, 3697, 3], "bf16", 16, 128, "halves"), (2, 8, [5000], "fp16", 64, 64, "pairs"), (5, 5, [1500, 1, 2999], "bf16", 128, 48, "halves"),
+    (1, 7, [7000, 7700], "fp16", 32, 112, "pairs"), (8, 1, [4097, 3500], "bf16", 32, 0, "halves"), (6, 3, [9000], "fp16", 16, 16, "halves")]
+
+
+@pytest.mark.parametrize("n_kv,group,q_lens,dtype,block,rot,style", PROMPTS)
+def test_append_of_whole_prompts(tq, n_kv, group, q_lens, dtype, block, rot, style):
+    rows, n_q = sum(q_lens), n_kv * group
+    assert rounds_of(rows, n_q + 2 * n_kv)[0] > 1
+    hist = [7 * i for i in range(len(q_lens))]
+    lens = np.array(hist) + np.array(q_lens)
+    c = Case(tq, dtype, block, n_q, n_kv, lens, seed=rows)
+    starts = starts_of(q_lens)
+    key, value, q = c.draw(rows, n_kv, 3.0, outlier=True), c.draw(rows, n_kv), c.draw(rows, n_q)
+    angles = angle_table(int(max(lens)), rot) if rot else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache, q_out = run_append(c, key, value, starts, lens, angles, style, q, status=status)
+    assert int(status) == 0
+    check_append(c, c.cache, cache, key, value, starts, lens, angles, style)
+    check_queries(c, q, q_out, starts, lens, angles, style)
+
+
+@pytest.mark.parametrize("n_kv,group,q_lens,dtype,block,rot,style", PROMPTS[:3])
+def test_append_of_whole_prompts_in_place(tq, n_kv, group, q_lens, dtype, block, rot, style):
+    """In a fused projection, with rows behind the last sequence."""
+    rows, n_q, extra = sum(q_lens), n_kv * group, 9
+    lens = np.array(q_lens)
+    c = Case(tq, dtype, block, n_q, n_kv, lens, seed=rows + 1)
+    starts = starts_of(q_lens)
+    fused = c.draw(rows + extra, n_q + 2 * n_kv)
+    dev = fused.cuda()
+    angles = angle_table(int(max(lens)), rot)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache, _ = run_append(c, dev[:, n_q:n_q + n_kv], dev[:, n_q + n_kv:], starts, lens, angles, style, dev[:, :n_q], dev[:, :n_q], status=status)
+    assert int(status) == 0
+    check_append(c, c.cache, cache, fused[:, n_q:n_q + n_kv], fused[:, n_q + n_kv:], starts, lens, angles, style)
+    check_queries(c, fused[:, :n_q], dev[:, :n_q], starts, lens, angles, style)
+    assert torch.equal(dev[:, n_q:].cpu(), fused[:, n_q:]) and torch.equal(dev[rows:].cpu(), fused[rows:])
