@@ -1288,3 +1288,98 @@ def test_append_of_whole_prompts_in_place(tq, n_kv, group, q_lens, dtype, block,
     check_append(c, c.cache, cache, fused[:, n_q:n_q + n_kv], fused[:, n_q + n_kv:], starts, lens, angles, style)
     check_queries(c, fused[:, :n_q], dev[:, :n_q], starts, lens, angles, style)
     assert torch.equal(dev[:, n_q:].cpu(), fused[:, n_q:]) and torch.equal(dev[rows:].cpu(), fused[rows:])
+
+
+# ---------------------------------------------------------------- chunks with output of the cache's type
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_len,length", [(4, 200), (140, 200), (140, 1500)])
+def test_continue_device_errors_with_16_bits(tq, mode, dtype, q_len, length):
+    c = Case(tq, dtype, 16, 4, 1, [length], seed=41).fill([length])
+    c.table[0, 3], c.table[0, 9], c.table[0, length // 16] = -1, 2 ** 31 - 1, -2
+    q = c.draw(q_len, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, [0, q_len], [length], dtype, status=status)
+    assert int(status) == tq.TQ_DEV_BLOCK_OUT_OF_RANGE
+    check_continue(c, q, got, [0, q_len], [length], dtype, rows=10)
+    c.table[:] = 2 ** 31 - 1                       # nothing left
+    assert not run_continue(c, q, [0, q_len], [length], dtype, status=status).any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("block", [16, 64])
+@pytest.mark.parametrize("hist,q_len,max_q", [(10, 20, 5), (0, 140, 70), (900, 30, 7), (2000, 90, 85)])
+def test_rows_that_were_not_stored_with_16_bits(tq, mode, dtype, block, hist, q_len, max_q):
+    n, kept = hist + q_len, hist + max_q
+    c = Case(tq, dtype, block, 4, 1, [n], seed=94)
+    c.cache[:] = 0xff
+    c.fill([kept])
+    q = c.draw(q_len, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, [0, q_len], [n], dtype, max_q=max_q, status=status)
+    assert int(status) == tq.TQ_DEV_SEQ_TOO_LONG
+    assert not got[max_q:].any()
+    check_continue(c, q[:max_q], got[:max_q], [0, max_q], [kept], dtype, rows=12)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("hist", [0, 800, 1900])
+def test_continue_later_positions_change_nothing_with_16_bits(tq, mode, dtype, hist):
+    q_len = 60
+    n, out = hist + q_len, []
+    for gain in (1.0, 100.0, 2.0 ** -20, 60000.0):
+        c = Case(tq, dtype, 16, 4, 1, [n], seed=93)
+        k, v, q = c.draw(n, 1).float(), c.draw(n, 1).float(), c.draw(q_len, 4)
+        k[hist + 32:] *= gain
+        v[hist + 32:] *= gain
+        top = float(torch.finfo(DT[dtype]).max)
+        c.put(0, k.clamp(-top, top).to(DT[dtype]), v.clamp(-top, top).to(DT[dtype]))
+        c.lens = np.array([n], dtype=np.int32)
+        out.append(run_continue(c, q, [0, q_len], [n], dtype)[:32])
+    for x in out[1:]:
+        assert np.array_equal(out[0], x)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_len,length,cut", [(140, 200, 150), (5, 900, 897), (20, 900, 500), (200, 2300, 2200)])
+def test_continue_cuts_long_sequences_with_16_bits(tq, mode, dtype, q_len, length, cut):
+    c = Case(tq, dtype, 32, 4, 1, [length], seed=49).fill([length])
+    q = c.draw(q_len, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, [0, q_len], [length], dtype, status=status, max_len=cut)
+    assert int(status) == tq.TQ_DEV_SEQ_TOO_LONG
+    k, v = c.kv(0)
+    for i in range(0, q_len, max(q_len // 20, 1)):
+        seen = min(length - q_len + i + 1, cut)
+        check_row(c, q[i], k[:seen], v[:seen], got[i], dtype, SCALE, True, (i, seen))
+
+
+@pytest.mark.parametrize("dtype,batch", [("bf16", 90), ("fp16", 500)])
+def test_continue_many_chunks_with_16_bits(tq, mode, dtype, batch):
+    c = Case(tq, dtype, 32, 8, 2, [1300], seed=batch).fill([1300])
+    c.table = np.repeat(c.table, batch, 0)
+    q_lens = c.rng.integers(0, 4, batch)
+    lens = np.maximum(c.rng.integers(1, 1301, batch), q_lens)
+    c.lens = lens.astype(np.int32)
+    starts = starts_of(q_lens)
+    q = c.draw(int(starts[-1]), 8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, starts, lens, dtype, status=status)
+    assert int(status) == 0
+    check_continue(c, q, got, starts, lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_len", [5, 150])
+def test_continue_rows_without_positions_with_16_bits(tq, mode, dtype, q_len):
+    c = Case(tq, dtype, 16, 4, 1, [q_len, 200], seed=40).fill([q_len - 3, 200])
+    starts = np.array([0, q_len, q_len + 4], dtype=np.int32)
+    q = c.draw(int(starts[-1]) + 9, 4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = run_continue(c, q, starts, [q_len - 3, 200], dtype, status=status)
+    assert int(status) == 0
+    assert not got[:3].any() and np.all(got[starts[-1]:] == 123.0)
+    check_continue(c, q, got, starts, [q_len - 3, 200], dtype, rows=10)
+    got = run_continue(c, q, starts, [0, 0], dtype, status=status)                  # nobody sees anything
+    assert int(status) == 0 and not got[:starts[-1]].any()
