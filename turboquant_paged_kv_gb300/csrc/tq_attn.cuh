@@ -19,14 +19,14 @@
 namespace tq {
 namespace {
 
-constexpr uint64_t kWaitNs = 20000000;  // x / y; most lines of work are short enough for 32 bits.
+constexpr uint64_t kWaitNs = 20000000;  // every wait gives up after 20 ms without progress
+constexpr uint32_t kSuspendNs = 1000;     // try_wait suspend-time hint
+
+// x / y; most lines of work are short enough for 32 bits.
 __device__ __forceinline__ long long divide(long long x, long long y) {
   if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
   return x / y;
 }
-
-// every wait gives up after 20 ms without progress
-constexpr uint32_t kSuspendNs = 1000;     // try_wait suspend-time hint
 
 enum KeyMode { kMse4 = 4, kMse3 = 3, kFp8 = 8 };
 
