@@ -1383,3 +1383,53 @@ def test_continue_rows_without_positions_with_16_bits(tq, mode, dtype, q_len):
     check_continue(c, q, got, starts, [q_len - 3, 200], dtype, rows=10)
     got = run_continue(c, q, starts, [0, 0], dtype, status=status)                  # nobody sees anything
     assert int(status) == 0 and not got[:starts[-1]].any()
+
+
+@pytest.mark.parametrize("total,shape", [(700, "single"), (5200, "pair")])
+def test_continue_of_many_sequences_in_graphs_and_on_streams(tq, total, shape):
+    """One captured call on 70 sequences, replayed for other starts, lengths and queries in padded tensors, while another
+    stream makes the same calls by itself with a workspace of its own."""
+    batch, most, group, n_kv = 70, 1500, 4, 2
+    assert (total * group > 256 * batch) == (shape == "pair") and total * n_kv > FEW
+    c = Case(tq, "bf16", 16, n_kv * group, n_kv, [most], seed=total).fill([most])
+    c.table = np.repeat(c.table, batch, 0)
+    cache, table, _ = c.gpu()
+    steps = []
+    for k, chunks in enumerate(([300, 150], [], [690 if shape == "single" else 1400], [129] * 3)):
+        q_lens, lens = mixed_lengths(c.rng, batch, chunks, most)
+        if sum(q_lens) > total:
+            q_lens[q_lens == 1] = 0
+        assert sum(q_lens) <= total
+        steps.append((starts_of(q_lens), lens.astype(np.int32), c.draw(total, n_kv * group)))
+    up = lambda x: torch.from_numpy(x).cuda()      # noqa: E731
+    need = tq.tq_kv16_continue_workspace_size(c.cfg, batch, total, total, most)
+    call = lambda q, s, n, out, ws: tq.tq_kv16_continue(c.cfg, q, s, total, cache, table, n, most, out, ws)      # noqa: E731
+    s, n, q = up(steps[0][0]), up(steps[0][1]), steps[0][2].cuda()
+    out = torch.full_like(q, 123.0)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(main):
+        call(q, s, n, out, ws)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            call(q, s, n, out, ws)
+    mine = [(up(a), up(b), x.cuda()) for a, b, x in steps]
+    other = [torch.full_like(q, 123.0) for _ in steps]
+    ws2 = torch.empty(need, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for (a, b, x), o in zip(mine, other):
+        with torch.cuda.stream(main):
+            s.copy_(a)
+            n.copy_(b)
+            q.copy_(x)
+            out.fill_(123.0)
+            graph.replay()
+        with torch.cuda.stream(side):
+            call(x, a, b, o, ws2)
+        torch.cuda.synchronize()
+        assert torch.equal(out, o)
+        a, b = a.cpu().numpy(), b.cpu().numpy()
+        c.lens = b
+        assert torch.all(out[int(a[-1]):] == 123.0)
+        check_continue(c, x.cpu(), out.double().cpu().numpy(), a, b, "bf16", rows=6)

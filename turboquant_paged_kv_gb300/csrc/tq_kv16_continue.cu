@@ -41,9 +41,10 @@
 // and 1 (of both CTAs of a pair, in its first), in turn, so that the two tiles stay half
 // a round apart; 10 finds the work and loads keys and values; 11, in the second CTA of
 // a pair, tells the first what has come, and in the first writes the zeros of queries past
-// max_q_len; 12-15 load queries. Keys and values come by bulk copies: they lie in the cache as the tensor cores read them (128-byte swizzle; K
-// a K-major operand, V an MN-major one). Every wait is bounded; one that runs out sets
-// TQ_DEV_TIMEOUT and ends the CTA, after its products and copies in flight.
+// max_q_len; 12-15 load queries. Keys and values come by bulk copies: they lie in the cache
+// as the tensor cores read them (128-byte swizzle; K a K-major operand, V an MN-major one).
+// Every wait is bounded; one that runs out sets TQ_DEV_TIMEOUT and ends the CTA, after its
+// products and copies in flight.
 //
 // Bound: tensor cores by its operations. 4 chunks of 2001-2048 queries over 0-6144, 32
 // query heads, fp16: 540 us, 1570 TFLOP/s, 0.83 of a measured bf16 GEMM (592 us, 1432,
@@ -484,14 +485,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv16_chunk_kernel(const ChunkArgs
       if (lane == 0) mbar_arrive(bar(kWEmpty0 + (part & 1)));
       if (w.seq < 0) break;
       before = w.tiles;
-      if (w.tiles == 0) {   // nothing is seen: zeros
-        if (rank == 0) {
-          for (int i = threadIdx.x; i < w.rows * (kKvD / 4); i += 256) {
-            const int row = i / (kKvD / 4), q = static_cast<int>(row * by_group >> 16);
-            write4<TO>(static_cast<TO*>(a.out) + (static_cast<long long>(w.q0 + q) * a.n_q + w.h * a.group + row - q * a.group) * kKvD + 4 * (i % (kKvD / 4)),
-                       make_float4(0.f, 0.f, 0.f, 0.f));
-          }
+      auto zero_rows = [&](int q0, int count) {   // `count` queries from q0 on, this KV head's part
+        const long long all = static_cast<long long>(count) * a.group * (kKvD / 4);
+        for (long long i = threadIdx.x; i < all; i += 256) {
+          const long long x = i / (kKvD / 4);
+          write4<TO>(static_cast<TO*>(a.out) + ((q0 + x / a.group) * a.n_q + w.h * a.group + x % a.group) * kKvD + 4 * (i % (kKvD / 4)),
+                     make_float4(0.f, 0.f, 0.f, 0.f));
         }
+      };
+      if (w.tiles == 0) {
+        if (rank == 0) zero_rows(w.q0, w.rows / a.group);
         continue;
       }
       if (t * CTAS * 128 >= w.rows) continue;
