@@ -1433,3 +1433,25 @@ def test_continue_of_many_sequences_in_graphs_and_on_streams(tq, total, shape):
         c.lens = b
         assert torch.all(out[int(a[-1]):] == 123.0)
         check_continue(c, x.cpu(), out.double().cpu().numpy(), a, b, "bf16", rows=6)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("line", [False, 4, 2, True])
+def test_decode_scores_of_a_hundred_million(tq, dtype, line):
+    """Scores of 2^27 + 16 and, in the second half, 2^27 + 32 log2 units, which fp32 holds exactly, 16 apart: the former
+    weigh 2^-16 of the latter. A record's log-sum-exp, within 8 of its maximum, is rounded to that maximum. The values are
+    -1 and 3, the result 3 within 4 2^-16 and the roundings of weights and sums (2^-12 in all, and half of that again)."""
+    n, batch = 2048, 40
+    c = Case(tq, dtype, 16, 4, 1, [n], seed=3)
+    k, v = torch.zeros((n, 1, 128)), torch.full((n, 1, 128), -1.0)
+    k[:, :, 0] = 2.0 ** 13
+    k[:n // 2, :, 1], k[n // 2:, :, 1], v[n // 2:] = 1.0, 2.0, 3.0
+    c.put(0, k.to(DT[dtype]), v.to(DT[dtype]))
+    scale = float(np.float32(np.log(2.0)))
+    assert np.float32(scale) * np.float32(1.4426950408889634) == 1.0
+    for rows in (1, batch):
+        c.table, c.lens = np.repeat(c.table[:1], rows, 0), np.full(rows, n, dtype=np.int32)
+        q = torch.zeros((rows, 4, 128))
+        q[:, :, 0], q[:, :, 1] = 2.0 ** 14, 16.0
+        got = run_decode(c, q.to(DT[dtype]), scale=scale, line=line)
+        assert np.all(np.abs(got - 3.0) <= 1.5 * 2.0 ** -12), (rows, float(np.abs(got - 3.0).max()))

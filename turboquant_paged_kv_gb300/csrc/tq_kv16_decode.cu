@@ -142,7 +142,8 @@ struct Heads {
       if (g + 8 >= left) x10 = x11 = -INFINITY;
     }
     const float t0 = fmaxf(x00, x10), t1 = fmaxf(x01, x11);
-    if (__any_sync(0xffffffffu, t0 > m0 + kStep || t1 > m1 + kStep)) {
+    // (the difference and not the sum, which rounds by as much as kStep where scores are 2^27: a weight of 2^16 fits in no fp16)
+    if (__any_sync(0xffffffffu, t0 - m0 > kStep || t1 - m1 > kStep)) {
       float u0 = fmaxf(m0, t0), u1 = fmaxf(m1, t1);
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
