@@ -623,7 +623,9 @@ tq_status tq_b8_continue(const tq_config* cfg, const void* q, long long q_stride
  * The cache holds finite numbers: tq_kv16_append sees to it for what it writes,
  * and what stands behind a sequence's end is not used, whatever it is. (An
  * infinity or a NaN that is put there in another way, among the values of a
- * position that a chunk sees, may reach all queries of that chunk.) */
+ * position that a chunk sees, may reach all queries of that chunk.) Attention
+ * sums values with weights of up to 60000 before it divides by the weights' sum,
+ * in fp32: with bf16 values of magnitudes from 1e30 on results may be infinite. */
 typedef struct {
   int is_bf16;
   int tile_tokens;         /* 16 */

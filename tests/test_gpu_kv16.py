@@ -1455,3 +1455,18 @@ def test_decode_scores_of_a_hundred_million(tq, dtype, line):
         q[:, :, 0], q[:, :, 1] = 2.0 ** 14, 16.0
         got = run_decode(c, q.to(DT[dtype]), scale=scale, line=line)
         assert np.all(np.abs(got - 3.0) <= 1.5 * 2.0 ** -12), (rows, float(np.abs(got - 3.0).max()))
+
+
+@pytest.mark.parametrize("top", [1e29, 6e4])
+@pytest.mark.parametrize("q_len", [3, 150])
+def test_large_values(tq, mode, top, q_len):
+    """bf16 values of up to 1e29 over 1500 positions, weighed with up to 60000 before the division by the weights' sum."""
+    n = 1500
+    c = Case(tq, "bf16", 16, 4, 1, [n], seed=8)
+    v = c.draw(n, 1).float()
+    c.put(0, c.draw(n, 1, 2.0, outlier=True), (v / v.abs().max() * top).to(torch.bfloat16))
+    c.lens = np.array([n], dtype=np.int32)
+    q = c.draw(q_len, 4)
+    for out in ("f32", "bf16"):
+        check_continue(c, q, run_continue(c, q, [0, q_len], [n], out), [0, q_len], [n], out, rows=10)
+        check_decode(c, q[:1], run_decode(c, q[:1], out_dtype=out, line={"rows": False, "single": True, "pair": True}.get(mode, mode)), out)
