@@ -21,11 +21,11 @@
 // its rows in different banks. Softmax in log2 units, the running maximum moving
 // only when a score passes it by 2^8 (one warp vote a tile).
 //
-// Bound: memory, the cache being read once. 64 x 512-16384, 8 KV heads: 361 us, 6.63 TB/s
-// of 2.39 GB (0.98 of a measured copy); 4 x 131072, 4 KV heads: 336, 6.43. (32 x 4096 by the
+// Bound: memory, the cache being read once. 64 x 512-16384, 8 KV heads: 357-369 us, 6.5-6.7 TB/s
+// of 2.39 GB (0.96-0.99 of a measured copy); 4 x 131072, 4 KV heads: 336, 6.4. (32 x 4096 by the
 // line: 90 us, 5.96 TB/s, 77 % of DRAM's cycles, tensor cores busy for 9 %, of which 4 to 5
 // us are the start, lengths, table and first tiles one after another, and 3 the merge; in
-// one launch 81, 6.6 TB/s.) 1 x 301 5.7, a chain of those loads, the tiles and the
+// one launch 82, 6.5 TB/s.) 1 x 301 5.7, a chain of those loads, the tiles and the
 // cluster's merge.
 #include <climits>
 
